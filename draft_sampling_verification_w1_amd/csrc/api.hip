@@ -205,6 +205,43 @@ BlockCands cands_at(void* ws, const CandLayout& L) {
   return c;
 }
 
+int check_ws_bytes(size_t need, void* ws, size_t ws_bytes) {
+  if (!ws) return fail(DSPARK_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", need);
+  if ((uintptr_t)ws % kAlign) return fail(DSPARK_ERR_WORKSPACE, "workspace not %zu-byte aligned", kAlign);
+  if (ws_bytes < need)
+    return fail(DSPARK_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", ws_bytes, need);
+  return DSPARK_OK;
+}
+
+// ---- log probabilities of given tokens ---------------------------------------
+int check_logprobs_shape(int N, int V, int n_top) {
+  if (N < 1 || N > (1 << 24)) return fail(DSPARK_ERR_SHAPE, "N=%d outside [1, 2^24]", N);
+  if (V < 1 || V >= (1 << 26)) return fail(DSPARK_ERR_SHAPE, "V=%d outside [1, 2^26)", V);
+  if (n_top < 0 || n_top > kMaxTopLogprobs)
+    return fail(DSPARK_ERR_SHAPE, "n_top=%d outside [0, %d]", n_top, kMaxTopLogprobs);
+  return DSPARK_OK;
+}
+
+// Split records; none (0 bytes) where a workgroup takes a whole row.
+struct LogprobLayout {
+  int nsplit, chunk;
+  size_t m, st, v, i, bytes;
+};
+
+LogprobLayout logprob_layout(int N, int V, int n_top) {
+  LogprobLayout L = {};
+  L.nsplit = logprob_splits(N, V, &L.chunk);
+  if (L.nsplit == 1) return L;
+  const size_t n = (size_t)N * L.nsplit;
+  Carver c;
+  L.m = c.take(n * sizeof(float));
+  L.st = c.take(n * 2 * sizeof(double));
+  L.v = c.take(n * n_top * sizeof(float));
+  L.i = c.take(n * n_top * sizeof(int32_t));
+  L.bytes = c.off;
+  return L;
+}
+
 // Packed tiles, then one float per tile (max |W2| over the tile).
 size_t packed_bytes(const dspark_problem* p) {
   const int ntiles = (p->V + kTile - 1) / kTile;
@@ -760,6 +797,63 @@ __attribute__((visibility("default"))) int dspark_sts_fit(int32_t N, int32_t gam
   hipError_t e = launch_sts_fit(N, gamma, s, y, G, grid, bins, temps, ece_units, ece1_units, a, ws,
                                 (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "sts_fit");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_emitted_tokens(
+    int32_t R, int32_t gamma, const int32_t* tokens, const int32_t* n_accept,
+    const int32_t* out_token, int32_t* ids, void* stream) {
+  if (R < 1 || R > 65536 || gamma < 1 || gamma > 64)
+    return fail(DSPARK_ERR_SHAPE, "R=%d, gamma=%d outside [1, 65536] x [1, 64]", R, gamma);
+  if (!tokens || !n_accept || !out_token || !ids)
+    return fail(DSPARK_ERR_ARG, "emitted_tokens: tensor pointers must be non-NULL");
+  hipError_t e = launch_emitted(R, gamma, tokens, n_accept, out_token, ids, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "emitted_tokens");
+  return ok();
+}
+
+__attribute__((visibility("default"))) size_t dspark_logprobs_workspace_bytes(int32_t N, int32_t V,
+                                                                             int32_t n_top) {
+  if (check_logprobs_shape(N, V, n_top) != DSPARK_OK) return 0;
+  return logprob_layout(N, V, n_top).bytes;
+}
+
+__attribute__((visibility("default"))) int dspark_token_logprobs(
+    int32_t dtype, int32_t N, int32_t V, int64_t ld, const void* logits, const int32_t* ids,
+    int32_t n_top, float* logprob, float* entropy, int32_t* top_ids, float* top_logprobs, void* ws,
+    size_t ws_bytes, void* stream) {
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16)
+    return fail(DSPARK_ERR_DTYPE, "dtype %d is not DSPARK_F32 or DSPARK_BF16", dtype);
+  if (int e = check_logprobs_shape(N, V, n_top)) return e;
+  if (ld < V) return fail(DSPARK_ERR_SHAPE, "row stride %lld is less than V=%d", (long long)ld, V);
+  if (!logits || !ids || !logprob || !entropy || (n_top > 0 && (!top_ids || !top_logprobs)))
+    return fail(DSPARK_ERR_ARG, "token_logprobs: tensor pointers must be non-NULL");
+  if ((uintptr_t)logits % (dtype == DSPARK_BF16 ? 2 : 4))
+    return fail(DSPARK_ERR_ARG, "token_logprobs: logits must be aligned to their element size");
+  const LogprobLayout L = logprob_layout(N, V, n_top);
+  if (L.bytes)
+    if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
+  LogprobArgs a = {};
+  a.N = N;
+  a.V = V;
+  a.ld = ld;
+  a.logits = logits;
+  a.ids = ids;
+  a.n_top = n_top;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.nsplit = L.nsplit;
+  a.chunk = L.chunk;
+  if (L.bytes) {
+    a.part_m = at<float>(ws, L.m);
+    a.part_st = at<double>(ws, L.st);
+    a.part_v = at<float>(ws, L.v);
+    a.part_i = at<int32_t>(ws, L.i);
+  }
+  hipError_t e = launch_logprobs(dtype == DSPARK_BF16, a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "token_logprobs");
   return ok();
 }
 

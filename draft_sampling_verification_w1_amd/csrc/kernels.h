@@ -269,4 +269,27 @@ hipError_t launch_acceptance_stats(int R, int gamma, const uint8_t* mask, const 
                                    int64_t* reached, int64_t* accepted, int64_t* sweep_verified,
                                    int64_t* sweep_accepted, hipStream_t stream);
 
+// ---- log probabilities of given tokens -------------------------------------
+constexpr int kMaxTopLogprobs = 64;
+struct LogprobArgs {
+  int N, V;
+  int64_t ld;            // entries from one row to the next
+  const void* logits;
+  const int32_t* ids;    // [N], outside [0, V): the row is skipped
+  int n_top;
+  float* logprob;        // [N]
+  float* entropy;        // [N]
+  int32_t* top_ids;      // [N, n_top]
+  float* top_logprobs;   // [N, n_top]
+  int nsplit, chunk;     // vocabulary splits per row, entries per split
+  float* part_m;         // [N * nsplit] largest entry of a split
+  double* part_st;       // [2 * N * nsplit] its two sums
+  float* part_v;         // [N * nsplit * n_top] its best entries, in order
+  int32_t* part_i;
+};
+int logprob_splits(int N, int V, int* chunk);
+hipError_t launch_logprobs(bool bf16, const LogprobArgs& a, hipStream_t stream);
+hipError_t launch_emitted(int R, int gamma, const int32_t* tokens, const int32_t* n_accept,
+                          const int32_t* out_token, int32_t* ids, hipStream_t stream);
+
 }  // namespace dspark

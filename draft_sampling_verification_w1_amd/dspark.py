@@ -22,6 +22,7 @@ SYMBOLS = ("dspark_w2_packed_bytes", "dspark_pack_w2", "dspark_workspace_bytes",
            "dspark_draft_step", "dspark_draft_step_noalloc", "dspark_verify", "dspark_confidence", "dspark_schedule",
            "dspark_schedule_capacity", "dspark_schedule_topk", "dspark_schedule_threshold",
            "dspark_acceptance_stats", "dspark_sts_workspace_bytes", "dspark_sts_fit",
+           "dspark_emitted_tokens", "dspark_logprobs_workspace_bytes", "dspark_token_logprobs",
            "dspark_check_inputs", "dspark_last_error", "dspark_timing_enable",
            "dspark_timing_report")
 
@@ -76,6 +77,12 @@ def lib() -> ctypes.CDLL:
         L.dspark_sts_fit.argtypes = [ctypes.c_int32, ctypes.c_int32, _vp, _vp, ctypes.c_int32, _vp,
                                      ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
         L.dspark_check_inputs.argtypes = [P, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+        i32, i64, size = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+        L.dspark_emitted_tokens.argtypes = [i32, i32, _vp, _vp, _vp, _vp, _vp]
+        L.dspark_logprobs_workspace_bytes.argtypes = [i32, i32, i32]
+        L.dspark_logprobs_workspace_bytes.restype = size
+        L.dspark_token_logprobs.argtypes = [i32, i32, i32, i64, _vp, _vp, i32, _vp, _vp, _vp, _vp,
+                                            _vp, size, _vp]
         L.dspark_last_error.restype = ctypes.c_char_p
         L.dspark_timing_enable.argtypes = [ctypes.c_int]
         L.dspark_timing_report.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
@@ -83,7 +90,7 @@ def lib() -> ctypes.CDLL:
                      "dspark_verify", "dspark_confidence",
                      "dspark_schedule", "dspark_schedule_capacity", "dspark_schedule_topk",
                      "dspark_schedule_threshold", "dspark_acceptance_stats", "dspark_sts_fit",
-                     "dspark_check_inputs",
+                     "dspark_check_inputs", "dspark_emitted_tokens", "dspark_token_logprobs",
                      "dspark_timing_enable", "dspark_timing_report"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -414,4 +421,70 @@ def sts_fit(s, y, grid, bins: int = 15):
     _check(lib().dspark_sts_fit(N, gamma, _ptr(s), _ptr(y), G, _ptr(grid), bins, _ptr(out["temps"]),
                                 _ptr(out["ece_units"]), _ptr(out["ece1_units"]), _ptr(out["a"]),
                                 _ptr(ws), need, _stream()))
+    return out
+
+
+def emitted_tokens(tokens, n_accept, out_token, out=None):
+    """The tokens a verified round emits (dspark_emitted_tokens): int32 [R,
+    gamma + 1], -1 behind each request's last one."""
+    R, gamma = tokens.shape
+    _need(tokens, "tokens", dtype=torch.int32)
+    _need(n_accept, "n_accept", dtype=torch.int32, shape=(R,))
+    _need(out_token, "out_token", dtype=torch.int32, shape=(R,))
+    if out is None:
+        out = torch.empty((R, gamma + 1), dtype=torch.int32, device=tokens.device)
+    _need(out, "out", dtype=torch.int32, shape=(R, gamma + 1))
+    with torch.cuda.device(tokens.device):
+        _check(lib().dspark_emitted_tokens(R, gamma, _ptr(tokens), _ptr(n_accept), _ptr(out_token),
+                                           _ptr(out), _stream()))
+    return out
+
+
+def logprobs_workspace(N: int, V: int, n_top: int, device=None) -> torch.Tensor:
+    """Workspace of token_logprobs for N rows of V logits (empty if none is needed)."""
+    return torch.empty(int(lib().dspark_logprobs_workspace_bytes(N, V, n_top)), dtype=torch.uint8,
+                       device=device or "cuda")
+
+
+def token_logprobs(logits, ids, n_top: int = 0, ws=None, out=None):
+    """Log probabilities of given tokens with entropy and the n_top most likely
+    tokens (dspark_token_logprobs).  logits [..., V] fp32 or bf16, contiguous, or
+    [N, V] with rows any distance >= V apart; ids [...] int32 (outside [0, V): the
+    row is skipped).  Returns a dict of logprob and entropy [...] fp32, top_ids
+    int32 and top_logprobs fp32 [..., n_top]; ``out`` may supply it preallocated."""
+    if not isinstance(logits, torch.Tensor) or logits.device.type != "cuda":
+        raise ValueError("logits must be a torch.Tensor on the GPU")
+    if logits.dtype not in _DTYPES:
+        raise ValueError(f"dtype must be float32 or bfloat16, got {logits.dtype}")
+    if logits.dim() < 2:
+        raise ValueError("logits must have shape [..., V]")
+    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
+    N = ids.numel()
+    if logits.dim() == 2 and logits.stride(1) == 1 and logits.stride(0) >= V:
+        ld = logits.stride(0)
+    else:
+        _need(logits, "logits")
+        ld = V
+    _need(ids, "ids", dtype=torch.int32, shape=lead)
+    dev = logits.device
+    if ids.device != dev:
+        raise ValueError("ids must be on the device of logits")
+    if out is None:
+        out = {"logprob": torch.empty(lead, dtype=torch.float32, device=dev),
+               "entropy": torch.empty(lead, dtype=torch.float32, device=dev),
+               "top_ids": torch.empty((*lead, n_top), dtype=torch.int32, device=dev),
+               "top_logprobs": torch.empty((*lead, n_top), dtype=torch.float32, device=dev)}
+    for name, dt, shape in (("logprob", torch.float32, lead), ("entropy", torch.float32, lead),
+                            ("top_ids", torch.int32, (*lead, n_top)),
+                            ("top_logprobs", torch.float32, (*lead, n_top))):
+        _need(out[name], name, dtype=dt, shape=shape)
+        if out[name].device != dev:
+            raise ValueError(f"{name} must be on the device of logits")
+    with torch.cuda.device(dev):
+        if ws is None:
+            ws = logprobs_workspace(N, V, n_top, dev)
+        _check(lib().dspark_token_logprobs(_DTYPES[logits.dtype], N, V, ld, _ptr(logits), _ptr(ids),
+                                           n_top, _ptr(out["logprob"]), _ptr(out["entropy"]),
+                                           _ptr(out["top_ids"]), _ptr(out["top_logprobs"]),
+                                           _ptr(ws), ws.numel(), _stream()))
     return out

@@ -260,6 +260,37 @@ int dspark_sts_fit(int32_t N, int32_t gamma, const double* s, const uint8_t* y, 
                    const double* grid, int32_t bins, float* temps, int64_t* ece_units,
                    int64_t* ece1_units, float* a, void* ws, size_t ws_bytes, void* stream);
 
+/* The tokens a verified round emits, in order.  [P1 요약]
+ * ids[r, k] = tokens[r, k] for k < n_accept[r], out_token[r] at k = n_accept[r]
+ * and -1 behind it; position k's distribution is row k of T.  tokens [R, gamma],
+ * n_accept, out_token [R], ids [R, gamma + 1] int32; n_accept is clamped to
+ * [0, gamma].  Limits: 1 <= R <= 65536, 1 <= gamma <= 64. */
+int dspark_emitted_tokens(int32_t R, int32_t gamma, const int32_t* tokens, const int32_t* n_accept,
+                          const int32_t* out_token, int32_t* ids, void* stream);
+
+/* Log probabilities of given tokens, with the entropy of their distribution
+ * and its most likely tokens.  For row r of logits z (V entries, the next row
+ * ld entries on, ld >= V; any element-aligned start) and x = ids[r]:
+ *   logprob[r] = z_x - lse,  lse = log sum_v exp(z_v)
+ *   entropy[r] = -sum_v p_v log p_v (nats), p = softmax(z)
+ *   top_ids[r, j], top_logprobs[r, j] = the (j + 1)-th most likely token and
+ *       its log probability, j < n_top; the lower token first among equal logits.
+ * An entry may be -inf (masked): its token has log probability -inf and is no
+ * alternative; places without one hold id -1 and -inf.  A row whose id lies
+ * outside [0, V) is skipped without being read: NaN, ids -1.  A row without a
+ * finite entry has no distribution: NaN, ids -1.
+ * logits: dtype; ids [N] int32; logprob, entropy [N] float32; top_ids int32 and
+ * top_logprobs float32 [N, n_top] (NULL if n_top is 0).  Sums in binary64 over
+ * binary32 exponentials (16 at a time in binary32).
+ * ws: dspark_logprobs_workspace_bytes(N, V, n_top) bytes, 256-byte aligned; 0
+ * bytes (ws may be NULL) where a workgroup takes a whole row.
+ * Limits: 1 <= N <= 2^24, 1 <= V < 2^26, 0 <= n_top <= 64. */
+size_t dspark_logprobs_workspace_bytes(int32_t N, int32_t V, int32_t n_top);
+int dspark_token_logprobs(int32_t dtype, int32_t N, int32_t V, int64_t ld, const void* logits,
+                          const int32_t* ids, int32_t n_top, float* logprob, float* entropy,
+                          int32_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
+                          void* stream);
+
 /* Device-side check of the values the host cannot see, the preconditions
  * above (a debugging aid, off the hot path: one pass over every tensor given).
  * counts: int64 [6] in device memory, overwritten with the number of
