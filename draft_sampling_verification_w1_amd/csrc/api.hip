@@ -242,6 +242,102 @@ LogprobLayout logprob_layout(int N, int V, int n_top) {
   return L;
 }
 
+// ---- paged cache ---------------------------------------------------------------
+int check_cache(const dspark_cache* c) {
+  if (!c) return fail(DSPARK_ERR_ARG, "cache is NULL");
+  if (c->dtype != DSPARK_F32 && c->dtype != DSPARK_BF16)
+    return fail(DSPARK_ERR_DTYPE, "dtype %d is not DSPARK_F32 or DSPARK_BF16", c->dtype);
+  if (c->slots < 1 || c->slots > kMaxCacheSlots)
+    return fail(DSPARK_ERR_SHAPE, "slots=%d outside [1, %d]", c->slots, kMaxCacheSlots);
+  if (c->pages < 1 || c->pages > (1 << 24))
+    return fail(DSPARK_ERR_SHAPE, "pages=%d outside [1, 2^24]", c->pages);
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1)))
+    return fail(DSPARK_ERR_SHAPE, "page_size=%d is not 16, 32, 64, 128 or 256", c->page_size);
+  if (c->max_pages < 1 || c->max_pages > (1 << 20) ||
+      (int64_t)c->slots * c->max_pages > (1 << 30) ||
+      (int64_t)c->max_pages * c->page_size >= ((int64_t)1 << 31))
+    return fail(DSPARK_ERR_SHAPE,
+                "max_pages=%d outside [1, 2^20], or slots*max_pages above 2^30, or "
+                "max_pages*page_size at 2^31 or above",
+                c->max_pages);
+  if (c->layers < 1 || c->layers > 1024 || c->kv_heads < 1 || c->kv_heads > 1024)
+    return fail(DSPARK_ERR_SHAPE, "layers=%d, kv_heads=%d outside [1, 1024]", c->layers, c->kv_heads);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(DSPARK_ERR_SHAPE, "head_dim=%d is not 64, 128 or 256", c->head_dim);
+  return DSPARK_OK;
+}
+
+int check_tables(const dspark_cache_tables* t) {
+  if (!t || !t->table || !t->lens || !t->held || !t->refs || !t->free_bits || !t->n_free)
+    return fail(DSPARK_ERR_ARG, "cache tables must be non-NULL");
+  const void* all[6] = {t->table, t->lens, t->held, t->refs, t->free_bits, t->n_free};
+  for (const void* p : all)
+    if ((uintptr_t)p % 4) return fail(DSPARK_ERR_ARG, "cache tables must be 4-byte aligned");
+  return DSPARK_OK;
+}
+
+CacheTables tables_of(const dspark_cache_tables* t) {
+  return CacheTables{t->table, t->lens, t->held, t->refs, (uint32_t*)t->free_bits, t->n_free};
+}
+
+CacheArgs cache_args(const dspark_cache* c, const dspark_cache_tables* t) {
+  CacheArgs a = {};
+  a.slots = c->slots;
+  a.max_pages = c->max_pages;
+  a.pages = c->pages;
+  a.page_shift = __builtin_ctz(c->page_size);
+  a.layers = c->layers;
+  a.kv_heads = c->kv_heads;
+  a.head_dim = c->head_dim;
+  a.page_bytes = c->kv_heads * c->page_size * c->head_dim * (c->dtype == DSPARK_BF16 ? 2 : 4);
+  if (t) a.t = tables_of(t);
+  return a;
+}
+
+int check_list(int n, const char* what) {
+  if (n < 1 || n > kMaxCacheSlots)
+    return fail(DSPARK_ERR_SHAPE, "%s: n=%d outside [1, %d]", what, n, kMaxCacheSlots);
+  return DSPARK_OK;
+}
+
+int check_tokens(const dspark_cache* c, int layer, int N, int heads, const char* what) {
+  if (layer < 0 || layer >= c->layers)
+    return fail(DSPARK_ERR_RANGE, "%s: layer %d outside [0, %d)", what, layer, c->layers);
+  if (N < 1 || N > (1 << 22)) return fail(DSPARK_ERR_SHAPE, "%s: N=%d outside [1, 2^22]", what, N);
+  if (heads < 1 || heads % c->kv_heads || (int64_t)N * heads > (1 << 30))
+    return fail(DSPARK_ERR_SHAPE, "%s: heads=%d is no multiple of kv_heads=%d, or N*heads above 2^30",
+                what, heads, c->kv_heads);
+  return DSPARK_OK;
+}
+
+// One layer's pages of K or V.
+void* layer_of(const dspark_cache* c, void* pool, int layer) {
+  return static_cast<char*>(pool) + (int64_t)layer * c->pages * cache_args(c, nullptr).page_bytes;
+}
+
+struct AttendLayout {
+  int rows, target;
+  size_t o, ml, bytes;
+};
+
+// Records of the items of split slots: a slot of n key tiles cut to ranges of r < n
+// has ceil(n / r) <= 2 n / r items per row tile and head, and r is at least the
+// batch's tiles over the target, so that there are at most 2 * target of them.
+AttendLayout attend_layout(const dspark_cache* c, int N, int heads, int max_chunk) {
+  AttendLayout L = {};
+  const int longest = max_chunk < N ? max_chunk : N;
+  const bool bf16 = c->dtype == DSPARK_BF16;
+  L.rows = attend_rows(bf16, c->head_dim, heads / c->kv_heads, longest);
+  L.target = kAttendTarget;
+  // sized for the largest tile, whatever chunk a call names
+  const size_t records = (size_t)2 * L.target * attend_max_rows(bf16, c->head_dim);
+  Carver v;
+  L.o = v.take(records * c->head_dim * sizeof(float));
+  L.ml = v.take(records * 2 * sizeof(float));
+  L.bytes = v.off;
+  return L;
+}
+
 // Packed tiles, then one float per tile (max |W2| over the tile).
 size_t packed_bytes(const dspark_problem* p) {
   const int ntiles = (p->V + kTile - 1) / kTile;
@@ -854,6 +950,162 @@ __attribute__((visibility("default"))) int dspark_token_logprobs(
   }
   hipError_t e = launch_logprobs(dtype == DSPARK_BF16, a, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "token_logprobs");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_init(const dspark_cache* c,
+                                                             const dspark_cache_tables* t,
+                                                             void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  hipError_t e = launch_cache_init(cache_args(c, t), (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_init");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_fork(const dspark_cache* c,
+                                                             const dspark_cache_tables* t, int32_t n,
+                                                             const int32_t* src, const int32_t* dst,
+                                                             int32_t* status, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_list(n, "cache_fork")) return e;
+  if (!src || !dst || !status)
+    return fail(DSPARK_ERR_ARG, "cache_fork: tensor pointers must be non-NULL");
+  hipError_t e = launch_cache_fork(cache_args(c, t), n, src, dst, status, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_fork");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_reserve(
+    const dspark_cache* c, const dspark_cache_tables* t, const int32_t* add, int32_t* status,
+    int32_t* cow_src, int32_t* cow_dst, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (!add || !status || !cow_src || !cow_dst)
+    return fail(DSPARK_ERR_ARG, "cache_reserve: tensor pointers must be non-NULL");
+  hipError_t e = launch_cache_reserve(cache_args(c, t), add, status, cow_src, cow_dst,
+                                      (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_reserve");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_commit(const dspark_cache* c,
+                                                               const dspark_cache_tables* t,
+                                                               const int32_t* keep, int32_t plus,
+                                                               void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (!keep) return fail(DSPARK_ERR_ARG, "cache_commit: keep must be non-NULL");
+  hipError_t e = launch_cache_commit(cache_args(c, t), keep, plus, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_commit");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_free(const dspark_cache* c,
+                                                             const dspark_cache_tables* t, int32_t n,
+                                                             const int32_t* slots, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_list(n, "cache_free")) return e;
+  if (!slots) return fail(DSPARK_ERR_ARG, "cache_free: slots must be non-NULL");
+  hipError_t e = launch_cache_free(cache_args(c, t), n, slots, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_free");
+  return ok();
+}
+
+__attribute__((visibility("default"))) size_t dspark_cache_compact_workspace_bytes(
+    const dspark_cache* c) {
+  if (check_cache(c) != DSPARK_OK) return 0;
+  return align_up((size_t)c->pages * sizeof(int32_t));
+}
+
+__attribute__((visibility("default"))) int dspark_cache_compact(
+    const dspark_cache* c, const dspark_cache_tables* t, const dspark_cache_tables* out,
+    int32_t* src, int32_t* dst, int32_t* n_moves, void* ws, size_t ws_bytes, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_tables(out)) return e;
+  if (!src || !dst || !n_moves)
+    return fail(DSPARK_ERR_ARG, "cache_compact: tensor pointers must be non-NULL");
+  if (int e = check_ws_bytes(align_up((size_t)c->pages * sizeof(int32_t)), ws, ws_bytes)) return e;
+  hipError_t e = launch_cache_compact(cache_args(c, t), tables_of(out), src, dst, n_moves,
+                                      static_cast<int32_t*>(ws), (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_compact");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_copy_pages(
+    const dspark_cache* c, void* K, void* V, int32_t n, const int32_t* src, const int32_t* dst,
+    const int32_t* count, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (n < 1 || n > (1 << 24))
+    return fail(DSPARK_ERR_SHAPE, "cache_copy_pages: n=%d outside [1, 2^24]", n);
+  if (!K || !V || !src || !dst)
+    return fail(DSPARK_ERR_ARG, "cache_copy_pages: tensor pointers must be non-NULL");
+  if (!aligned16(K) || !aligned16(V))
+    return fail(DSPARK_ERR_ARG, "cache_copy_pages: K and V must be 16-byte aligned");
+  hipError_t e = launch_cache_copy(cache_args(c, nullptr), K, V, n, src, dst, count,
+                                   (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_copy_pages");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_append(
+    const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, void* K, void* V, int32_t N,
+    const void* k, const void* v, const int32_t* offsets, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_tokens(c, layer, N, c->kv_heads, "cache_append")) return e;
+  if (!K || !V || !k || !v || !offsets)
+    return fail(DSPARK_ERR_ARG, "cache_append: tensor pointers must be non-NULL");
+  if (!aligned16(K) || !aligned16(V) || !aligned16(k) || !aligned16(v))
+    return fail(DSPARK_ERR_ARG, "cache_append: K, V, k and v must be 16-byte aligned");
+  hipError_t e = launch_cache_append(cache_args(c, t), c->dtype == DSPARK_BF16, layer_of(c, K, layer),
+                                     layer_of(c, V, layer), N, k, v, offsets, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_append");
+  return ok();
+}
+
+__attribute__((visibility("default"))) size_t dspark_attend_workspace_bytes(const dspark_cache* c,
+                                                                           int32_t N, int32_t heads) {
+  if (check_cache(c) != DSPARK_OK) return 0;
+  if (check_tokens(c, 0, N, heads, "attend") != DSPARK_OK) return 0;
+  return attend_layout(c, N, heads, N).bytes;
+}
+
+__attribute__((visibility("default"))) int dspark_attend(
+    const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, const void* K,
+    const void* V, int32_t N, int32_t heads, const void* q, const int32_t* offsets, float scale,
+    int32_t max_chunk, void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_tokens(c, layer, N, heads, "attend")) return e;
+  if (!(scale > 0.f) || scale > 1e30f)
+    return fail(DSPARK_ERR_RANGE, "attend: scale %g is not positive and finite", (double)scale);
+  if (max_chunk < 1) return fail(DSPARK_ERR_SHAPE, "attend: max_chunk=%d is below 1", max_chunk);
+  if (!K || !V || !q || !offsets || !out)
+    return fail(DSPARK_ERR_ARG, "attend: tensor pointers must be non-NULL");
+  if (!aligned16(K) || !aligned16(V) || !aligned16(q) || !aligned16(out))
+    return fail(DSPARK_ERR_ARG, "attend: K, V, q and out must be 16-byte aligned");
+  const AttendLayout L = attend_layout(c, N, heads, max_chunk);
+  if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
+  AttendArgs a = {};
+  a.c = cache_args(c, t);
+  a.N = N;
+  a.heads = heads;
+  a.group = heads / c->kv_heads;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q = q;
+  a.K = layer_of(c, const_cast<void*>(K), layer);
+  a.V = layer_of(c, const_cast<void*>(V), layer);
+  a.offsets = offsets;
+  a.out = out;
+  a.target = L.target;
+  a.part_o = at<float>(ws, L.o);
+  a.part_ml = at<float>(ws, L.ml);
+  hipError_t e = launch_attend(c->dtype == DSPARK_BF16, L.rows, a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "attend");
   return ok();
 }
 

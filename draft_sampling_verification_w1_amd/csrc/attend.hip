@@ -1,0 +1,606 @@
+// attend.hip -- attention of a chunk of new tokens per slot over a paged cache.
+//
+// Token i of slot s's chunk sees the keys at positions p <= lens[s] + i:
+//   o = sum_p softmax_p(scale q . k_p) v_p,
+// computed in one pass over the keys with a running maximum m and sum l:
+//   p = 2^(c q.k - m), l += p, O += p v; a rise of m by d scales l and O by 2^-d.
+//
+// Layout.  A page stores K as [kv_head][D / E][token][E] and V as
+// [kv_head][token / E][D][E] (E elements = 16 bytes), which are the matrix cores'
+// operand orders: the pass computes S^T = K Q^T and O^T = V^T P^T, so that
+//   - a wave's load of a K or V operand is 64 lanes x 16 contiguous-by-row bytes,
+//     straight from HBM to the registers that feed the matrix instruction (no LDS,
+//     no barrier, no transposition), and
+//   - S^T's accumulator already is P^T's operand: a lane holds the scores of one
+//     query (column l % 16); which keys it holds is settled by the order in which
+//     the key rows of K are loaded (key_of), chosen to match V's 16-byte groups.
+//
+// Work.  A row of a tile is one (token, query head of the kv head's group) pair, so
+// that the group shares every key it reads.  An item is (slot, kv head, row tile,
+// range of keys); its four waves take a quarter of the range each and join their
+// sums through LDS.  Slots and lengths are known on the device only: each workgroup
+// works out the whole batch's items from lens and offsets (one round trip), cut to
+// ranges of about equal length, and walks over its share.  Ranges of one slot are
+// joined by k_attend_join.
+#include "device_common.h"
+#include "kernels.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWaves = 4;
+constexpr int kKeys = 32;      // keys per step of a wave
+constexpr int kMinTiles = 4;   // shortest range of an item, in steps
+constexpr float kRise = 8.f;   // the running maximum may lag by this (in log2)
+
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// What differs between the element types.  `Chunk` is a lane's 16 bytes of an operand.
+template <typename E>
+struct Ops;
+
+template <>
+struct Ops<uint16_t> {
+  typedef bf16x8 Chunk;
+  static constexpr int kE = 8;
+  static constexpr int kVChunks = 1;  // V operands per step and 16 dimensions
+  // key of row m of 16-key block u of a step: lane group q's accumulators of both
+  // blocks are then keys 8q .. 8q + 7, one 16-byte group of V
+  static __device__ __forceinline__ int key_of(int u, int m) { return 8 * (m >> 2) + 4 * u + (m & 3); }
+  // first key of the group that lane group q loads for V operand u
+  static __device__ __forceinline__ int vkey_of(int, int q) { return 8 * q; }
+  // position of accumulator j of block u among the step's keys, for lane group q
+  static __device__ __forceinline__ int skey_of(int u, int j, int q) { return 8 * q + 4 * u + j; }
+  static __device__ __forceinline__ f32x4 score(Chunk k, Chunk q, f32x4 s) { return mma(k, q, s); }
+  static __device__ __forceinline__ Chunk zero() {
+    Chunk c;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = (__bf16)0.f;
+    return c;
+  }
+  // elements n .. 7 cleared
+  static __device__ __forceinline__ Chunk keep(Chunk c, int n) {
+    union { Chunk b; uint32_t w[4]; } x;
+    x.b = c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t mask = n >= 2 * i + 2 ? 0xFFFFFFFFu : (n == 2 * i + 1 ? 0x0000FFFFu : 0u);
+      x.w[i] &= mask;
+    }
+    return x.b;
+  }
+};
+
+template <>
+struct Ops<float> {
+  typedef f32x4 Chunk;
+  static constexpr int kE = 4;
+  static constexpr int kVChunks = 2;
+  static __device__ __forceinline__ int key_of(int u, int m) { return 16 * u + m; }
+  static __device__ __forceinline__ int vkey_of(int u, int q) { return 16 * u + 4 * q; }
+  static __device__ __forceinline__ int skey_of(int u, int j, int q) { return 16 * u + 4 * q + j; }
+  static __device__ __forceinline__ f32x4 score(Chunk k, Chunk q, f32x4 s) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s = __builtin_amdgcn_mfma_f32_16x16x4f32(k[j], q[j], s, 0, 0, 0);
+    return s;
+  }
+  static __device__ __forceinline__ Chunk zero() { return f32x4{0.f, 0.f, 0.f, 0.f}; }
+  static __device__ __forceinline__ Chunk keep(Chunk c, int n) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = i < n ? c[i] : 0.f;
+    return c;
+  }
+};
+
+// ---- the batch's work items -----------------------------------------------------
+struct SlotWork {
+  int o0, chunk;     // first token row and tokens of the chunk
+  int len;           // cached tokens before it
+  int keys;          // keys that exist: len + chunk, at most the table's width
+  int row_tiles, key_tiles;
+};
+
+__device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int rows) {
+  SlotWork w;
+  w.o0 = min(max(a.offsets[s], 0), a.N);
+  const int o1 = min(max(a.offsets[s + 1], w.o0), a.N);
+  w.chunk = o1 - w.o0;
+  w.len = max(a.c.t.lens[s], 0);
+  const int64_t width = (int64_t)a.c.max_pages << a.c.page_shift;
+  const int64_t keys = (int64_t)w.len + w.chunk;
+  w.keys = (int)(keys < width ? keys : width);
+  w.row_tiles = (int)(((int64_t)w.chunk * a.group + rows - 1) / rows);
+  w.key_tiles = (w.keys + kKeys - 1) / kKeys;
+  return w;
+}
+
+__device__ __forceinline__ int splits_of(const SlotWork& w, int range) {
+  return w.row_tiles == 0 ? 0 : max(1, (w.key_tiles + range - 1) / range);
+}
+
+// Items before each thread's run of slots (thread t: slots [t per, t per + per)), the
+// items of split slots apart.
+struct Plan {
+  int before[kThreads + 1];
+  int split_before[kThreads + 1];
+  int64_t sum[kWaves];
+  int range;  // key tiles per item
+  int per;
+};
+
+// kGroups: count the (slot, kv head, row tile) groups of split slots instead of all items.
+template <bool kGroups>
+__device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& plan) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (a.c.slots + kThreads - 1) / kThreads;
+  const int s0 = tid * per, s1 = min(s0 + per, a.c.slots);
+  int64_t work = 0;
+  for (int s = s0; s < s1; ++s) {
+    const SlotWork w = slot_work(a, s, rows);
+    work += (int64_t)w.row_tiles * w.key_tiles;
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) work += __shfl_xor(work, off, 64);
+  if (lane == 0) plan.sum[wave] = work;
+  __syncthreads();
+  work = (plan.sum[0] + plan.sum[1] + plan.sum[2] + plan.sum[3]) * a.c.kv_heads;
+  const int64_t r = (work + a.target - 1) / a.target;
+  const int range = (int)(r > kMinTiles ? r : kMinTiles);
+  int items = 0, split = 0;
+  for (int s = s0; s < s1; ++s) {
+    const SlotWork w = slot_work(a, s, rows);
+    const int ns = splits_of(w, range);
+    const int n = ns * w.row_tiles * a.c.kv_heads;
+    if (ns > 1) {
+      split += n;
+      if (kGroups) items += w.row_tiles * a.c.kv_heads;
+    }
+    if (!kGroups) items += n;
+  }
+  int x = items, y = split;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int px = __shfl_up(x, off, 64), py = __shfl_up(y, off, 64);
+    if (lane >= off) {
+      x += px;
+      y += py;
+    }
+  }
+  __syncthreads();
+  if (lane == 63) plan.sum[wave] = ((int64_t)y << 32) | (uint32_t)x;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) {
+      x += (int)(uint32_t)plan.sum[w];
+      y += (int)(plan.sum[w] >> 32);
+    }
+  }
+  plan.before[tid + 1] = x;
+  plan.split_before[tid + 1] = y;
+  if (tid == 0) {
+    plan.before[0] = 0;
+    plan.split_before[0] = 0;
+    plan.range = range;
+    plan.per = per;
+  }
+  __syncthreads();
+}
+
+struct Item {
+  SlotWork w;
+  int slot, head, tile, split, splits;
+  int part;  // first partial record of the (head, tile) group; split i has part + i
+};
+
+// Item `id` of the plan: the thread run that holds it by bisection, then the slot in it.
+template <bool kGroups>
+__device__ __forceinline__ Item find_item(const AttendArgs& a, int rows, const Plan& plan, int id) {
+  int lo = 0, hi = kThreads - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (plan.before[mid] <= id) lo = mid;
+    else hi = mid - 1;
+  }
+  Item it;
+  int left = id - plan.before[lo], part = plan.split_before[lo];
+  int s = lo * plan.per;
+  const int end = min(s + plan.per, a.c.slots);
+  for (;; ++s) {
+    it.w = slot_work(a, s, rows);
+    it.splits = splits_of(it.w, plan.range);
+    const int groups = it.w.row_tiles * a.c.kv_heads;
+    const int all = groups * it.splits;
+    const int n = kGroups ? (it.splits > 1 ? groups : 0) : all;
+    if (left < n || s + 1 >= end) break;
+    left -= n;
+    if (it.splits > 1) part += all;
+  }
+  it.slot = s;
+  // row tiles that read the same keys are neighbours
+  it.tile = left % it.w.row_tiles;
+  const int rest = left / it.w.row_tiles;
+  it.head = rest % a.c.kv_heads;
+  it.split = kGroups ? 0 : rest / a.c.kv_heads;
+  it.part = part + (it.head * it.w.row_tiles + it.tile) * it.splits;
+  return it;
+}
+
+template <typename E>
+__device__ __forceinline__ void store4(E* to, f32x4 v);
+template <>
+__device__ __forceinline__ void store4<float>(float* to, f32x4 v) {
+  *reinterpret_cast<f32x4*>(to) = v;
+}
+template <>
+__device__ __forceinline__ void store4<uint16_t>(uint16_t* to, f32x4 v) {
+  // rounded to nearest even, once
+  typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+  bf16x4 b;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = (__bf16)v[i];
+  *reinterpret_cast<bf16x4*>(to) = b;
+}
+
+// One item.  NQ 16-row blocks per wave; D dimensions.
+template <typename E, int D, int NQ>
+__device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it, int range,
+                                            float* sh_ml, float* sh_o) {
+  typedef Ops<E> Op;
+  typedef typename Op::Chunk Chunk;
+  constexpr int kE = Op::kE;
+  constexpr int kSteps = D / (4 * kE);  // K operands per 16 keys
+  constexpr int kDT = D / 16;           // 16-dimension blocks of the output
+  constexpr int kVC = Op::kVChunks;
+  constexpr int kRows = 16 * NQ;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int n = lane & 15, quad = lane >> 4;
+  const int G = a.group, H = a.c.kv_heads;
+  const int row0 = it.tile * kRows, rows = it.w.chunk * G;
+  const E* q = static_cast<const E*>(a.q);
+
+  // queries as operands: lane (n, quad), operand s: dimensions kE (4 s + quad) ..
+  Chunk qo[NQ][kSteps];
+  int limit[NQ];  // keys that the lane's row sees
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int row = row0 + 16 * i + n;
+    const bool live = row < rows;
+    const int token = live ? row / G : 0;
+    const E* p = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D;
+    limit[i] = min(it.w.len + token + 1, it.w.keys);
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s)
+      qo[i][s] = live ? *reinterpret_cast<const Chunk*>(p + kE * (4 * s + quad)) : Op::zero();
+  }
+  // keys any row of the tile sees, and keys all of them see
+  const int last_row = min(row0 + kRows, rows) - 1;
+  const int seen = min(it.w.len + last_row / G + 1, it.w.keys);
+  const int common = min(it.w.len + row0 / G + 1, it.w.keys);
+  // the wave's quarter of the item's range, in steps of kKeys keys
+  const int t_first = it.split * range;
+  const int t_end = min(t_first + range, (seen + kKeys - 1) / kKeys);
+  const int count = max(0, t_end - t_first);
+  const int t0 = t_first + count * wave / kWaves, t1 = t_first + count * (wave + 1) / kWaves;
+
+  f32x4 o[NQ][kDT];
+  float m[NQ], l[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[i][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // Page ids of 64 consecutive table columns, one per lane; a step reads its two
+  // halves' ids from them.  Ids outside the pool count as no page.
+  const int shift = a.c.page_shift;
+  const int32_t* table = a.c.t.table + (int64_t)it.slot * a.c.max_pages;
+  int col0 = (t0 * kKeys) >> shift;
+  auto columns = [&](int c0) {
+    const int c = c0 + lane;
+    const int p = c < a.c.max_pages ? table[c] : -1;
+    return p >= 0 && p < a.c.pages ? p : -1;
+  };
+  int ids = columns(col0);
+  const int page = 1 << shift;
+  const int64_t page_elems = (int64_t)H * page * D;
+  const E* Kh = static_cast<const E*>(a.K) + (int64_t)it.head * page * D;
+  const E* Vh = static_cast<const E*>(a.V) + (int64_t)it.head * page * D;
+  // ids of the pages of keys [32 t, 32 t + 16) and [32 t + 16, 32 t + 32)
+  auto pages_of = [&](int t, int& pa, int& pb) {
+    const int ca = (t * kKeys) >> shift, cb = (t * kKeys + 16) >> shift;
+    if (cb >= col0 + 64) {
+      col0 = ca;
+      ids = columns(col0);
+    }
+    pa = __builtin_amdgcn_readlane(ids, ca - col0);
+    pb = __builtin_amdgcn_readlane(ids, cb - col0);
+  };
+  auto load_k = [&](int t, int pa, int pb, Chunk (&k)[2][kSteps]) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int key = Op::key_of(u, n);
+      const int p = max(key < 16 ? pa : pb, 0);
+      const int at = (t * kKeys + key) & (page - 1);
+      const E* base = Kh + p * page_elems + (int64_t)at * kE;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        k[u][s] = *reinterpret_cast<const Chunk*>(base + (int64_t)(4 * s + quad) * page * kE);
+    }
+  };
+  auto load_v = [&](int t, int pa, int pb, Chunk (&v)[kVC][kDT]) {
+#pragma unroll
+    for (int u = 0; u < kVC; ++u) {
+      const int key = Op::vkey_of(u, quad);
+      const int p = max(key < 16 ? pa : pb, 0);
+      const int at = (t * kKeys + key) & (page - 1);
+      const E* base = Vh + p * page_elems + (int64_t)(at / kE) * D * kE;
+#pragma unroll
+      for (int d = 0; d < kDT; ++d)
+        v[u][d] = *reinterpret_cast<const Chunk*>(base + (16 * d + n) * kE);
+    }
+  };
+
+  Chunk k[2][kSteps], v[kVC][kDT];
+  int pa = -1, pb = -1;
+  if (t0 < t1) {
+    pages_of(t0, pa, pb);
+    load_k(t0, pa, pb, k);
+  }
+  for (int t = t0; t < t1; ++t) {
+    load_v(t, pa, pb, v);
+    f32x4 s[NQ][2];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kSteps; ++c) acc = Op::score(k[u][c], qo[i][c], acc);
+        s[i][u] = acc;
+      }
+    const int ma = pa, mb = pb;
+    if (t + 1 < t1) {
+      pages_of(t + 1, pa, pb);
+      load_k(t + 1, pa, pb, k);
+    }
+    // keys that some row does not see: behind its position, or on no page
+    if ((t + 1) * kKeys > common || ma < 0 || mb < 0) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = Op::skey_of(u, j, quad);
+            const bool there = t * kKeys + key < limit[i] && (key < 16 ? ma : mb) >= 0;
+            s[i][u][j] = there ? s[i][u][j] : -INFINITY;
+          }
+      // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN
+#pragma unroll
+      for (int u = 0; u < kVC; ++u) {
+        const int key = Op::vkey_of(u, quad);
+        const int keep = (key < 16 ? ma : mb) >= 0 ? min(max(seen - (t * kKeys + key), 0), kE) : 0;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) v[u][d] = Op::keep(v[u][d], keep);
+      }
+    }
+    Chunk p[NQ][kVC];
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float mx = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
+                       fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
+      mx *= a.scale_log2;
+      // the maximum moves only when some row has passed it by 2^kRise: until then
+      // the sums grow past 1, far from binary32's end, and nothing is rescaled
+      if (__ballot(mx > m[i] + kRise)) {
+        float mn = fmaxf(m[i], mx);
+        mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
+        mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
+        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[i] - mn);
+        m[i] = mn;
+        l[i] *= f;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) o[i][d] *= f;
+      }
+      const float ref = m[i] == -INFINITY ? 0.f : m[i];
+      float e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        e[j] = __builtin_amdgcn_exp2f(fmaf(s[i][j >> 2][j & 3], a.scale_log2, -ref));
+      l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(E) == 2) p[i][0][j] = (__bf16)e[j];
+        else p[i][j >> 2][j & 3] = e[j];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kVC; ++u)
+#pragma unroll
+      for (int d = 0; d < kDT; ++d)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) o[i][d] = Op::score(v[u][d], p[i][u], o[i][d]);
+  }
+
+  // ---- the four waves' sums joined ----
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    l[i] += __shfl_xor(l[i], 16, 64);
+    l[i] += __shfl_xor(l[i], 32, 64);
+    if (quad == 0) {
+      sh_ml[(wave * kRows + 16 * i + n) * 2] = m[i];
+      sh_ml[(wave * kRows + 16 * i + n) * 2 + 1] = l[i];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    float mn = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + 16 * i + n) * 2]);
+    const float f = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] - mn);
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) o[i][d] *= f;
+  }
+  constexpr int kPart = 32;        // dimensions joined at a time
+  constexpr int kLd = kPart + 4;   // row stride, against bank conflicts
+  const bool whole = it.splits == 1;
+  const int64_t rec = it.part + it.split;
+#pragma unroll
+  for (int d0 = 0; d0 < D; d0 += kPart) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int d = 0; d < kPart / 16; ++d)
+        *reinterpret_cast<f32x4*>(sh_o + (wave * kRows + 16 * i + n) * kLd + 16 * d + 4 * quad) =
+            o[i][d0 / 16 + d];
+    __syncthreads();
+    for (int x = threadIdx.x; x < kRows * (kPart / 4); x += kThreads) {
+      const int r = x / (kPart / 4), c = x % (kPart / 4);
+      const int row = row0 + r;
+      if (row < rows) {
+        f32x4 sum = *reinterpret_cast<const f32x4*>(sh_o + r * kLd + 4 * c);
+#pragma unroll
+        for (int w = 1; w < kWaves; ++w)
+          sum += *reinterpret_cast<const f32x4*>(sh_o + (w * kRows + r) * kLd + 4 * c);
+        float mn = -INFINITY, ls = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + r) * 2]);
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          const float mw = sh_ml[(w * kRows + r) * 2];
+          if (mw != -INFINITY) ls += sh_ml[(w * kRows + r) * 2 + 1] * __builtin_amdgcn_exp2f(mw - mn);
+        }
+        if (whole) {
+          const int token = row / G;
+          E* to = static_cast<E*>(a.out) +
+                  ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row - token * G)) * D + d0 + 4 * c;
+          store4<E>(to, sum * (ls > 0.f ? 1.f / ls : 0.f));
+        } else {
+          *reinterpret_cast<f32x4*>(a.part_o + (rec * kRows + r) * D + d0 + 4 * c) = sum;
+          if (d0 == 0 && c == 0) {
+            a.part_ml[(rec * kRows + r) * 2] = mn;
+            a.part_ml[(rec * kRows + r) * 2 + 1] = ls;
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename E, int D, int NQ>
+__global__ __launch_bounds__(kThreads, NQ * D <= 256 ? 2 : 1) void k_attend(AttendArgs a) {
+  constexpr int kRows = 16 * NQ;
+  __shared__ Plan plan;
+  __shared__ float sh_ml[kWaves * kRows * 2];
+  __shared__ __align__(16) float sh_o[kWaves * kRows * 36];
+  make_plan<false>(a, kRows, plan);
+  const int total = plan.before[kThreads];
+  // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
+  // items, so that row tiles that read the same keys share its L2.
+  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3, step = gridDim.x >> 3;
+  const int first = (int)((int64_t)total * xcd / 8), last = (int)((int64_t)total * (xcd + 1) / 8);
+  for (int id = first + idx; id < last; id += step) {
+    const Item it = find_item<false>(a, kRows, plan, id);
+    attend_item<E, D, NQ>(a, it, plan.range, sh_ml, sh_o);
+  }
+}
+
+// Joins the key ranges of split slots: a workgroup per (slot, kv head, row tile), D / 4
+// threads per row.
+template <typename E>
+__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, int rows_per_tile) {
+  __shared__ Plan plan;
+  make_plan<true>(a, rows_per_tile, plan);
+  const int total = plan.before[kThreads];
+  const int D = a.c.head_dim, G = a.group;
+  const int per_row = D / 4;
+  for (int id = blockIdx.x; id < total; id += gridDim.x) {
+    const Item it = find_item<true>(a, rows_per_tile, plan, id);
+    const int row0 = it.tile * rows_per_tile;
+    const int rows = min(rows_per_tile, it.w.chunk * G - row0);
+    for (int x = threadIdx.x; x < rows * per_row; x += kThreads) {
+      const int r = x / per_row, c = x % per_row;
+      float mn = -INFINITY;
+      for (int i = 0; i < it.splits; ++i)
+        mn = fmaxf(mn, a.part_ml[((int64_t)(it.part + i) * rows_per_tile + r) * 2]);
+      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+      float ls = 0.f;
+      for (int i = 0; i < it.splits; ++i) {
+        const int64_t o = (int64_t)(it.part + i) * rows_per_tile + r;
+        const float mi = a.part_ml[o * 2];
+        if (mi == -INFINITY) continue;
+        const float f = __builtin_amdgcn_exp2f(mi - mn);
+        ls += a.part_ml[o * 2 + 1] * f;
+        sum += *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c) * f;
+      }
+      const int row = row0 + r, token = row / G;
+      E* to = static_cast<E*>(a.out) +
+              ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row - token * G)) * D + 4 * c;
+      store4<E>(to, sum * (ls > 0.f ? 1.f / ls : 0.f));
+    }
+  }
+}
+
+template <typename E, int D, int NQ>
+void start(const AttendArgs& a, int grid, hipStream_t stream) {
+  hipLaunchKernelGGL((k_attend<E, D, NQ>), dim3(grid), dim3(kThreads), 0, stream, a);
+}
+
+}  // namespace
+
+// The largest tile: what the registers hold (the output's accumulators take
+// D / 4 registers per 16 rows, the queries' operands half of that).
+int attend_max_rows(bool bf16, int head_dim) {
+  return 16 * (bf16 ? (head_dim == 256 ? 2 : 5) : (head_dim == 256 ? 1 : 2));
+}
+
+// Rows (token, head) of a tile: as many 16-row blocks as the longest chunk needs,
+// spread evenly over its tiles.
+int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
+  const int most = attend_max_rows(bf16, head_dim);
+  const int64_t rows = (int64_t)max_chunk * group;
+  const int64_t tiles = (rows + most - 1) / most;
+  const int need = (int)(((rows + tiles - 1) / tiles + 15) / 16);
+  const int sizes[4] = {1, 2, 3, 5};
+  for (int n : sizes)
+    if (n >= need) return 16 * n;
+  return most;
+}
+
+hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream) {
+  {
+    TimingScope t("attend", stream);
+    const int grid = 512;
+    const int D = a.c.head_dim, nq = rows / 16;
+#define ATTEND(E, DIM, N) \
+  if (D == DIM && nq == N) start<E, DIM, N>(a, grid, stream); else
+    if (bf16) {
+      ATTEND(uint16_t, 64, 1) ATTEND(uint16_t, 64, 2) ATTEND(uint16_t, 64, 3) ATTEND(uint16_t, 64, 5)
+      ATTEND(uint16_t, 128, 1) ATTEND(uint16_t, 128, 2) ATTEND(uint16_t, 128, 3) ATTEND(uint16_t, 128, 5)
+      ATTEND(uint16_t, 256, 1) ATTEND(uint16_t, 256, 2) return hipErrorInvalidValue;
+    } else {
+      ATTEND(float, 64, 1) ATTEND(float, 64, 2) ATTEND(float, 128, 1) ATTEND(float, 128, 2)
+      ATTEND(float, 256, 1) return hipErrorInvalidValue;
+    }
+#undef ATTEND
+  }
+  {
+    TimingScope t("attend_join", stream);
+    if (bf16)
+      hipLaunchKernelGGL(k_attend_join<uint16_t>, dim3(512), dim3(kThreads), 0, stream, a, rows);
+    else
+      hipLaunchKernelGGL(k_attend_join<float>, dim3(512), dim3(kThreads), 0, stream, a, rows);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace dspark

@@ -292,4 +292,57 @@ hipError_t launch_logprobs(bool bf16, const LogprobArgs& a, hipStream_t stream);
 hipError_t launch_emitted(int R, int gamma, const int32_t* tokens, const int32_t* n_accept,
                           const int32_t* out_token, int32_t* ids, hipStream_t stream);
 
+// ---- paged key/value cache ---------------------------------------------------
+constexpr int kMaxCacheSlots = 4096;
+struct CacheTables {
+  int32_t* table;      // [slots, max_pages]
+  int32_t* lens;       // [slots] tokens
+  int32_t* held;       // [slots] pages
+  int32_t* refs;       // [pages]
+  uint32_t* free_bits; // [ceil(pages / 32)]
+  int32_t* n_free;     // [1]
+};
+struct CacheArgs {
+  int slots, max_pages, pages, page_shift, layers, kv_heads, head_dim;
+  int page_bytes;      // of K (and of V) in one layer
+  CacheTables t;
+};
+hipError_t launch_cache_init(const CacheArgs& a, hipStream_t stream);
+hipError_t launch_cache_fork(const CacheArgs& a, int n, const int32_t* src, const int32_t* dst,
+                             int32_t* status, hipStream_t stream);
+hipError_t launch_cache_free(const CacheArgs& a, int n, const int32_t* slots, hipStream_t stream);
+hipError_t launch_cache_commit(const CacheArgs& a, const int32_t* keep, int plus,
+                               hipStream_t stream);
+hipError_t launch_cache_reserve(const CacheArgs& a, const int32_t* add, int32_t* status,
+                                int32_t* cow_src, int32_t* cow_dst, hipStream_t stream);
+hipError_t launch_cache_compact(const CacheArgs& a, const CacheTables& out, int32_t* src,
+                                int32_t* dst, int32_t* n_moves, int32_t* rank,
+                                hipStream_t stream);
+hipError_t launch_cache_copy(const CacheArgs& a, void* K, void* V, int n, const int32_t* src,
+                             const int32_t* dst, const int32_t* count, hipStream_t stream);
+hipError_t launch_cache_append(const CacheArgs& a, bool bf16, void* K, void* V, int N,
+                               const void* k, const void* v, const int32_t* offsets,
+                               hipStream_t stream);
+
+// Attention of a chunk of new tokens per slot over the pages.
+struct AttendArgs {
+  CacheArgs c;
+  int N, heads, group;     // token rows of q, query heads, query heads per kv head
+  float scale_log2;        // score scale * log2 e
+  const void* q;           // [N, heads, head_dim]
+  const void* K;           // one layer's pages
+  const void* V;
+  const int32_t* offsets;  // [slots + 1]
+  void* out;               // [N, heads, head_dim]
+  int target;              // work items aimed at
+  float* part_o;           // [2 * target][rows][head_dim] of the items of split slots
+  float* part_ml;          // [2 * target][rows][2] largest score and sum
+};
+// Items aimed at: what is resident at once (256 CUs, one or two workgroups each)
+// twice or four times over, so that ranges of unlike length even out.
+constexpr int kAttendTarget = 1024;
+int attend_max_rows(bool bf16, int head_dim);
+int attend_rows(bool bf16, int head_dim, int group, int max_chunk);
+hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
+
 }  // namespace dspark

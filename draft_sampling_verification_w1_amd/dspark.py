@@ -7,6 +7,7 @@ library has not been built this module raises instead of falling back.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -23,7 +24,10 @@ SYMBOLS = ("dspark_w2_packed_bytes", "dspark_pack_w2", "dspark_workspace_bytes",
            "dspark_schedule_capacity", "dspark_schedule_topk", "dspark_schedule_threshold",
            "dspark_acceptance_stats", "dspark_sts_workspace_bytes", "dspark_sts_fit",
            "dspark_emitted_tokens", "dspark_logprobs_workspace_bytes", "dspark_token_logprobs",
-           "dspark_check_inputs", "dspark_last_error", "dspark_timing_enable",
+           "dspark_cache_init", "dspark_cache_fork", "dspark_cache_reserve", "dspark_cache_commit",
+           "dspark_cache_free", "dspark_cache_compact_workspace_bytes", "dspark_cache_compact",
+           "dspark_cache_copy_pages", "dspark_cache_append", "dspark_attend_workspace_bytes",
+           "dspark_attend", "dspark_check_inputs", "dspark_last_error", "dspark_timing_enable",
            "dspark_timing_report")
 
 
@@ -31,6 +35,15 @@ class Problem(ctypes.Structure):
     _fields_ = [("R", ctypes.c_int32), ("gamma", ctypes.c_int32), ("V", ctypes.c_int32),
                 ("rank", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("seed", ctypes.c_uint64)]
+
+
+class Cache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("slots", "max_pages", "pages", "page_size", "layers",
+                                              "kv_heads", "head_dim", "dtype")]
+
+
+class CacheTables(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("table", "lens", "held", "refs", "free_bits", "n_free")]
 
 
 class DsparkError(RuntimeError):
@@ -83,6 +96,21 @@ def lib() -> ctypes.CDLL:
         L.dspark_logprobs_workspace_bytes.restype = size
         L.dspark_token_logprobs.argtypes = [i32, i32, i32, i64, _vp, _vp, i32, _vp, _vp, _vp, _vp,
                                             _vp, size, _vp]
+        C, CT = ctypes.POINTER(Cache), ctypes.POINTER(CacheTables)
+        L.dspark_cache_init.argtypes = [C, CT, _vp]
+        L.dspark_cache_fork.argtypes = [C, CT, i32, _vp, _vp, _vp, _vp]
+        L.dspark_cache_reserve.argtypes = [C, CT, _vp, _vp, _vp, _vp, _vp]
+        L.dspark_cache_commit.argtypes = [C, CT, _vp, i32, _vp]
+        L.dspark_cache_free.argtypes = [C, CT, i32, _vp, _vp]
+        L.dspark_cache_compact_workspace_bytes.argtypes = [C]
+        L.dspark_cache_compact_workspace_bytes.restype = size
+        L.dspark_cache_compact.argtypes = [C, CT, CT, _vp, _vp, _vp, _vp, size, _vp]
+        L.dspark_cache_copy_pages.argtypes = [C, _vp, _vp, i32, _vp, _vp, _vp, _vp]
+        L.dspark_cache_append.argtypes = [C, CT, i32, _vp, _vp, i32, _vp, _vp, _vp, _vp]
+        L.dspark_attend_workspace_bytes.argtypes = [C, i32, i32]
+        L.dspark_attend_workspace_bytes.restype = size
+        L.dspark_attend.argtypes = [C, CT, i32, _vp, _vp, i32, i32, _vp, _vp, ctypes.c_float, i32,
+                                    _vp, _vp, size, _vp]
         L.dspark_last_error.restype = ctypes.c_char_p
         L.dspark_timing_enable.argtypes = [ctypes.c_int]
         L.dspark_timing_report.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
@@ -91,6 +119,9 @@ def lib() -> ctypes.CDLL:
                      "dspark_schedule", "dspark_schedule_capacity", "dspark_schedule_topk",
                      "dspark_schedule_threshold", "dspark_acceptance_stats", "dspark_sts_fit",
                      "dspark_check_inputs", "dspark_emitted_tokens", "dspark_token_logprobs",
+                     "dspark_cache_init", "dspark_cache_fork", "dspark_cache_reserve",
+                     "dspark_cache_commit", "dspark_cache_free", "dspark_cache_compact",
+                     "dspark_cache_copy_pages", "dspark_cache_append", "dspark_attend",
                      "dspark_timing_enable", "dspark_timing_report"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L
@@ -108,6 +139,13 @@ def _ptr(t):
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _on(device):
+    """The context in which calls go to `device` (none needed if it is the current one)."""
+    if device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
 
 
 def _need(t, name, dtype=None, shape=None):
@@ -434,7 +472,7 @@ def emitted_tokens(tokens, n_accept, out_token, out=None):
     if out is None:
         out = torch.empty((R, gamma + 1), dtype=torch.int32, device=tokens.device)
     _need(out, "out", dtype=torch.int32, shape=(R, gamma + 1))
-    with torch.cuda.device(tokens.device):
+    with _on(tokens.device):
         _check(lib().dspark_emitted_tokens(R, gamma, _ptr(tokens), _ptr(n_accept), _ptr(out_token),
                                            _ptr(out), _stream()))
     return out
@@ -480,7 +518,7 @@ def token_logprobs(logits, ids, n_top: int = 0, ws=None, out=None):
         _need(out[name], name, dtype=dt, shape=shape)
         if out[name].device != dev:
             raise ValueError(f"{name} must be on the device of logits")
-    with torch.cuda.device(dev):
+    with _on(dev):
         if ws is None:
             ws = logprobs_workspace(N, V, n_top, dev)
         _check(lib().dspark_token_logprobs(_DTYPES[logits.dtype], N, V, ld, _ptr(logits), _ptr(ids),

@@ -291,6 +291,135 @@ int dspark_token_logprobs(int32_t dtype, int32_t N, int32_t V, int64_t ld, const
                           int32_t* top_ids, float* top_logprobs, void* ws, size_t ws_bytes,
                           void* stream);
 
+/* ---- Paged key/value cache -------------------------------------------------
+ * What the target's verify forward pass keeps between rounds, and its pages:
+ * a round appends the chunk of tokens it verifies (the anchor and the
+ * scheduled drafts) and keeps the accepted ones.  Every length is on the
+ * device; no call needs the host to know one.
+ *
+ * Storage, owned by the caller (E = 16 bytes of elements: 8 bf16, 4 f32):
+ *   K [layers, pages, kv_heads, head_dim / E, page_size, E]
+ *   V [layers, pages, kv_heads, page_size / E, head_dim, E]   (dtype, 16-byte aligned)
+ * (the operand orders of the matrix cores).  Tables (dspark_cache_tables):
+ *   table     [slots, max_pages] int32, a slot's pages in order, -1 behind them
+ *   lens      [slots] int32, tokens cached
+ *   held      [slots] int32, pages held (at least ceil(lens / page_size))
+ *   refs      [pages] int32, slots that hold a page
+ *   free_bits [ceil(pages / 32)] uint32, bit p % 32 of word p / 32: refs[p] == 0
+ *   n_free    [1] int32
+ * dspark_cache_init empties them; after that they change through these calls
+ * only, on one stream or in an order that the caller keeps.  Pages are taken
+ * lowest index first, so that equal calls give equal tables.  Slot ids, page
+ * ids and lengths read from the device are checked before they index memory:
+ * an invalid page holds no keys, and what would be written to it is dropped.
+ * Limits: 1 <= slots <= 4096, 1 <= pages <= 2^24, page_size 16, 32, 64, 128 or
+ * 256, 1 <= max_pages <= 2^20, slots * max_pages <= 2^30, max_pages * page_size
+ * < 2^31, 1 <= layers, kv_heads <= 1024, head_dim 64, 128 or 256. */
+typedef struct {
+  int32_t slots;
+  int32_t max_pages;
+  int32_t pages;
+  int32_t page_size;
+  int32_t layers;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t dtype;
+} dspark_cache;
+
+typedef struct {
+  int32_t* table;
+  int32_t* lens;
+  int32_t* held;
+  int32_t* refs;
+  uint32_t* free_bits;
+  int32_t* n_free;
+} dspark_cache_tables;
+
+/* Empty tables: every slot without tokens, every page free. */
+int dspark_cache_init(const dspark_cache* c, const dspark_cache_tables* t, void* stream);
+
+/* Forks: slot dst[i] gets the tokens of slot src[i] by sharing its pages (one
+ * more reference each; nothing is copied).  status[i] = 0, or 1 for a pair that is
+ * refused and changes nothing: an index outside [0, slots), a dst that holds
+ * pages, a dst that an earlier pair names, or a src that is any pair's dst.
+ * src, dst, status [n] int32, 1 <= n <= 4096. */
+int dspark_cache_fork(const dspark_cache* c, const dspark_cache_tables* t, int32_t n,
+                      const int32_t* src, const int32_t* dst, int32_t* status, void* stream);
+
+/* Pages for add[s] more tokens of every slot (add[s] <= 0: the slot is left
+ * alone; lens does not change).  A slot whose next token falls into a page that it
+ * shares gets a page of its own for it: cow_src[s], cow_dst[s] name the copy to
+ * make (dspark_cache_copy_pages, before the next reserve), -1 for none; when
+ * every sharer of the page is served in the call, the lowest slot keeps it.
+ * status[s]: 0; 1 out of pages (slots are served in order until one does not
+ * fit; it and the later ones that need pages get none); 2 the table row is too
+ * short (the slot gets none).  A slot with a status other than 0 must not
+ * append.  add, status, cow_src, cow_dst [slots] int32. */
+int dspark_cache_reserve(const dspark_cache* c, const dspark_cache_tables* t, const int32_t* add,
+                         int32_t* status, int32_t* cow_src, int32_t* cow_dst, void* stream);
+
+/* Ends a round: lens[s] += keep[s] + plus, clamped to [0, held * page_size], and
+ * the pages behind the new length are released (a negative sum rolls back).
+ * keep[s] = INT32_MIN leaves the slot alone.  After dspark_verify, keep =
+ * n_accept with plus = 1 keeps the anchor and the accepted drafts; the last
+ * emitted token is the next round's anchor.  keep [slots] int32. */
+int dspark_cache_commit(const dspark_cache* c, const dspark_cache_tables* t, const int32_t* keep,
+                        int32_t plus, void* stream);
+
+/* Releases every page of the listed slots and empties them.  An index outside
+ * [0, slots) is skipped; one listed twice is released once.  slots [n] int32,
+ * 1 <= n <= 4096. */
+int dspark_cache_free(const dspark_cache* c, const dspark_cache_tables* t, int32_t n,
+                      const int32_t* slots, void* stream);
+
+/* Moves the used pages to the front of the pool: with u pages in use, page
+ * src[i] >= u goes to the free page dst[i] < u, both ascending, i < n_moves[0]
+ * (-1 behind).  Writes the tables after the moves to `out` (which may be t, or
+ * other tables while a round still reads t); the caller then copies the pages
+ * (dspark_cache_copy_pages with count = n_moves).  The sources keep their
+ * contents.  src, dst [pages] int32, n_moves [1] int32.
+ * ws: dspark_cache_compact_workspace_bytes(c) bytes, 256-byte aligned. */
+size_t dspark_cache_compact_workspace_bytes(const dspark_cache* c);
+int dspark_cache_compact(const dspark_cache* c, const dspark_cache_tables* t,
+                         const dspark_cache_tables* out, int32_t* src, int32_t* dst,
+                         int32_t* n_moves, void* ws, size_t ws_bytes, void* stream);
+
+/* Copies page src[i] to page dst[i] in K and V of every layer, i < n, or i <
+ * min(n, count[0]) if count (device) is given.  Pairs with an index outside
+ * [0, pages) are skipped.  No page may be two pairs' dst, or one's dst and
+ * another's src.  src, dst [n] int32, 1 <= n <= 2^24. */
+int dspark_cache_copy_pages(const dspark_cache* c, void* K, void* V, int32_t n, const int32_t* src,
+                            const int32_t* dst, const int32_t* count, void* stream);
+
+/* Writes a chunk's keys and values into one layer's pages.  Tokens are
+ * flattened over the slots: slot s has rows offsets[s] .. offsets[s + 1] - 1 of
+ * k and v [N, kv_heads, head_dim], row i at position lens[s] + i - offsets[s];
+ * rows behind offsets[slots] belong to nobody.  The pages have to be reserved;
+ * a token without one is dropped.  offsets [slots + 1] int32, from 0, not
+ * falling.  Limits: 1 <= N <= 2^22. */
+int dspark_cache_append(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, void* K,
+                        void* V, int32_t N, const void* k, const void* v, const int32_t* offsets,
+                        void* stream);
+
+/* Attention of a chunk of new tokens per slot over the cache (after
+ * dspark_cache_append wrote the chunk): row i of slot s, head h, sees the
+ * positions p <= lens[s] + i - offsets[s] that are on a page of the slot,
+ *   out[i, h] = sum_p softmax_p(scale q[i, h] . k[p, g]) v[p, g], g = h / (heads / kv_heads),
+ * 0 if there is none.  q, out [N, heads, head_dim] dtype, flattened as in
+ * dspark_cache_append; rows behind offsets[slots] are left as they were.  A
+ * slot may have no rows.  Scores, sums and outputs accumulate in binary32 (bf16:
+ * the weights are rounded to bf16 for the product with v; one rounding at the
+ * end).  Keys and values that any of the chunk's tokens sees must be finite; what
+ * else the pages hold does not matter.
+ * max_chunk: the longest chunk expected, >= 1; it chooses the tiling only, any
+ * chunk is computed.  scale > 0.  heads a multiple of kv_heads, N * heads <= 2^30.
+ * ws: dspark_attend_workspace_bytes(c, N, heads) bytes, 256-byte aligned. */
+size_t dspark_attend_workspace_bytes(const dspark_cache* c, int32_t N, int32_t heads);
+int dspark_attend(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, const void* K,
+                  const void* V, int32_t N, int32_t heads, const void* q, const int32_t* offsets,
+                  float scale, int32_t max_chunk, void* out, void* ws, size_t ws_bytes,
+                  void* stream);
+
 /* Device-side check of the values the host cannot see, the preconditions
  * above (a debugging aid, off the hot path: one pass over every tensor given).
  * counts: int64 [6] in device memory, overwritten with the number of
