@@ -33,7 +33,7 @@ HIPCC_FLAGS = [
 # before any difference of infinities is formed); without NaNs to honour, the
 # compiler drops the NaN-quieting v_max it otherwise puts in front of every
 # maximum of matrix-core results.
-EXTRA_FLAGS = {"bias_pass.hip": ["-fno-honor-nans"]}
+EXTRA_FLAGS = {"bias_pass.hip": ["-fno-honor-nans"], "attend.hip": ["-fno-honor-nans"]}
 
 
 def _hipcc() -> str:

@@ -29,8 +29,8 @@ namespace dspark {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = 4;
+constexpr int kPlanThreads = 256;  // the workgroup's first threads work out the plan
+constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kKeys = 32;      // keys per step of a wave
 constexpr int kMinTiles = 4;   // shortest range of an item, in steps
 constexpr float kRise = 8.f;   // the running maximum may lag by this (in log2)
@@ -122,22 +122,23 @@ __device__ __forceinline__ int splits_of(const SlotWork& w, int range) {
   return w.row_tiles == 0 ? 0 : max(1, (w.key_tiles + range - 1) / range);
 }
 
-// Items before each thread's run of slots (thread t: slots [t per, t per + per)), the
-// items of split slots apart.
+// Items before each plan thread's run of slots (thread t: slots [t per, t per +
+// per)), the items of split slots apart.
 struct Plan {
-  int before[kThreads + 1];
-  int split_before[kThreads + 1];
-  int64_t sum[kWaves];
+  int before[kPlanThreads + 1];
+  int split_before[kPlanThreads + 1];
+  int64_t sum[kPlanWaves];
   int range;  // key tiles per item
   int per;
 };
 
-// kGroups: count the (slot, kv head, row tile) groups of split slots instead of all items.
+// kGroups: count the (slot, kv head, row tile) groups of split slots instead of all
+// items.  At least kPlanThreads threads.
 template <bool kGroups>
 __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& plan) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int per = (a.c.slots + kThreads - 1) / kThreads;
-  const int s0 = tid * per, s1 = min(s0 + per, a.c.slots);
+  const int per = (a.c.slots + kPlanThreads - 1) / kPlanThreads;
+  const int s0 = tid < kPlanThreads ? tid * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
   int64_t work = 0;
   for (int s = s0; s < s1; ++s) {
     const SlotWork w = slot_work(a, s, rows);
@@ -145,9 +146,12 @@ __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& p
   }
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) work += __shfl_xor(work, off, 64);
-  if (lane == 0) plan.sum[wave] = work;
+  if (lane == 0 && wave < kPlanWaves) plan.sum[wave] = work;
   __syncthreads();
-  work = (plan.sum[0] + plan.sum[1] + plan.sum[2] + plan.sum[3]) * a.c.kv_heads;
+  work = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) work += plan.sum[w];
+  work *= a.c.kv_heads;
   const int64_t r = (work + a.target - 1) / a.target;
   const int range = (int)(r > kMinTiles ? r : kMinTiles);
   int items = 0, split = 0;
@@ -171,17 +175,19 @@ __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& p
     }
   }
   __syncthreads();
-  if (lane == 63) plan.sum[wave] = ((int64_t)y << 32) | (uint32_t)x;
+  if (lane == 63 && wave < kPlanWaves) plan.sum[wave] = ((int64_t)y << 32) | (uint32_t)x;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < kPlanWaves; ++w) {
     if (w < wave) {
       x += (int)(uint32_t)plan.sum[w];
       y += (int)(plan.sum[w] >> 32);
     }
   }
-  plan.before[tid + 1] = x;
-  plan.split_before[tid + 1] = y;
+  if (tid < kPlanThreads) {
+    plan.before[tid + 1] = x;
+    plan.split_before[tid + 1] = y;
+  }
   if (tid == 0) {
     plan.before[0] = 0;
     plan.split_before[0] = 0;
@@ -200,7 +206,7 @@ struct Item {
 // Item `id` of the plan: the thread run that holds it by bisection, then the slot in it.
 template <bool kGroups>
 __device__ __forceinline__ Item find_item(const AttendArgs& a, int rows, const Plan& plan, int id) {
-  int lo = 0, hi = kThreads - 1;
+  int lo = 0, hi = kPlanThreads - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (plan.before[mid] <= id) lo = mid;
@@ -246,8 +252,10 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* to, f32x4 v) {
   *reinterpret_cast<bf16x4*>(to) = b;
 }
 
-// One item.  NQ 16-row blocks per wave; D dimensions.
-template <typename E, int D, int NQ>
+// One item.  D dimensions; RW x KW waves: RW row groups of NQ 16-row blocks each, KW
+// parts of the key range.
+// kHalf: pages of 16 tokens under bf16, where one operand spans two pages.
+template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
 __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it, int range,
                                             float* sh_ml, float* sh_o) {
   typedef Ops<E> Op;
@@ -256,8 +264,12 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   constexpr int kSteps = D / (4 * kE);  // K operands per 16 keys
   constexpr int kDT = D / 16;           // 16-dimension blocks of the output
   constexpr int kVC = Op::kVChunks;
-  constexpr int kRows = 16 * NQ;
+  constexpr int kWaveRows = 16 * NQ;
+  constexpr int kRows = kWaveRows * RW;
+  constexpr int kThreads = 64 * RW * KW;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int part = wave / RW;                 // the wave's part of the keys
+  const int wrow = (wave % RW) * kWaveRows;   // its first row in the tile
   const int n = lane & 15, quad = lane >> 4;
   const int G = a.group, H = a.c.kv_heads;
   const int row0 = it.tile * kRows, rows = it.w.chunk * G;
@@ -268,7 +280,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   int limit[NQ];  // keys that the lane's row sees
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int row = row0 + 16 * i + n;
+    const int row = row0 + wrow + 16 * i + n;
     const bool live = row < rows;
     const int token = live ? row / G : 0;
     const E* p = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D;
@@ -281,11 +293,11 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   const int last_row = min(row0 + kRows, rows) - 1;
   const int seen = min(it.w.len + last_row / G + 1, it.w.keys);
   const int common = min(it.w.len + row0 / G + 1, it.w.keys);
-  // the wave's quarter of the item's range, in steps of kKeys keys
+  // the wave's part of the item's range, in steps of kKeys keys
   const int t_first = it.split * range;
   const int t_end = min(t_first + range, (seen + kKeys - 1) / kKeys);
   const int count = max(0, t_end - t_first);
-  const int t0 = t_first + count * wave / kWaves, t1 = t_first + count * (wave + 1) / kWaves;
+  const int t0 = t_first + count * part / KW, t1 = t_first + count * (part + 1) / KW;
 
   f32x4 o[NQ][kDT];
   float m[NQ], l[NQ];
@@ -322,28 +334,45 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
     pa = __builtin_amdgcn_readlane(ids, ca - col0);
     pb = __builtin_amdgcn_readlane(ids, cb - col0);
   };
+  // Operand addresses: a wave-uniform base (page, step, layer) and a lane's 32-bit
+  // offset that stays the same through the pass.
+  const uint32_t k_lane = (uint32_t)(((Op::key_of(0, n) & (page - 1)) + quad * page) * 16);
+  const uint32_t v_lane = (uint32_t)(((Op::vkey_of(0, quad) & (page - 1)) / kE * D + n) * 16);
+  const int64_t page_size_bytes = page_elems * (int64_t)sizeof(E);
+  const char* Kb = reinterpret_cast<const char*>(Kh);
+  const char* Vb = reinterpret_cast<const char*>(Vh);
   auto load_k = [&](int t, int pa, int pb, Chunk (&k)[2][kSteps]) {
+    const char* ba = Kb + max(pa, 0) * page_size_bytes;
+    const char* bb = Kb + max(pb, 0) * page_size_bytes;
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int key = Op::key_of(u, n);
-      const int p = max(key < 16 ? pa : pb, 0);
-      const int at = (t * kKeys + key) & (page - 1);
-      const E* base = Kh + p * page_elems + (int64_t)at * kE;
+      // bf16: the 32 keys of a step lie on one page (kHalf: 16 on each of two);
+      // f32: block u's 16 keys do
+      const int first = sizeof(E) == 2 ? t * kKeys : t * kKeys + 16 * u;
+      const int at = kHalf ? 4 * u : (first & (page - 1)) + (sizeof(E) == 2 ? 4 * u : 0);
+      const char* base = sizeof(E) == 2 || u == 0 ? ba : bb;
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s)
-        k[u][s] = *reinterpret_cast<const Chunk*>(base + (int64_t)(4 * s + quad) * page * kE);
+      for (int s = 0; s < kSteps; ++s) {
+        const int64_t to = (int64_t)(4 * s * page + at) * 16;
+        if constexpr (kHalf) k[u][s] = *reinterpret_cast<const Chunk*>((n < 8 ? ba : bb) + to + k_lane);
+        else k[u][s] = *reinterpret_cast<const Chunk*>(base + to + k_lane);
+      }
     }
   };
   auto load_v = [&](int t, int pa, int pb, Chunk (&v)[kVC][kDT]) {
+    const char* ba = Vb + max(pa, 0) * page_size_bytes;
+    const char* bb = Vb + max(pb, 0) * page_size_bytes;
 #pragma unroll
     for (int u = 0; u < kVC; ++u) {
-      const int key = Op::vkey_of(u, quad);
-      const int p = max(key < 16 ? pa : pb, 0);
-      const int at = (t * kKeys + key) & (page - 1);
-      const E* base = Vh + p * page_elems + (int64_t)(at / kE) * D * kE;
+      const int first = t * kKeys + 16 * u;
+      const int64_t at = kHalf ? 0 : (int64_t)((first & (page - 1)) / kE) * D * 16;
+      const char* base = u == 0 ? ba : bb;
 #pragma unroll
-      for (int d = 0; d < kDT; ++d)
-        v[u][d] = *reinterpret_cast<const Chunk*>(base + (16 * d + n) * kE);
+      for (int d = 0; d < kDT; ++d) {
+        const int64_t to = at + 16 * 16 * d;
+        if constexpr (kHalf) v[u][d] = *reinterpret_cast<const Chunk*>((quad < 2 ? ba : bb) + to + v_lane);
+        else v[u][d] = *reinterpret_cast<const Chunk*>(base + to + v_lane);
+      }
     }
   };
 
@@ -355,47 +384,32 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   }
   for (int t = t0; t < t1; ++t) {
     load_v(t, pa, pb, v);
-    f32x4 s[NQ][2];
+    const int ma = pa, mb = pb;
+    // keys that some row does not see: behind its position, or on no page
+    const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0;
+    Chunk p[NQ][kVC];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+    for (int i = 0; i < NQ; ++i) {
+      f32x4 s[2];
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kSteps; ++c) acc = Op::score(k[u][c], qo[i][c], acc);
-        s[i][u] = acc;
+        s[u] = acc;
       }
-    const int ma = pa, mb = pb;
-    if (t + 1 < t1) {
-      pages_of(t + 1, pa, pb);
-      load_k(t + 1, pa, pb, k);
-    }
-    // keys that some row does not see: behind its position, or on no page
-    if ((t + 1) * kKeys > common || ma < 0 || mb < 0) {
-#pragma unroll
-      for (int i = 0; i < NQ; ++i)
+      if (partial) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = Op::skey_of(u, j, quad);
             const bool there = t * kKeys + key < limit[i] && (key < 16 ? ma : mb) >= 0;
-            s[i][u][j] = there ? s[i][u][j] : -INFINITY;
+            s[u][j] = there ? s[u][j] : -INFINITY;
           }
-      // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN
-#pragma unroll
-      for (int u = 0; u < kVC; ++u) {
-        const int key = Op::vkey_of(u, quad);
-        const int keep = (key < 16 ? ma : mb) >= 0 ? min(max(seen - (t * kKeys + key), 0), kE) : 0;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) v[u][d] = Op::keep(v[u][d], keep);
       }
-    }
-    Chunk p[NQ][kVC];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      float mx = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                       fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3])));
+      float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
+                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
       mx *= a.scale_log2;
       // the maximum moves only when some row has passed it by 2^kRise: until then
       // the sums grow past 1, far from binary32's end, and nothing is rescaled
@@ -413,12 +427,26 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
       float e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        e[j] = __builtin_amdgcn_exp2f(fmaf(s[i][j >> 2][j & 3], a.scale_log2, -ref));
+        e[j] = __builtin_amdgcn_exp2f(fmaf(s[j >> 2][j & 3], a.scale_log2, -ref));
       l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if constexpr (sizeof(E) == 2) p[i][0][j] = (__bf16)e[j];
         else p[i][j >> 2][j & 3] = e[j];
+      }
+    }
+    if (t + 1 < t1) {
+      pages_of(t + 1, pa, pb);
+      load_k(t + 1, pa, pb, k);
+    }
+    if (partial) {
+      // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN
+#pragma unroll
+      for (int u = 0; u < kVC; ++u) {
+        const int key = Op::vkey_of(u, quad);
+        const int keep = (key < 16 ? ma : mb) >= 0 ? min(max(seen - (t * kKeys + key), 0), kE) : 0;
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) v[u][d] = Op::keep(v[u][d], keep);
       }
     }
 #pragma unroll
@@ -429,14 +457,14 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
         for (int i = 0; i < NQ; ++i) o[i][d] = Op::score(v[u][d], p[i][u], o[i][d]);
   }
 
-  // ---- the four waves' sums joined ----
+  // ---- the sums of the key parts joined ----
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     l[i] += __shfl_xor(l[i], 16, 64);
     l[i] += __shfl_xor(l[i], 32, 64);
     if (quad == 0) {
-      sh_ml[(wave * kRows + 16 * i + n) * 2] = m[i];
-      sh_ml[(wave * kRows + 16 * i + n) * 2 + 1] = l[i];
+      sh_ml[(part * kRows + wrow + 16 * i + n) * 2] = m[i];
+      sh_ml[(part * kRows + wrow + 16 * i + n) * 2 + 1] = l[i];
     }
   }
   __syncthreads();
@@ -444,7 +472,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   for (int i = 0; i < NQ; ++i) {
     float mn = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + 16 * i + n) * 2]);
+    for (int w = 0; w < KW; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + wrow + 16 * i + n) * 2]);
     const float f = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] - mn);
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[i][d] *= f;
@@ -459,7 +487,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
       for (int d = 0; d < kPart / 16; ++d)
-        *reinterpret_cast<f32x4*>(sh_o + (wave * kRows + 16 * i + n) * kLd + 16 * d + 4 * quad) =
+        *reinterpret_cast<f32x4*>(sh_o + (part * kRows + wrow + 16 * i + n) * kLd + 16 * d + 4 * quad) =
             o[i][d0 / 16 + d];
     __syncthreads();
     for (int x = threadIdx.x; x < kRows * (kPart / 4); x += kThreads) {
@@ -468,13 +496,13 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
       if (row < rows) {
         f32x4 sum = *reinterpret_cast<const f32x4*>(sh_o + r * kLd + 4 * c);
 #pragma unroll
-        for (int w = 1; w < kWaves; ++w)
+        for (int w = 1; w < KW; ++w)
           sum += *reinterpret_cast<const f32x4*>(sh_o + (w * kRows + r) * kLd + 4 * c);
         float mn = -INFINITY, ls = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + r) * 2]);
+        for (int w = 0; w < KW; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + r) * 2]);
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < KW; ++w) {
           const float mw = sh_ml[(w * kRows + r) * 2];
           if (mw != -INFINITY) ls += sh_ml[(w * kRows + r) * 2 + 1] * __builtin_amdgcn_exp2f(mw - mn);
         }
@@ -496,38 +524,45 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   }
 }
 
-template <typename E, int D, int NQ>
-__global__ __launch_bounds__(kThreads, NQ * D <= 256 ? 2 : 1) void k_attend(AttendArgs a) {
-  constexpr int kRows = 16 * NQ;
+// Waves per SIMD that the registers of NQ row blocks of D dimensions leave room for.
+template <typename E, int D, int NQ, int RW, int KW>
+struct Shape {
+  static constexpr int waves = NQ * D <= 384 ? 2 : 1;
+  static constexpr int per_cu = waves * 4 / (RW * KW) > 0 ? waves * 4 / (RW * KW) : 1;
+};
+
+template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
+__global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) void k_attend(AttendArgs a) {
+  constexpr int kRows = 16 * NQ * RW;
   __shared__ Plan plan;
-  __shared__ float sh_ml[kWaves * kRows * 2];
-  __shared__ __align__(16) float sh_o[kWaves * kRows * 36];
+  __shared__ float sh_ml[KW * kRows * 2];
+  __shared__ __align__(16) float sh_o[KW * kRows * 36];
   make_plan<false>(a, kRows, plan);
-  const int total = plan.before[kThreads];
+  const int total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
   // items, so that row tiles that read the same keys share its L2.
   const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3, step = gridDim.x >> 3;
   const int first = (int)((int64_t)total * xcd / 8), last = (int)((int64_t)total * (xcd + 1) / 8);
   for (int id = first + idx; id < last; id += step) {
     const Item it = find_item<false>(a, kRows, plan, id);
-    attend_item<E, D, NQ>(a, it, plan.range, sh_ml, sh_o);
+    attend_item<E, D, NQ, RW, KW, kHalf>(a, it, plan.range, sh_ml, sh_o);
   }
 }
 
 // Joins the key ranges of split slots: a workgroup per (slot, kv head, row tile), D / 4
 // threads per row.
 template <typename E>
-__global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, int rows_per_tile) {
+__global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int rows_per_tile) {
   __shared__ Plan plan;
   make_plan<true>(a, rows_per_tile, plan);
-  const int total = plan.before[kThreads];
+  const int total = plan.before[kPlanThreads];
   const int D = a.c.head_dim, G = a.group;
   const int per_row = D / 4;
   for (int id = blockIdx.x; id < total; id += gridDim.x) {
     const Item it = find_item<true>(a, rows_per_tile, plan, id);
     const int row0 = it.tile * rows_per_tile;
     const int rows = min(rows_per_tile, it.w.chunk * G - row0);
-    for (int x = threadIdx.x; x < rows * per_row; x += kThreads) {
+    for (int x = threadIdx.x; x < rows * per_row; x += kPlanThreads) {
       const int r = x / per_row, c = x % per_row;
       float mn = -INFINITY;
       for (int i = 0; i < it.splits; ++i)
@@ -550,55 +585,79 @@ __global__ __launch_bounds__(kThreads) void k_attend_join(AttendArgs a, int rows
   }
 }
 
-template <typename E, int D, int NQ>
-void start(const AttendArgs& a, int grid, hipStream_t stream) {
-  hipLaunchKernelGGL((k_attend<E, D, NQ>), dim3(grid), dim3(kThreads), 0, stream, a);
+template <typename E, int D, int NQ, int RW, int KW>
+void start(const AttendArgs& a, hipStream_t stream) {
+  const int grid = 256 * Shape<E, D, NQ, RW, KW>::per_cu;
+  if (sizeof(E) == 2 && a.c.page_shift == 4)
+    hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, sizeof(E) == 2>), dim3(grid), dim3(64 * RW * KW), 0,
+                       stream, a);
+  else
+    hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, false>), dim3(grid), dim3(64 * RW * KW), 0, stream, a);
+}
+
+// Tiles in use: rows, then the row groups of 16-row blocks.
+template <typename E, int D>
+bool start_rows(int rows, const AttendArgs& a, hipStream_t stream) {
+  if constexpr (sizeof(E) == 2 && D <= 128) {
+    switch (rows) {
+      case 16: start<E, D, 1, 1, 4>(a, stream); return true;
+      case 32: start<E, D, 2, 1, 4>(a, stream); return true;
+      case 48: start<E, D, 3, 1, 4>(a, stream); return true;
+      case 64: start<E, D, 2, 2, 4>(a, stream); return true;
+      case 96: start<E, D, 3, 2, 4>(a, stream); return true;
+    }
+  } else if constexpr (sizeof(E) == 2) {
+    switch (rows) {
+      case 16: start<E, D, 1, 1, 4>(a, stream); return true;
+      case 32: start<E, D, 1, 2, 4>(a, stream); return true;
+    }
+  } else {
+    switch (rows) {
+      case 16: start<E, D, 1, 1, 4>(a, stream); return true;
+      case 32: start<E, D, 1, 2, 4>(a, stream); return true;
+    }
+  }
+  return false;
 }
 
 }  // namespace
 
 // The largest tile: what the registers hold (the output's accumulators take
 // D / 4 registers per 16 rows, the queries' operands half of that).
-int attend_max_rows(bool bf16, int head_dim) {
-  return 16 * (bf16 ? (head_dim == 256 ? 2 : 5) : (head_dim == 256 ? 1 : 2));
-}
+int attend_max_rows(bool bf16, int head_dim) { return bf16 && head_dim <= 128 ? 96 : 32; }
 
-// Rows (token, head) of a tile: as many 16-row blocks as the longest chunk needs,
-// spread evenly over its tiles.
+// Rows (token, head) of a tile: as many as the longest chunk needs, spread evenly
+// over its tiles.
 int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
   const int most = attend_max_rows(bf16, head_dim);
   const int64_t rows = (int64_t)max_chunk * group;
   const int64_t tiles = (rows + most - 1) / most;
-  const int need = (int)(((rows + tiles - 1) / tiles + 15) / 16);
-  const int sizes[4] = {1, 2, 3, 5};
+  const int need = (int)((rows + tiles - 1) / tiles);
+  const int sizes[5] = {16, 32, 48, 64, 96};
   for (int n : sizes)
-    if (n >= need) return 16 * n;
+    if (n >= need && n <= most) return n;
   return most;
 }
 
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream) {
   {
     TimingScope t("attend", stream);
-    const int grid = 512;
-    const int D = a.c.head_dim, nq = rows / 16;
-#define ATTEND(E, DIM, N) \
-  if (D == DIM && nq == N) start<E, DIM, N>(a, grid, stream); else
-    if (bf16) {
-      ATTEND(uint16_t, 64, 1) ATTEND(uint16_t, 64, 2) ATTEND(uint16_t, 64, 3) ATTEND(uint16_t, 64, 5)
-      ATTEND(uint16_t, 128, 1) ATTEND(uint16_t, 128, 2) ATTEND(uint16_t, 128, 3) ATTEND(uint16_t, 128, 5)
-      ATTEND(uint16_t, 256, 1) ATTEND(uint16_t, 256, 2) return hipErrorInvalidValue;
-    } else {
-      ATTEND(float, 64, 1) ATTEND(float, 64, 2) ATTEND(float, 128, 1) ATTEND(float, 128, 2)
-      ATTEND(float, 256, 1) return hipErrorInvalidValue;
-    }
-#undef ATTEND
+    const int D = a.c.head_dim;
+    const bool started =
+        bf16 ? (D == 64 ? start_rows<uint16_t, 64>(rows, a, stream)
+                        : (D == 128 ? start_rows<uint16_t, 128>(rows, a, stream)
+                                    : start_rows<uint16_t, 256>(rows, a, stream)))
+             : (D == 64 ? start_rows<float, 64>(rows, a, stream)
+                        : (D == 128 ? start_rows<float, 128>(rows, a, stream)
+                                    : start_rows<float, 256>(rows, a, stream)));
+    if (!started) return hipErrorInvalidValue;
   }
   {
     TimingScope t("attend_join", stream);
     if (bf16)
-      hipLaunchKernelGGL(k_attend_join<uint16_t>, dim3(512), dim3(kThreads), 0, stream, a, rows);
+      hipLaunchKernelGGL(k_attend_join<uint16_t>, dim3(512), dim3(kPlanThreads), 0, stream, a, rows);
     else
-      hipLaunchKernelGGL(k_attend_join<float>, dim3(512), dim3(kThreads), 0, stream, a, rows);
+      hipLaunchKernelGGL(k_attend_join<float>, dim3(512), dim3(kPlanThreads), 0, stream, a, rows);
   }
   return hipGetLastError();
 }
