@@ -316,21 +316,23 @@ void* layer_of(const dspark_cache* c, void* pool, int layer) {
 }
 
 struct AttendLayout {
-  int rows, target;
+  int rows, grid;
   size_t o, ml, bytes;
 };
 
-// Records of the items of split slots: a slot of n key tiles cut to ranges of r < n
-// has ceil(n / r) <= 2 n / r items per row tile and head, and r is at least the
-// batch's tiles over the target, so that there are at most 2 * target of them.
+// Records of the groups that spans cut: two per span at most.
 AttendLayout attend_layout(const dspark_cache* c, int N, int heads, int max_chunk) {
   AttendLayout L = {};
-  const int longest = max_chunk < N ? max_chunk : N;
   const bool bf16 = c->dtype == DSPARK_BF16;
+  const int longest = max_chunk < N ? max_chunk : N;
   L.rows = attend_rows(bf16, c->head_dim, heads / c->kv_heads, longest);
-  L.target = kAttendTarget;
-  // sized for the largest tile, whatever chunk a call names
-  const size_t records = (size_t)2 * L.target * attend_max_rows(bf16, c->head_dim);
+  L.grid = attend_grid(c->head_dim, L.rows);
+  // sized for any tile, whatever chunk a call names
+  size_t records = 0;
+  for (int rows = 16; rows <= attend_max_rows(bf16, c->head_dim); rows += 16) {
+    const size_t n = (size_t)2 * attend_grid(c->head_dim, rows) * rows;
+    records = records > n ? records : n;
+  }
   Carver v;
   L.o = v.take(records * c->head_dim * sizeof(float));
   L.ml = v.take(records * 2 * sizeof(float));
@@ -1101,7 +1103,7 @@ __attribute__((visibility("default"))) int dspark_attend(
   a.V = layer_of(c, const_cast<void*>(V), layer);
   a.offsets = offsets;
   a.out = out;
-  a.target = L.target;
+  a.grid = L.grid;
   a.part_o = at<float>(ws, L.o);
   a.part_ml = at<float>(ws, L.ml);
   hipError_t e = launch_attend(c->dtype == DSPARK_BF16, L.rows, a, (hipStream_t)stream);

@@ -32,7 +32,7 @@ namespace {
 constexpr int kPlanThreads = 256;  // the workgroup's first threads work out the plan
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kKeys = 32;      // keys per step of a wave
-constexpr int kMinTiles = 4;   // shortest range of an item, in steps
+constexpr int kMinSpan = 4;    // shortest span of a workgroup, in steps
 constexpr float kRise = 8.f;   // the running maximum may lag by this (in log2)
 
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -96,144 +96,136 @@ struct Ops<float> {
   }
 };
 
-// ---- the batch's work items -----------------------------------------------------
+// ---- the batch's work, cut into equal spans -----------------------------------------
+// A group is one (slot, kv head, row tile) and has as many units as its rows see key
+// steps.  Row tile i of a slot is put together with the slot's i-th last one: what a
+// chunk's later tokens see more than its earlier ones evens out, so that every pair
+// has `pair_units` units (a bound; a pair may end before it) and a slot's work has a
+// closed form.  All units of the batch lie on a line in the order slot, head, pair; a
+// workgroup takes a span of it, a group that spans cut is joined afterwards.
 struct SlotWork {
-  int o0, chunk;     // first token row and tokens of the chunk
-  int len;           // cached tokens before it
-  int keys;          // keys that exist: len + chunk, at most the table's width
-  int row_tiles, key_tiles;
+  int o0, chunk;  // first token row and tokens of the chunk
+  int len;        // cached tokens before it
+  int keys;       // keys that exist: len + chunk, at most the table's width
+  int tiles, pairs;
+  int pair_units;
+  int64_t units;
 };
+
+// Key steps that the rows up to the end of row tile i see.
+__device__ __forceinline__ int tile_units(const SlotWork& w, int group, int rows, int i) {
+  const int last = min((i + 1) * rows, w.chunk * group) - 1;
+  return (min(w.len + last / group + 1, w.keys) + kKeys - 1) / kKeys;
+}
 
 __device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int rows) {
   SlotWork w;
   w.o0 = min(max(a.offsets[s], 0), a.N);
   const int o1 = min(max(a.offsets[s + 1], w.o0), a.N);
   w.chunk = o1 - w.o0;
-  w.len = max(a.c.t.lens[s], 0);
   const int64_t width = (int64_t)a.c.max_pages << a.c.page_shift;
+  const int64_t len = max(a.c.t.lens[s], 0);
+  w.len = (int)(len < width ? len : width);
   const int64_t keys = (int64_t)w.len + w.chunk;
   w.keys = (int)(keys < width ? keys : width);
-  w.row_tiles = (int)(((int64_t)w.chunk * a.group + rows - 1) / rows);
-  w.key_tiles = (w.keys + kKeys - 1) / kKeys;
+  w.tiles = (w.chunk * a.group + rows - 1) / rows;
+  w.pairs = (w.tiles + 1) >> 1;
+  w.pair_units = 0;
+  w.units = 0;
+  if (w.tiles > 0) {
+    const int last = tile_units(w, a.group, rows, w.tiles - 1);
+    // one or two tiles: exact; more: two steps' rounding at most above the outer pair
+    w.pair_units = w.tiles == 1 ? last
+                                : tile_units(w, a.group, rows, 0) + last + (w.tiles == 2 ? 0 : 2);
+    w.units = (int64_t)w.pair_units * w.pairs * a.c.kv_heads;
+  }
   return w;
 }
 
-__device__ __forceinline__ int splits_of(const SlotWork& w, int range) {
-  return w.row_tiles == 0 ? 0 : max(1, (w.key_tiles + range - 1) / range);
-}
-
-// Items before each plan thread's run of slots (thread t: slots [t per, t per +
-// per)), the items of split slots apart.
+// Units before each plan thread's run of slots (thread t: slots [t per, t per + per)).
 struct Plan {
-  int before[kPlanThreads + 1];
-  int split_before[kPlanThreads + 1];
+  int64_t before[kPlanThreads + 1];
   int64_t sum[kPlanWaves];
-  int range;  // key tiles per item
+  int64_t span;
+  int spans;
   int per;
 };
 
-// kGroups: count the (slot, kv head, row tile) groups of split slots instead of all
-// items.  At least kPlanThreads threads.
-template <bool kGroups>
+// At least kPlanThreads threads.
 __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& plan) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.c.slots + kPlanThreads - 1) / kPlanThreads;
   const int s0 = tid < kPlanThreads ? tid * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
-  int64_t work = 0;
-  for (int s = s0; s < s1; ++s) {
-    const SlotWork w = slot_work(a, s, rows);
-    work += (int64_t)w.row_tiles * w.key_tiles;
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) work += __shfl_xor(work, off, 64);
-  if (lane == 0 && wave < kPlanWaves) plan.sum[wave] = work;
-  __syncthreads();
-  work = 0;
-#pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) work += plan.sum[w];
-  work *= a.c.kv_heads;
-  const int64_t r = (work + a.target - 1) / a.target;
-  const int range = (int)(r > kMinTiles ? r : kMinTiles);
-  int items = 0, split = 0;
-  for (int s = s0; s < s1; ++s) {
-    const SlotWork w = slot_work(a, s, rows);
-    const int ns = splits_of(w, range);
-    const int n = ns * w.row_tiles * a.c.kv_heads;
-    if (ns > 1) {
-      split += n;
-      if (kGroups) items += w.row_tiles * a.c.kv_heads;
-    }
-    if (!kGroups) items += n;
-  }
-  int x = items, y = split;
+  int64_t x = 0;
+  for (int s = s0; s < s1; ++s) x += slot_work(a, s, rows).units;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
-    const int px = __shfl_up(x, off, 64), py = __shfl_up(y, off, 64);
-    if (lane >= off) {
-      x += px;
-      y += py;
-    }
+    const int64_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
   }
+  if (lane == 63 && wave < kPlanWaves) plan.sum[wave] = x;
   __syncthreads();
-  if (lane == 63 && wave < kPlanWaves) plan.sum[wave] = ((int64_t)y << 32) | (uint32_t)x;
-  __syncthreads();
+  int64_t total = 0;
 #pragma unroll
   for (int w = 0; w < kPlanWaves; ++w) {
-    if (w < wave) {
-      x += (int)(uint32_t)plan.sum[w];
-      y += (int)(plan.sum[w] >> 32);
-    }
+    if (w < wave) x += plan.sum[w];
+    total += plan.sum[w];
   }
-  if (tid < kPlanThreads) {
-    plan.before[tid + 1] = x;
-    plan.split_before[tid + 1] = y;
-  }
+  if (tid < kPlanThreads) plan.before[tid + 1] = x;
   if (tid == 0) {
+    int64_t span = (total + a.grid - 1) / a.grid;
+    span = span > kMinSpan ? span : kMinSpan;
     plan.before[0] = 0;
-    plan.split_before[0] = 0;
-    plan.range = range;
+    plan.span = span;
+    plan.spans = (int)((total + span - 1) / span);
     plan.per = per;
   }
   __syncthreads();
 }
 
-struct Item {
+// The group that unit x lies in.
+struct Group {
   SlotWork w;
-  int slot, head, tile, split, splits;
-  int part;  // first partial record of the (head, tile) group; split i has part + i
+  int slot, head, tile;
+  int units;      // of the group
+  int64_t start;  // its first unit on the line
+  int64_t next;   // units == 0 (x lies behind its pair's end): the next pair's first unit
 };
 
-// Item `id` of the plan: the thread run that holds it by bisection, then the slot in it.
-template <bool kGroups>
-__device__ __forceinline__ Item find_item(const AttendArgs& a, int rows, const Plan& plan, int id) {
+__device__ __forceinline__ Group find_group(const AttendArgs& a, int rows, const Plan& plan,
+                                            int64_t x) {
   int lo = 0, hi = kPlanThreads - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (plan.before[mid] <= id) lo = mid;
+    if (plan.before[mid] <= x) lo = mid;
     else hi = mid - 1;
   }
-  Item it;
-  int left = id - plan.before[lo], part = plan.split_before[lo];
+  Group g;
+  int64_t left = x - plan.before[lo];
   int s = lo * plan.per;
   const int end = min(s + plan.per, a.c.slots);
   for (;; ++s) {
-    it.w = slot_work(a, s, rows);
-    it.splits = splits_of(it.w, plan.range);
-    const int groups = it.w.row_tiles * a.c.kv_heads;
-    const int all = groups * it.splits;
-    const int n = kGroups ? (it.splits > 1 ? groups : 0) : all;
-    if (left < n || s + 1 >= end) break;
-    left -= n;
-    if (it.splits > 1) part += all;
+    g.w = slot_work(a, s, rows);
+    if (left < g.w.units || s + 1 >= end) break;
+    left -= g.w.units;
   }
-  it.slot = s;
-  // row tiles that read the same keys are neighbours
-  it.tile = left % it.w.row_tiles;
-  const int rest = left / it.w.row_tiles;
-  it.head = rest % a.c.kv_heads;
-  it.split = kGroups ? 0 : rest / a.c.kv_heads;
-  it.part = part + (it.head * it.w.row_tiles + it.tile) * it.splits;
-  return it;
+  g.slot = s;
+  const int64_t pair = left / g.w.pair_units;
+  const int off = (int)(left - pair * g.w.pair_units);
+  g.head = (int)(pair / g.w.pairs);
+  const int i = (int)(pair - (int64_t)g.head * g.w.pairs), j = g.w.tiles - 1 - i;
+  const int ui = tile_units(g.w, a.group, rows, i);
+  g.next = x - off + g.w.pair_units;
+  g.tile = i;
+  g.units = ui;
+  g.start = x - off;
+  if (off >= ui) {
+    const int uj = j > i ? tile_units(g.w, a.group, rows, j) : 0;
+    g.tile = j;
+    g.units = off < ui + uj ? uj : 0;
+    g.start = x - off + ui;
+  }
+  return g;
 }
 
 template <typename E>
@@ -252,12 +244,13 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* to, f32x4 v) {
   *reinterpret_cast<bf16x4*>(to) = b;
 }
 
-// One item.  D dimensions; RW x KW waves: RW row groups of NQ 16-row blocks each, KW
+// Key steps [first, end) of a group; `rec`: the record that takes the sums of a group
+// that is cut, or -1.  D dimensions; RW x KW waves: RW row groups of NQ 16-row blocks each, KW
 // parts of the key range.
 // kHalf: pages of 16 tokens under bf16, where one operand spans two pages.
 template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
-__device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it, int range,
-                                            float* sh_ml, float* sh_o) {
+__device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& it, int first,
+                                             int end, int64_t rec, float* sh_ml, float* sh_o) {
   typedef Ops<E> Op;
   typedef typename Op::Chunk Chunk;
   constexpr int kE = Op::kE;
@@ -293,11 +286,9 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   const int last_row = min(row0 + kRows, rows) - 1;
   const int seen = min(it.w.len + last_row / G + 1, it.w.keys);
   const int common = min(it.w.len + row0 / G + 1, it.w.keys);
-  // the wave's part of the item's range, in steps of kKeys keys
-  const int t_first = it.split * range;
-  const int t_end = min(t_first + range, (seen + kKeys - 1) / kKeys);
-  const int count = max(0, t_end - t_first);
-  const int t0 = t_first + count * part / KW, t1 = t_first + count * (part + 1) / KW;
+  // the wave's part of the steps
+  const int count = end - first;
+  const int t0 = first + count * part / KW, t1 = first + count * (part + 1) / KW;
 
   f32x4 o[NQ][kDT];
   float m[NQ], l[NQ];
@@ -479,8 +470,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
   }
   constexpr int kPart = 32;        // dimensions joined at a time
   constexpr int kLd = kPart + 4;   // row stride, against bank conflicts
-  const bool whole = it.splits == 1;
-  const int64_t rec = it.part + it.split;
 #pragma unroll
   for (int d0 = 0; d0 < D; d0 += kPart) {
 #pragma unroll
@@ -506,7 +495,7 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
           const float mw = sh_ml[(w * kRows + r) * 2];
           if (mw != -INFINITY) ls += sh_ml[(w * kRows + r) * 2 + 1] * __builtin_amdgcn_exp2f(mw - mn);
         }
-        if (whole) {
+        if (rec < 0) {
           const int token = row / G;
           E* to = static_cast<E*>(a.out) +
                   ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row - token * G)) * D + d0 + 4 * c;
@@ -528,7 +517,6 @@ __device__ __forceinline__ void attend_item(const AttendArgs& a, const Item& it,
 template <typename E, int D, int NQ, int RW, int KW>
 struct Shape {
   static constexpr int waves = NQ * D <= 384 ? 2 : 1;
-  static constexpr int per_cu = waves * 4 / (RW * KW) > 0 ? waves * 4 / (RW * KW) : 1;
 };
 
 template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
@@ -537,57 +525,73 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   __shared__ Plan plan;
   __shared__ float sh_ml[KW * kRows * 2];
   __shared__ __align__(16) float sh_o[KW * kRows * 36];
-  make_plan<false>(a, kRows, plan);
-  const int total = plan.before[kPlanThreads];
+  make_plan(a, kRows, plan);
+  const int64_t total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
-  // items, so that row tiles that read the same keys share its L2.
-  const int xcd = blockIdx.x & 7, idx = blockIdx.x >> 3, step = gridDim.x >> 3;
-  const int first = (int)((int64_t)total * xcd / 8), last = (int)((int64_t)total * (xcd + 1) / 8);
-  for (int id = first + idx; id < last; id += step) {
-    const Item it = find_item<false>(a, kRows, plan, id);
-    attend_item<E, D, NQ, RW, KW, kHalf>(a, it, plan.range, sh_ml, sh_o);
+  // spans, so that row tiles that read the same keys share its L2.
+  const int per_xcd = (plan.spans + 7) >> 3;
+  const int idx = (int)(blockIdx.x >> 3), span = (int)(blockIdx.x & 7) * per_xcd + idx;
+  if (idx >= per_xcd || span >= plan.spans) return;
+  const int64_t x0 = span * plan.span, x1 = min(x0 + plan.span, total);
+  for (int64_t x = x0; x < x1;) {
+    const Group g = find_group(a, kRows, plan, x);
+    if (g.units == 0) {
+      x = g.next;
+      continue;
+    }
+    const int first = (int)(x - g.start);
+    const int end = (int)min((int64_t)g.units, first + (x1 - x));
+    // a cut group's record: a span has two at most, of its first and of its last group
+    const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
+    attend_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh_o);
+    x += end - first;
   }
 }
 
-// Joins the key ranges of split slots: a workgroup per (slot, kv head, row tile), D / 4
-// threads per row.
+// Joins the groups that spans cut.  Workgroup (k, b): the group that lies across the
+// start of span k + 1, if that is the first such place in it; rows 16 b to 16 b + 15.
 template <typename E>
 __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int rows_per_tile) {
   __shared__ Plan plan;
-  make_plan<true>(a, rows_per_tile, plan);
-  const int total = plan.before[kPlanThreads];
+  make_plan(a, rows_per_tile, plan);
+  const int k = (int)blockIdx.x + 1;
+  if (k >= plan.spans) return;
+  const int64_t x = k * plan.span;
+  const Group g = find_group(a, rows_per_tile, plan, x);
+  if (g.units == 0 || g.start == x || g.start < x - plan.span) return;
   const int D = a.c.head_dim, G = a.group;
   const int per_row = D / 4;
-  for (int id = blockIdx.x; id < total; id += gridDim.x) {
-    const Item it = find_item<true>(a, rows_per_tile, plan, id);
-    const int row0 = it.tile * rows_per_tile;
-    const int rows = min(rows_per_tile, it.w.chunk * G - row0);
-    for (int x = threadIdx.x; x < rows * per_row; x += kPlanThreads) {
-      const int r = x / per_row, c = x % per_row;
-      float mn = -INFINITY;
-      for (int i = 0; i < it.splits; ++i)
-        mn = fmaxf(mn, a.part_ml[((int64_t)(it.part + i) * rows_per_tile + r) * 2]);
-      f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-      float ls = 0.f;
-      for (int i = 0; i < it.splits; ++i) {
-        const int64_t o = (int64_t)(it.part + i) * rows_per_tile + r;
-        const float mi = a.part_ml[o * 2];
-        if (mi == -INFINITY) continue;
-        const float f = __builtin_amdgcn_exp2f(mi - mn);
-        ls += a.part_ml[o * 2 + 1] * f;
-        sum += *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c) * f;
-      }
-      const int row = row0 + r, token = row / G;
-      E* to = static_cast<E*>(a.out) +
-              ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row - token * G)) * D + 4 * c;
-      store4<E>(to, sum * (ls > 0.f ? 1.f / ls : 0.f));
+  const int row0 = g.tile * rows_per_tile;
+  const int r0 = 16 * (int)blockIdx.y;
+  const int r1 = min(r0 + 16, min(rows_per_tile, g.w.chunk * G - row0));
+  // pieces: the end of span k - 1 (its only or its last group), then first groups
+  const int last = (int)((g.start + g.units - 1) / plan.span);
+  const int64_t head = 2 * (int64_t)(k - 1) + (g.start != (k - 1) * plan.span);
+  for (int y = threadIdx.x; y < (r1 - r0) * per_row; y += kPlanThreads) {
+    const int r = r0 + y / per_row, c = y % per_row;
+    float m = -INFINITY, l = 0.f;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    for (int p = k - 1; p <= last; ++p) {
+      const int64_t o = (p == k - 1 ? head : 2 * (int64_t)p) * rows_per_tile + r;
+      const float mp = a.part_ml[o * 2], lp = a.part_ml[o * 2 + 1];
+      const f32x4 op = *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c);
+      const float mn = fmaxf(m, mp);
+      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
+      const float fp = mp == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mp - mn);
+      l = l * f + lp * fp;
+      sum = sum * f + op * fp;
+      m = mn;
     }
+    const int row = row0 + r, token = row / G;
+    E* to = static_cast<E*>(a.out) +
+            ((int64_t)(g.w.o0 + token) * a.heads + g.head * G + (row - token * G)) * D + 4 * c;
+    store4<E>(to, sum * (l > 0.f ? 1.f / l : 0.f));
   }
 }
 
 template <typename E, int D, int NQ, int RW, int KW>
 void start(const AttendArgs& a, hipStream_t stream) {
-  const int grid = 256 * Shape<E, D, NQ, RW, KW>::per_cu;
+  const int grid = a.grid;
   if (sizeof(E) == 2 && a.c.page_shift == 4)
     hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, sizeof(E) == 2>), dim3(grid), dim3(64 * RW * KW), 0,
                        stream, a);
@@ -639,6 +643,12 @@ int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
   return most;
 }
 
+// Workgroups, and spans at most: two waves per SIMD, as many as the registers hold.
+int attend_grid(int head_dim, int rows) {
+  const bool eight = head_dim == 256 ? rows == 32 : rows > 48;  // eight waves or four
+  return eight ? 256 : 512;
+}
+
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream) {
   {
     TimingScope t("attend", stream);
@@ -654,10 +664,11 @@ hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t s
   }
   {
     TimingScope t("attend_join", stream);
+    const dim3 join((unsigned)(a.grid - 1), (unsigned)(rows / 16));
     if (bf16)
-      hipLaunchKernelGGL(k_attend_join<uint16_t>, dim3(512), dim3(kPlanThreads), 0, stream, a, rows);
+      hipLaunchKernelGGL(k_attend_join<uint16_t>, join, dim3(kPlanThreads), 0, stream, a, rows);
     else
-      hipLaunchKernelGGL(k_attend_join<float>, dim3(512), dim3(kPlanThreads), 0, stream, a, rows);
+      hipLaunchKernelGGL(k_attend_join<float>, join, dim3(kPlanThreads), 0, stream, a, rows);
   }
   return hipGetLastError();
 }

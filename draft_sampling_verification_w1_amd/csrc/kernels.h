@@ -334,13 +334,11 @@ struct AttendArgs {
   const void* V;
   const int32_t* offsets;  // [slots + 1]
   void* out;               // [N, heads, head_dim]
-  int target;              // work items aimed at
-  float* part_o;           // [2 * target][rows][head_dim] of the items of split slots
-  float* part_ml;          // [2 * target][rows][2] largest score and sum
+  int grid;                // workgroups = spans of the batch's work at most (attend_grid)
+  float* part_o;           // [2 * grid][rows][head_dim] of cut groups
+  float* part_ml;          // [2 * grid][rows][2] largest score and sum
 };
-// Items aimed at: what is resident at once (256 CUs, one or two workgroups each)
-// twice or four times over, so that ranges of unlike length even out.
-constexpr int kAttendTarget = 1024;
+int attend_grid(int head_dim, int rows);
 int attend_max_rows(bool bf16, int head_dim);
 int attend_rows(bool bf16, int head_dim, int group, int max_chunk);
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
