@@ -244,13 +244,27 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* to, f32x4 v) {
   *reinterpret_cast<bf16x4*>(to) = b;
 }
 
+// Whether a step's operands go through LDS: several row groups share them.
+template <typename E, int D, int RW>
+__host__ __device__ constexpr bool staged() {
+  return sizeof(E) == 2 && D <= 128 && RW > 1;
+}
+// LDS of a workgroup: two steps' operands of every key part, then (at the same
+// place) the parts' outputs, 32 dimensions at a time.
+template <typename E, int D, int NQ, int RW, int KW>
+__host__ __device__ constexpr int lds_bytes() {
+  const int stages = staged<E, D, RW>() ? 2 * KW * kKeys * D * 2 * (int)sizeof(E) : 0;
+  const int join = KW * 16 * NQ * RW * 36 * 4;
+  return stages > join ? stages : join;
+}
+
 // Key steps [first, end) of a group; `rec`: the record that takes the sums of a group
 // that is cut, or -1.  D dimensions; RW x KW waves: RW row groups of NQ 16-row blocks each, KW
 // parts of the key range.
 // kHalf: pages of 16 tokens under bf16, where one operand spans two pages.
 template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
 __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& it, int first,
-                                             int end, int64_t rec, float* sh_ml, float* sh_o) {
+                                             int end, int64_t rec, float* sh_ml, uint8_t* sh) {
   typedef Ops<E> Op;
   typedef typename Op::Chunk Chunk;
   constexpr int kE = Op::kE;
@@ -260,6 +274,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
   constexpr int kWaveRows = 16 * NQ;
   constexpr int kRows = kWaveRows * RW;
   constexpr int kThreads = 64 * RW * KW;
+  constexpr bool kStaged = staged<E, D, RW>();
+  constexpr int kLoads = 2 * kSteps + kVC * kDT;  // operands of a step, 1 KB each
+  float* sh_o = reinterpret_cast<float*>(sh);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave / RW;                 // the wave's part of the keys
   const int wrow = (wave % RW) * kWaveRows;   // its first row in the tile
@@ -367,18 +384,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
   };
 
-  Chunk k[2][kSteps], v[kVC][kDT];
-  int pa = -1, pb = -1;
-  if (t0 < t1) {
-    pages_of(t0, pa, pb);
-    load_k(t0, pa, pb, k);
-  }
-  for (int t = t0; t < t1; ++t) {
-    load_v(t, pa, pb, v);
-    const int ma = pa, mb = pb;
-    // keys that some row does not see: behind its position, or on no page
-    const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0;
-    Chunk p[NQ][kVC];
+  // a step's weights p from its keys, and what they add to the output
+  auto weights = [&](const Chunk (&k)[2][kSteps], int t, int ma, int mb, bool partial,
+                     Chunk (&p)[NQ][kVC]) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       f32x4 s[2];
@@ -426,10 +434,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
         else p[i][j >> 2][j & 3] = e[j];
       }
     }
-    if (t + 1 < t1) {
-      pages_of(t + 1, pa, pb);
-      load_k(t + 1, pa, pb, k);
-    }
+  };
+  auto add_values = [&](Chunk (&v)[kVC][kDT], int t, int ma, int mb, bool partial,
+                        const Chunk (&p)[NQ][kVC]) {
     if (partial) {
       // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN
 #pragma unroll
@@ -446,6 +453,96 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       for (int d = 0; d < kDT; ++d)
 #pragma unroll
         for (int i = 0; i < NQ; ++i) o[i][d] = Op::score(v[u][d], p[i][u], o[i][d]);
+  };
+  // keys that some row does not see: behind its position, or on no page
+  auto is_partial = [&](int t, int ma, int mb) {
+    return (t + 1) * kKeys > common || ma < 0 || mb < 0;
+  };
+
+  Chunk k[2][kSteps], v[kVC][kDT], p[NQ][kVC];
+  if constexpr (!kStaged) {
+    // one row group: the keys go from memory to the operands' registers, the next
+    // step's while this one is worked on
+    int pa = -1, pb = -1;
+    if (t0 < t1) {
+      pages_of(t0, pa, pb);
+      load_k(t0, pa, pb, k);
+    }
+    for (int t = t0; t < t1; ++t) {
+      load_v(t, pa, pb, v);
+      const int ma = pa, mb = pb;
+      const bool partial = is_partial(t, ma, mb);
+      weights(k, t, ma, mb, partial, p);
+      if (t + 1 < t1) {
+        pages_of(t + 1, pa, pb);
+        load_k(t + 1, pa, pb, k);
+      }
+      add_values(v, t, ma, mb, partial, p);
+    }
+  } else {
+    // RW row groups use the same keys: a part's RW waves load 1 / RW of a step's
+    // operands each, one step ahead in registers and one in LDS, from where all of
+    // them read it (operand order: no bank conflicts).
+    constexpr int kShare = kLoads / RW;
+    static_assert(kShare * RW == kLoads && (2 * kSteps) % kShare == 0, "K or V for each wave");
+    const int r = wave % RW;
+    const bool keys = r * kShare < 2 * kSteps;
+    const int l0 = keys ? r * kShare : r * kShare - 2 * kSteps;
+    const char* pool = keys ? Kb : Vb;
+    const uint32_t at_lane = keys ? k_lane : v_lane;
+    Chunk* const tile = reinterpret_cast<Chunk*>(sh) + part * kLoads * 64 + lane;
+    Chunk hold[kShare];
+    auto fetch = [&](int t, int pa, int pb) {
+      const char* ba = pool + max(pa, 0) * page_size_bytes;
+      const char* bb = pool + max(pb, 0) * page_size_bytes;
+      const char* mine = kHalf && (keys ? n >= 8 : quad >= 2) ? bb : ba;
+      const int first = (t * kKeys) & (page - 1);
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) {
+        const int x = l0 + i;
+        const int64_t to = keys ? (int64_t)(4 * (x % kSteps) * page + (kHalf ? 0 : first) + 4 * (x / kSteps)) * 16
+                                : (int64_t)((kHalf ? 0 : first / kE * D) + 16 * x) * 16;
+        hold[i] = *reinterpret_cast<const Chunk*>(mine + to + at_lane);
+      }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < kShare; ++i) tile[(buf * KW * kLoads + r * kShare + i) * 64] = hold[i];
+    };
+    int a0 = -1, b0 = -1, a1 = -1, b1 = -1, a2 = -1, b2 = -1;  // pages of the steps in flight
+    if (t0 < t1) {
+      pages_of(t0, a0, b0);
+      fetch(t0, a0, b0);
+      put(0);
+    }
+    if (t0 + 1 < t1) {
+      pages_of(t0 + 1, a1, b1);
+      fetch(t0 + 1, a1, b1);
+    }
+    __syncthreads();
+    const int stages = (count + KW - 1) / KW;  // of the longest part
+    for (int st = 0; st < stages; ++st) {
+      const int t = t0 + st;
+      if (t + 1 < t1) put((st + 1) & 1);
+      if (t + 2 < t1) {
+        pages_of(t + 2, a2, b2);
+        fetch(t + 2, a2, b2);
+      }
+      if (t < t1) {
+        const Chunk* from = tile + (st & 1) * KW * kLoads * 64;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int c = 0; c < kSteps; ++c) k[u][c] = from[(u * kSteps + c) * 64];
+        const bool partial = is_partial(t, a0, b0);
+        weights(k, t, a0, b0, partial, p);
+#pragma unroll
+        for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
+        add_values(v, t, a0, b0, partial, p);
+      }
+      a0 = a1, b0 = b1, a1 = a2, b1 = b2;
+      __syncthreads();
+    }
   }
 
   // ---- the sums of the key parts joined ----
@@ -524,7 +621,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   constexpr int kRows = 16 * NQ * RW;
   __shared__ Plan plan;
   __shared__ float sh_ml[KW * kRows * 2];
-  __shared__ __align__(16) float sh_o[KW * kRows * 36];
+  __shared__ __align__(16) uint8_t sh[lds_bytes<E, D, NQ, RW, KW>()];
   make_plan(a, kRows, plan);
   const int64_t total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
@@ -543,7 +640,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
     const int end = (int)min((int64_t)g.units, first + (x1 - x));
     // a cut group's record: a span has two at most, of its first and of its last group
     const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
-    attend_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh_o);
+    attend_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh);
     x += end - first;
   }
 }
@@ -599,28 +696,21 @@ void start(const AttendArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, false>), dim3(grid), dim3(64 * RW * KW), 0, stream, a);
 }
 
-// Tiles in use: rows, then the row groups of 16-row blocks.
+// Tiles in use: bf16 up to 128 dimensions; the others have two.  (rows, NQ, RW, KW)
+#define ATTEND_TILES(X) \
+  X(16, 1, 1, 4) X(32, 2, 1, 4) X(48, 3, 1, 4) X(64, 2, 2, 4) X(96, 3, 2, 4) X(128, 2, 4, 2) \
+  X(192, 3, 4, 2) X(256, 2, 8, 1) X(384, 3, 8, 1)
+
 template <typename E, int D>
 bool start_rows(int rows, const AttendArgs& a, hipStream_t stream) {
+#define ATTEND_CASE(ROWS, NQ, RW, KW) \
+  case ROWS: start<E, D, NQ, RW, KW>(a, stream); return true;
   if constexpr (sizeof(E) == 2 && D <= 128) {
-    switch (rows) {
-      case 16: start<E, D, 1, 1, 4>(a, stream); return true;
-      case 32: start<E, D, 2, 1, 4>(a, stream); return true;
-      case 48: start<E, D, 3, 1, 4>(a, stream); return true;
-      case 64: start<E, D, 2, 2, 4>(a, stream); return true;
-      case 96: start<E, D, 3, 2, 4>(a, stream); return true;
-    }
-  } else if constexpr (sizeof(E) == 2) {
-    switch (rows) {
-      case 16: start<E, D, 1, 1, 4>(a, stream); return true;
-      case 32: start<E, D, 1, 2, 4>(a, stream); return true;
-    }
+    switch (rows) { ATTEND_TILES(ATTEND_CASE) }
   } else {
-    switch (rows) {
-      case 16: start<E, D, 1, 1, 4>(a, stream); return true;
-      case 32: start<E, D, 1, 2, 4>(a, stream); return true;
-    }
+    switch (rows) { ATTEND_CASE(16, 1, 1, 4) ATTEND_CASE(32, 1, 2, 4) }
   }
+#undef ATTEND_CASE
   return false;
 }
 
@@ -628,7 +718,7 @@ bool start_rows(int rows, const AttendArgs& a, hipStream_t stream) {
 
 // The largest tile: what the registers hold (the output's accumulators take
 // D / 4 registers per 16 rows, the queries' operands half of that).
-int attend_max_rows(bool bf16, int head_dim) { return bf16 && head_dim <= 128 ? 96 : 32; }
+int attend_max_rows(bool bf16, int head_dim) { return bf16 && head_dim <= 128 ? 384 : 32; }
 
 // Rows (token, head) of a tile: as many as the longest chunk needs, spread evenly
 // over its tiles.
@@ -637,9 +727,10 @@ int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
   const int64_t rows = (int64_t)max_chunk * group;
   const int64_t tiles = (rows + most - 1) / most;
   const int need = (int)((rows + tiles - 1) / tiles);
-  const int sizes[5] = {16, 32, 48, 64, 96};
-  for (int n : sizes)
-    if (n >= need && n <= most) return n;
+#define ATTEND_SIZE(ROWS, NQ, RW, KW) \
+  if (ROWS >= need && ROWS <= most) return ROWS;
+  ATTEND_TILES(ATTEND_SIZE)
+#undef ATTEND_SIZE
   return most;
 }
 
