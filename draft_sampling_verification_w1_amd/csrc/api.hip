@@ -326,11 +326,11 @@ AttendLayout attend_layout(const dspark_cache* c, int N, int heads, int max_chun
   const bool bf16 = c->dtype == DSPARK_BF16;
   const int longest = max_chunk < N ? max_chunk : N;
   L.rows = attend_rows(bf16, c->head_dim, heads / c->kv_heads, longest);
-  L.grid = attend_grid(c->head_dim, L.rows);
+  L.grid = attend_grid(bf16, c->head_dim, L.rows);
   // sized for any tile, whatever chunk a call names
   size_t records = 0;
   for (int rows = 16; rows <= attend_max_rows(bf16, c->head_dim); rows += 16) {
-    const size_t n = (size_t)2 * attend_grid(c->head_dim, rows) * rows;
+    const size_t n = (size_t)2 * attend_grid(bf16, c->head_dim, rows) * rows;
     records = records > n ? records : n;
   }
   Carver v;

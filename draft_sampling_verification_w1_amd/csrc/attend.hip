@@ -247,7 +247,7 @@ __device__ __forceinline__ void store4<uint16_t>(uint16_t* to, f32x4 v) {
 // Whether a step's operands go through LDS: several row groups share them.
 template <typename E, int D, int RW>
 __host__ __device__ constexpr bool staged() {
-  return sizeof(E) == 2 && D <= 128 && RW > 1;
+  return sizeof(E) == 2 && RW > 1;
 }
 // LDS of a workgroup: two steps' operands of every key part, then (at the same
 // place) the parts' outputs, 32 dimensions at a time.
@@ -264,7 +264,8 @@ __host__ __device__ constexpr int lds_bytes() {
 // kHalf: pages of 16 tokens under bf16, where one operand spans two pages.
 template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
 __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& it, int first,
-                                             int end, int64_t rec, float* sh_ml, uint8_t* sh) {
+                                             int end, int64_t rec, float* sh_ml, int* sh_limit,
+                                             uint8_t* sh) {
   typedef Ops<E> Op;
   typedef typename Op::Chunk Chunk;
   constexpr int kE = Op::kE;
@@ -285,16 +286,19 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
   const int row0 = it.tile * kRows, rows = it.w.chunk * G;
   const E* q = static_cast<const E*>(a.q);
 
+  // keys that each row sees; read from LDS where they matter, to keep them out of the
+  // registers of the pass
+  for (int r = threadIdx.x; r < kRows; r += kThreads)
+    sh_limit[r] = min(it.w.len + min((row0 + r) / G, it.w.chunk) + 1, it.w.keys);
+  __syncthreads();
   // queries as operands: lane (n, quad), operand s: dimensions kE (4 s + quad) ..
   Chunk qo[NQ][kSteps];
-  int limit[NQ];  // keys that the lane's row sees
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const int row = row0 + wrow + 16 * i + n;
     const bool live = row < rows;
     const int token = live ? row / G : 0;
     const E* p = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D;
-    limit[i] = min(it.w.len + token + 1, it.w.keys);
 #pragma unroll
     for (int s = 0; s < kSteps; ++s)
       qo[i][s] = live ? *reinterpret_cast<const Chunk*>(p + kE * (4 * s + quad)) : Op::zero();
@@ -384,36 +388,46 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
   };
 
-  // a step's weights p from its keys, and what they add to the output
-  auto weights = [&](const Chunk (&k)[2][kSteps], int t, int ma, int mb, bool partial,
-                     Chunk (&p)[NQ][kVC]) {
+  // scores of a 16-key block with every row block
+  auto scores = [&](const Chunk (&k)[kSteps], int u, f32x4 (&s)[NQ][2]) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      f32x4 s[2];
+    for (int i = 0; i < NQ; ++i) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-        for (int c = 0; c < kSteps; ++c) acc = Op::score(k[u][c], qo[i][c], acc);
-        s[u] = acc;
-      }
-      if (partial) {
+      for (int i = 0; i < NQ; ++i) s[i][u] = Op::score(k[c], qo[i][c], s[i][u]);
+  };
+  // a step's weights p from its scores
+  auto weights = [&](f32x4 (&s)[NQ][2], int t, int ma, int mb, bool partial, Chunk (&p)[NQ][kVC]) {
+    if (partial) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int left = sh_limit[wrow + 16 * i + n] - t * kKeys;  // of this step's keys
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int key = Op::skey_of(u, j, quad);
-            const bool there = t * kKeys + key < limit[i] && (key < 16 ? ma : mb) >= 0;
-            s[u][j] = there ? s[u][j] : -INFINITY;
+            const bool there = key < left && (key < 16 ? ma : mb) >= 0;
+            s[i][u][j] = there ? s[i][u][j] : -INFINITY;
           }
       }
-      float mx = fmaxf(fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[0][2], s[0][3])),
-                       fmaxf(fmaxf(s[1][0], s[1][1]), fmaxf(s[1][2], s[1][3])));
-      mx *= a.scale_log2;
-      // the maximum moves only when some row has passed it by 2^kRise: until then
-      // the sums grow past 1, far from binary32's end, and nothing is rescaled
-      if (__ballot(mx > m[i] + kRise)) {
-        float mn = fmaxf(m[i], mx);
+    }
+    // the maximum moves only when some row has passed it by 2^kRise: until then the
+    // sums grow past 1, far from binary32's end, and nothing is rescaled
+    float mx[NQ];
+    bool risen = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      mx[i] = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
+                    fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3]))) *
+              a.scale_log2;
+      risen |= mx[i] > m[i] + kRise;
+    }
+    if (__ballot(risen)) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        float mn = fmaxf(m[i], mx[i]);
         mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
         mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
         const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[i] - mn);
@@ -422,11 +436,14 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
 #pragma unroll
         for (int d = 0; d < kDT; ++d) o[i][d] *= f;
       }
+    }
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
       const float ref = m[i] == -INFINITY ? 0.f : m[i];
       float e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        e[j] = __builtin_amdgcn_exp2f(fmaf(s[j >> 2][j & 3], a.scale_log2, -ref));
+        e[j] = __builtin_amdgcn_exp2f(fmaf(s[i][j >> 2][j & 3], a.scale_log2, -ref));
       l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -435,18 +452,13 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       }
     }
   };
-  auto add_values = [&](Chunk (&v)[kVC][kDT], int t, int ma, int mb, bool partial,
-                        const Chunk (&p)[NQ][kVC]) {
-    if (partial) {
-      // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN
-#pragma unroll
-      for (int u = 0; u < kVC; ++u) {
-        const int key = Op::vkey_of(u, quad);
-        const int keep = (key < 16 ? ma : mb) >= 0 ? min(max(seen - (t * kKeys + key), 0), kE) : 0;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) v[u][d] = Op::keep(v[u][d], keep);
-      }
-    }
+  // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN.  Keys of
+  // V operand u that lane group q may use:
+  auto usable = [&](int t, int u, int ma, int mb) {
+    const int key = Op::vkey_of(u, quad);
+    return (key < 16 ? ma : mb) >= 0 ? min(max(seen - (t * kKeys + key), 0), kE) : 0;
+  };
+  auto add_values = [&](const Chunk (&v)[kVC][kDT], const Chunk (&p)[NQ][kVC]) {
 #pragma unroll
     for (int u = 0; u < kVC; ++u)
 #pragma unroll
@@ -459,10 +471,12 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     return (t + 1) * kKeys > common || ma < 0 || mb < 0;
   };
 
-  Chunk k[2][kSteps], v[kVC][kDT], p[NQ][kVC];
+  f32x4 s[NQ][2];
+  Chunk p[NQ][kVC];
   if constexpr (!kStaged) {
     // one row group: the keys go from memory to the operands' registers, the next
     // step's while this one is worked on
+    Chunk k[2][kSteps], v[kVC][kDT];
     int pa = -1, pb = -1;
     if (t0 < t1) {
       pages_of(t0, pa, pb);
@@ -472,12 +486,22 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       load_v(t, pa, pb, v);
       const int ma = pa, mb = pb;
       const bool partial = is_partial(t, ma, mb);
-      weights(k, t, ma, mb, partial, p);
+      scores(k[0], 0, s);
+      scores(k[1], 1, s);
       if (t + 1 < t1) {
         pages_of(t + 1, pa, pb);
         load_k(t + 1, pa, pb, k);
       }
-      add_values(v, t, ma, mb, partial, p);
+      weights(s, t, ma, mb, partial, p);
+      if (partial) {
+#pragma unroll
+        for (int u = 0; u < kVC; ++u) {
+          const int keep = usable(t, u, ma, mb);
+#pragma unroll
+          for (int d = 0; d < kDT; ++d) v[u][d] = Op::keep(v[u][d], keep);
+        }
+      }
+      add_values(v, p);
     }
   } else {
     // RW row groups use the same keys: a part's RW waves load 1 / RW of a step's
@@ -505,7 +529,12 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
         hold[i] = *reinterpret_cast<const Chunk*>(mine + to + at_lane);
       }
     };
-    auto put = [&](int buf) {
+    auto put = [&](int buf, int t, int pa, int pb) {
+      if (!keys && is_partial(t, pa, pb)) {
+        const int keep = usable(t, 0, pa, pb);
+#pragma unroll
+        for (int i = 0; i < kShare; ++i) hold[i] = Op::keep(hold[i], keep);
+      }
 #pragma unroll
       for (int i = 0; i < kShare; ++i) tile[(buf * KW * kLoads + r * kShare + i) * 64] = hold[i];
     };
@@ -513,7 +542,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     if (t0 < t1) {
       pages_of(t0, a0, b0);
       fetch(t0, a0, b0);
-      put(0);
+      put(0, t0, a0, b0);
     }
     if (t0 + 1 < t1) {
       pages_of(t0 + 1, a1, b1);
@@ -523,7 +552,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     const int stages = (count + KW - 1) / KW;  // of the longest part
     for (int st = 0; st < stages; ++st) {
       const int t = t0 + st;
-      if (t + 1 < t1) put((st + 1) & 1);
+      if (t + 1 < t1) put((st + 1) & 1, t + 1, a1, b1);
       if (t + 2 < t1) {
         pages_of(t + 2, a2, b2);
         fetch(t + 2, a2, b2);
@@ -531,14 +560,18 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       if (t < t1) {
         const Chunk* from = tile + (st & 1) * KW * kLoads * 64;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < 2; ++u) {
+          Chunk k[kSteps];
 #pragma unroll
-          for (int c = 0; c < kSteps; ++c) k[u][c] = from[(u * kSteps + c) * 64];
-        const bool partial = is_partial(t, a0, b0);
-        weights(k, t, a0, b0, partial, p);
+          for (int c = 0; c < kSteps; ++c) k[c] = from[(u * kSteps + c) * 64];
+          scores(k, u, s);
+        }
+        weights(s, t, a0, b0, is_partial(t, a0, b0), p);
+        __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
+        Chunk v[kVC][kDT];
 #pragma unroll
         for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
-        add_values(v, t, a0, b0, partial, p);
+        add_values(v, p);
       }
       a0 = a1, b0 = b1, a1 = a2, b1 = b2;
       __syncthreads();
@@ -613,7 +646,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
 // Waves per SIMD that the registers of NQ row blocks of D dimensions leave room for.
 template <typename E, int D, int NQ, int RW, int KW>
 struct Shape {
-  static constexpr int waves = NQ * D <= 384 ? 2 : 1;
+  static constexpr int waves = (sizeof(E) == 2 && D <= 128) || RW * KW == 8 ? 2 : 1;
 };
 
 template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
@@ -621,6 +654,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   constexpr int kRows = 16 * NQ * RW;
   __shared__ Plan plan;
   __shared__ float sh_ml[KW * kRows * 2];
+  __shared__ int sh_limit[kRows];
   __shared__ __align__(16) uint8_t sh[lds_bytes<E, D, NQ, RW, KW>()];
   make_plan(a, kRows, plan);
   const int64_t total = plan.before[kPlanThreads];
@@ -640,7 +674,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
     const int end = (int)min((int64_t)g.units, first + (x1 - x));
     // a cut group's record: a span has two at most, of its first and of its last group
     const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
-    attend_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh);
+    attend_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh);
     x += end - first;
   }
 }
@@ -696,19 +730,23 @@ void start(const AttendArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, false>), dim3(grid), dim3(64 * RW * KW), 0, stream, a);
 }
 
-// Tiles in use: bf16 up to 128 dimensions; the others have two.  (rows, NQ, RW, KW)
+// Tiles in use: rows (16 NQ RW), NQ, RW, KW.
 #define ATTEND_TILES(X) \
-  X(16, 1, 1, 4) X(32, 2, 1, 4) X(48, 3, 1, 4) X(64, 2, 2, 4) X(96, 3, 2, 4) X(128, 2, 4, 2) \
-  X(192, 3, 4, 2) X(256, 2, 8, 1) X(384, 3, 8, 1)
+  X(16, 1, 1, 4) X(32, 2, 1, 4) X(64, 2, 2, 4) X(96, 3, 2, 4) X(128, 2, 4, 2) X(192, 3, 4, 2) \
+  X(256, 2, 8, 1) X(384, 3, 8, 1)
+#define ATTEND_TILES_256(X) X(16, 1, 1, 4) X(32, 1, 2, 2) X(64, 1, 4, 2) X(128, 1, 8, 1)
+#define ATTEND_TILES_F32(X) X(16, 1, 1, 4) X(32, 1, 2, 2)
 
 template <typename E, int D>
 bool start_rows(int rows, const AttendArgs& a, hipStream_t stream) {
 #define ATTEND_CASE(ROWS, NQ, RW, KW) \
   case ROWS: start<E, D, NQ, RW, KW>(a, stream); return true;
-  if constexpr (sizeof(E) == 2 && D <= 128) {
-    switch (rows) { ATTEND_TILES(ATTEND_CASE) }
+  if constexpr (sizeof(E) == 4) {
+    switch (rows) { ATTEND_TILES_F32(ATTEND_CASE) }
+  } else if constexpr (D == 256) {
+    switch (rows) { ATTEND_TILES_256(ATTEND_CASE) }
   } else {
-    switch (rows) { ATTEND_CASE(16, 1, 1, 4) ATTEND_CASE(32, 1, 2, 4) }
+    switch (rows) { ATTEND_TILES(ATTEND_CASE) }
   }
 #undef ATTEND_CASE
   return false;
@@ -717,8 +755,8 @@ bool start_rows(int rows, const AttendArgs& a, hipStream_t stream) {
 }  // namespace
 
 // The largest tile: what the registers hold (the output's accumulators take
-// D / 4 registers per 16 rows, the queries' operands half of that).
-int attend_max_rows(bool bf16, int head_dim) { return bf16 && head_dim <= 128 ? 384 : 32; }
+// D / 4 registers per 16 rows of a wave, the queries' operands half of that).
+int attend_max_rows(bool bf16, int head_dim) { return !bf16 ? 32 : (head_dim == 256 ? 128 : 384); }
 
 // Rows (token, head) of a tile: as many as the longest chunk needs, spread evenly
 // over its tiles.
@@ -728,16 +766,23 @@ int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
   const int64_t tiles = (rows + most - 1) / most;
   const int need = (int)((rows + tiles - 1) / tiles);
 #define ATTEND_SIZE(ROWS, NQ, RW, KW) \
-  if (ROWS >= need && ROWS <= most) return ROWS;
-  ATTEND_TILES(ATTEND_SIZE)
+  if (ROWS >= need) return ROWS;
+  if (!bf16) {
+    ATTEND_TILES_F32(ATTEND_SIZE)
+  } else if (head_dim == 256) {
+    ATTEND_TILES_256(ATTEND_SIZE)
+  } else {
+    ATTEND_TILES(ATTEND_SIZE)
+  }
 #undef ATTEND_SIZE
   return most;
 }
 
-// Workgroups, and spans at most: two waves per SIMD, as many as the registers hold.
-int attend_grid(int head_dim, int rows) {
-  const bool eight = head_dim == 256 ? rows == 32 : rows > 48;  // eight waves or four
-  return eight ? 256 : 512;
+// Workgroups, and spans at most: what is resident at once.  Two waves per SIMD (four
+// waves of up to 256 registers from each of two workgroups, or one of eight waves),
+// one where a wave needs more registers.
+int attend_grid(bool bf16, int head_dim, int rows) {
+  return bf16 && head_dim <= 128 && rows <= 32 ? 512 : 256;
 }
 
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream) {

@@ -338,7 +338,7 @@ struct AttendArgs {
   float* part_o;           // [2 * grid][rows][head_dim] of cut groups
   float* part_ml;          // [2 * grid][rows][2] largest score and sum
 };
-int attend_grid(int head_dim, int rows);
+int attend_grid(bool bf16, int head_dim, int rows);
 int attend_max_rows(bool bf16, int head_dim);
 int attend_rows(bool bf16, int head_dim, int group, int max_chunk);
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
