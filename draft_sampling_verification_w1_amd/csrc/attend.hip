@@ -262,7 +262,7 @@ __host__ __device__ constexpr int lds_bytes() {
 // that is cut, or -1.  D dimensions; RW x KW waves: RW row groups of NQ 16-row blocks each, KW
 // parts of the key range.
 // kHalf: pages of 16 tokens under bf16, where one operand spans two pages.
-template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
+template <typename E, int D, int NQ, int RW, int KW, int kAhead, bool kHalf>
 __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& it, int first,
                                              int end, int64_t rec, float* sh_ml, int* sh_limit,
                                              uint8_t* sh) {
@@ -505,8 +505,8 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
   } else {
     // RW row groups use the same keys: a part's RW waves load 1 / RW of a step's
-    // operands each, one step ahead in registers and one in LDS, from where all of
-    // them read it (operand order: no bank conflicts).
+    // operands each, kAhead steps ahead in registers and one in LDS, from where all
+    // of them read it (operand order: no bank conflicts).
     constexpr int kShare = kLoads / RW;
     static_assert(kShare * RW == kLoads && (2 * kSteps) % kShare == 0, "K or V for each wave");
     const int r = wave % RW;
@@ -515,8 +515,8 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     const char* pool = keys ? Kb : Vb;
     const uint32_t at_lane = keys ? k_lane : v_lane;
     Chunk* const tile = reinterpret_cast<Chunk*>(sh) + part * kLoads * 64 + lane;
-    Chunk hold[kShare];
-    auto fetch = [&](int t, int pa, int pb) {
+    Chunk hold[kAhead][kShare];
+    auto fetch = [&](Chunk (&h)[kShare], int t, int pa, int pb) {
       const char* ba = pool + max(pa, 0) * page_size_bytes;
       const char* bb = pool + max(pb, 0) * page_size_bytes;
       const char* mine = kHalf && (keys ? n >= 8 : quad >= 2) ? bb : ba;
@@ -526,55 +526,69 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
         const int x = l0 + i;
         const int64_t to = keys ? (int64_t)(4 * (x % kSteps) * page + (kHalf ? 0 : first) + 4 * (x / kSteps)) * 16
                                 : (int64_t)((kHalf ? 0 : first / kE * D) + 16 * x) * 16;
-        hold[i] = *reinterpret_cast<const Chunk*>(mine + to + at_lane);
+        h[i] = *reinterpret_cast<const Chunk*>(mine + to + at_lane);
       }
     };
-    auto put = [&](int buf, int t, int pa, int pb) {
+    auto put = [&](Chunk (&h)[kShare], int buf, int t, int pa, int pb) {
       if (!keys && is_partial(t, pa, pb)) {
         const int keep = usable(t, 0, pa, pb);
 #pragma unroll
-        for (int i = 0; i < kShare; ++i) hold[i] = Op::keep(hold[i], keep);
+        for (int i = 0; i < kShare; ++i) h[i] = Op::keep(h[i], keep);
       }
 #pragma unroll
-      for (int i = 0; i < kShare; ++i) tile[(buf * KW * kLoads + r * kShare + i) * 64] = hold[i];
+      for (int i = 0; i < kShare; ++i) tile[(buf * KW * kLoads + r * kShare + i) * 64] = h[i];
     };
-    int a0 = -1, b0 = -1, a1 = -1, b1 = -1, a2 = -1, b2 = -1;  // pages of the steps in flight
+    int ca = -1, cb = -1;          // pages of the step in LDS
+    int ha[kAhead], hb[kAhead];    // and of the steps in registers
     if (t0 < t1) {
-      pages_of(t0, a0, b0);
-      fetch(t0, a0, b0);
-      put(0, t0, a0, b0);
+      pages_of(t0, ca, cb);
+      fetch(hold[0], t0, ca, cb);
+      put(hold[0], 0, t0, ca, cb);
     }
-    if (t0 + 1 < t1) {
-      pages_of(t0 + 1, a1, b1);
-      fetch(t0 + 1, a1, b1);
+#pragma unroll
+    for (int i = 1; i <= kAhead; ++i) {
+      ha[i % kAhead] = hb[i % kAhead] = -1;
+      if (t0 + i < t1) {
+        pages_of(t0 + i, ha[i % kAhead], hb[i % kAhead]);
+        fetch(hold[i % kAhead], t0 + i, ha[i % kAhead], hb[i % kAhead]);
+      }
     }
     __syncthreads();
     const int stages = (count + KW - 1) / KW;  // of the longest part
-    for (int st = 0; st < stages; ++st) {
-      const int t = t0 + st;
-      if (t + 1 < t1) put((st + 1) & 1, t + 1, a1, b1);
-      if (t + 2 < t1) {
-        pages_of(t + 2, a2, b2);
-        fetch(t + 2, a2, b2);
-      }
-      if (t < t1) {
-        const Chunk* from = tile + (st & 1) * KW * kLoads * 64;
+    for (int st0 = 0; st0 < stages; st0 += kAhead) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          Chunk k[kSteps];
+      for (int j = 0; j < kAhead; ++j) {
+        const int st = st0 + j, t = t0 + st;
+        if (st < stages) {
+          Chunk(&h)[kShare] = hold[(j + 1) % kAhead];
+          int& na = ha[(j + 1) % kAhead];
+          int& nb = hb[(j + 1) % kAhead];
+          const int xa = na, xb = nb;
+          if (t + 1 < t1) put(h, (st + 1) & 1, t + 1, xa, xb);
+          if (t + 1 + kAhead < t1) {
+            pages_of(t + 1 + kAhead, na, nb);
+            fetch(h, t + 1 + kAhead, na, nb);
+          }
+          if (t < t1) {
+            const Chunk* from = tile + (st & 1) * KW * kLoads * 64;
 #pragma unroll
-          for (int c = 0; c < kSteps; ++c) k[c] = from[(u * kSteps + c) * 64];
-          scores(k, u, s);
+            for (int u = 0; u < 2; ++u) {
+              Chunk k[kSteps];
+#pragma unroll
+              for (int c = 0; c < kSteps; ++c) k[c] = from[(u * kSteps + c) * 64];
+              scores(k, u, s);
+            }
+            weights(s, t, ca, cb, is_partial(t, ca, cb), p);
+            __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
+            Chunk v[kVC][kDT];
+#pragma unroll
+            for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
+            add_values(v, p);
+          }
+          ca = xa, cb = xb;
+          __syncthreads();
         }
-        weights(s, t, a0, b0, is_partial(t, a0, b0), p);
-        __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
-        Chunk v[kVC][kDT];
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
-        add_values(v, p);
       }
-      a0 = a1, b0 = b1, a1 = a2, b1 = b2;
-      __syncthreads();
     }
   }
 
@@ -649,7 +663,7 @@ struct Shape {
   static constexpr int waves = (sizeof(E) == 2 && D <= 128) || RW * KW == 8 ? 2 : 1;
 };
 
-template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
+template <typename E, int D, int NQ, int RW, int KW, int kAhead, bool kHalf>
 __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) void k_attend(AttendArgs a) {
   constexpr int kRows = 16 * NQ * RW;
   __shared__ Plan plan;
@@ -674,7 +688,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
     const int end = (int)min((int64_t)g.units, first + (x1 - x));
     // a cut group's record: a span has two at most, of its first and of its last group
     const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
-    attend_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh);
+    attend_steps<E, D, NQ, RW, KW, kAhead, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh);
     x += end - first;
   }
 }
@@ -720,27 +734,27 @@ __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int 
   }
 }
 
-template <typename E, int D, int NQ, int RW, int KW>
+template <typename E, int D, int NQ, int RW, int KW, int kAhead>
 void start(const AttendArgs& a, hipStream_t stream) {
   const int grid = a.grid;
   if (sizeof(E) == 2 && a.c.page_shift == 4)
-    hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, sizeof(E) == 2>), dim3(grid), dim3(64 * RW * KW), 0,
+    hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, kAhead, sizeof(E) == 2>), dim3(grid), dim3(64 * RW * KW), 0,
                        stream, a);
   else
-    hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, false>), dim3(grid), dim3(64 * RW * KW), 0, stream, a);
+    hipLaunchKernelGGL((k_attend<E, D, NQ, RW, KW, kAhead, false>), dim3(grid), dim3(64 * RW * KW), 0, stream, a);
 }
 
-// Tiles in use: rows (16 NQ RW), NQ, RW, KW.
+// Tiles in use: rows (16 NQ RW), NQ, RW, KW, steps held in registers.
 #define ATTEND_TILES(X) \
-  X(16, 1, 1, 4) X(32, 2, 1, 4) X(64, 2, 2, 4) X(96, 3, 2, 4) X(128, 2, 4, 2) X(192, 3, 4, 2) \
-  X(256, 2, 8, 1) X(384, 3, 8, 1)
-#define ATTEND_TILES_256(X) X(16, 1, 1, 4) X(32, 1, 2, 2) X(64, 1, 4, 2) X(128, 1, 8, 1)
-#define ATTEND_TILES_F32(X) X(16, 1, 1, 4) X(32, 1, 2, 2)
+  X(16, 1, 1, 4, 1) X(32, 2, 1, 4, 1) X(64, 2, 2, 2, 1) X(96, 3, 2, 2, 1) X(128, 2, 4, 2, 2) \
+  X(192, 3, 4, 2, 1) X(256, 2, 8, 1, 2) X(384, 3, 8, 1, 1)
+#define ATTEND_TILES_256(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 2) X(64, 1, 4, 2, 1) X(128, 1, 8, 1, 1)
+#define ATTEND_TILES_F32(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1)
 
 template <typename E, int D>
 bool start_rows(int rows, const AttendArgs& a, hipStream_t stream) {
-#define ATTEND_CASE(ROWS, NQ, RW, KW) \
-  case ROWS: start<E, D, NQ, RW, KW>(a, stream); return true;
+#define ATTEND_CASE(ROWS, NQ, RW, KW, AHEAD) \
+  case ROWS: start<E, D, NQ, RW, KW, AHEAD>(a, stream); return true;
   if constexpr (sizeof(E) == 4) {
     switch (rows) { ATTEND_TILES_F32(ATTEND_CASE) }
   } else if constexpr (D == 256) {
@@ -765,7 +779,7 @@ int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
   const int64_t rows = (int64_t)max_chunk * group;
   const int64_t tiles = (rows + most - 1) / most;
   const int need = (int)((rows + tiles - 1) / tiles);
-#define ATTEND_SIZE(ROWS, NQ, RW, KW) \
+#define ATTEND_SIZE(ROWS, NQ, RW, KW, AHEAD) \
   if (ROWS >= need) return ROWS;
   if (!bf16) {
     ATTEND_TILES_F32(ATTEND_SIZE)
@@ -782,7 +796,7 @@ int attend_rows(bool bf16, int head_dim, int group, int max_chunk) {
 // waves of up to 256 registers from each of two workgroups, or one of eight waves),
 // one where a wave needs more registers.
 int attend_grid(bool bf16, int head_dim, int rows) {
-  return bf16 && head_dim <= 128 && rows <= 32 ? 512 : 256;
+  return bf16 && head_dim <= 128 && rows <= 96 ? 512 : 256;
 }
 
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream) {
