@@ -190,26 +190,32 @@ struct Group {
   int units;      // of the group
   int64_t start;  // its first unit on the line
   int64_t next;   // units == 0 (x lies behind its pair's end): the next pair's first unit
+  int64_t slot_start, slot_end;
 };
 
-__device__ __forceinline__ Group find_group(const AttendArgs& a, int rows, const Plan& plan,
-                                            int64_t x) {
-  int lo = 0, hi = kPlanThreads - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (plan.before[mid] <= x) lo = mid;
-    else hi = mid - 1;
+// `g` may hold the group before it: a slot is looked up when the line leaves it.
+__device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const Plan& plan,
+                                           int64_t x, Group& g) {
+  if (x >= g.slot_end) {
+    int lo = 0, hi = kPlanThreads - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (plan.before[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    int64_t start = plan.before[lo];
+    int s = lo * plan.per;
+    const int end = min(s + plan.per, a.c.slots);
+    for (;; ++s) {
+      g.w = slot_work(a, s, rows);
+      if (x < start + g.w.units || s + 1 >= end) break;
+      start += g.w.units;
+    }
+    g.slot = s;
+    g.slot_start = start;
+    g.slot_end = start + g.w.units;
   }
-  Group g;
-  int64_t left = x - plan.before[lo];
-  int s = lo * plan.per;
-  const int end = min(s + plan.per, a.c.slots);
-  for (;; ++s) {
-    g.w = slot_work(a, s, rows);
-    if (left < g.w.units || s + 1 >= end) break;
-    left -= g.w.units;
-  }
-  g.slot = s;
+  const int64_t left = x - g.slot_start;
   const int64_t pair = left / g.w.pair_units;
   const int off = (int)(left - pair * g.w.pair_units);
   g.head = (int)(pair / g.w.pairs);
@@ -225,7 +231,6 @@ __device__ __forceinline__ Group find_group(const AttendArgs& a, int rows, const
     g.units = off < ui + uj ? uj : 0;
     g.start = x - off + ui;
   }
-  return g;
 }
 
 template <typename E>
@@ -250,11 +255,11 @@ __host__ __device__ constexpr bool staged() {
   return sizeof(E) == 2 && RW > 1;
 }
 // LDS of a workgroup: two steps' operands of every key part, then (at the same
-// place) the parts' outputs, 32 dimensions at a time.
+// place) the outputs of all parts but the first.
 template <typename E, int D, int NQ, int RW, int KW>
 __host__ __device__ constexpr int lds_bytes() {
   const int stages = staged<E, D, RW>() ? 2 * KW * kKeys * D * 2 * (int)sizeof(E) : 0;
-  const int join = KW * 16 * NQ * RW * 36 * 4;
+  const int join = KW > 1 ? (KW - 1) * 16 * NQ * RW * D * 4 : 16;
   return stages > join ? stages : join;
 }
 
@@ -277,7 +282,6 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
   constexpr int kThreads = 64 * RW * KW;
   constexpr bool kStaged = staged<E, D, RW>();
   constexpr int kLoads = 2 * kSteps + kVC * kDT;  // operands of a step, 1 KB each
-  float* sh_o = reinterpret_cast<float*>(sh);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave / RW;                 // the wave's part of the keys
   const int wrow = (wave % RW) * kWaveRows;   // its first row in the tile
@@ -286,23 +290,6 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
   const int row0 = it.tile * kRows, rows = it.w.chunk * G;
   const E* q = static_cast<const E*>(a.q);
 
-  // keys that each row sees; read from LDS where they matter, to keep them out of the
-  // registers of the pass
-  for (int r = threadIdx.x; r < kRows; r += kThreads)
-    sh_limit[r] = min(it.w.len + min((row0 + r) / G, it.w.chunk) + 1, it.w.keys);
-  __syncthreads();
-  // queries as operands: lane (n, quad), operand s: dimensions kE (4 s + quad) ..
-  Chunk qo[NQ][kSteps];
-#pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    const int row = row0 + wrow + 16 * i + n;
-    const bool live = row < rows;
-    const int token = live ? row / G : 0;
-    const E* p = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      qo[i][s] = live ? *reinterpret_cast<const Chunk*>(p + kE * (4 * s + quad)) : Op::zero();
-  }
   // keys any row of the tile sees, and keys all of them see
   const int last_row = min(row0 + kRows, rows) - 1;
   const int seen = min(it.w.len + last_row / G + 1, it.w.keys);
@@ -332,6 +319,24 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     return p >= 0 && p < a.c.pages ? p : -1;
   };
   int ids = columns(col0);
+  // keys that each row sees; read from LDS where they matter, to keep them out of the
+  // registers of the pass
+  for (int r = threadIdx.x; r < kRows; r += kThreads)
+    sh_limit[r] = min(it.w.len + min((row0 + r) / G, it.w.chunk) + 1, it.w.keys);
+  // queries as operands: lane (n, quad), operand s: dimensions kE (4 s + quad) ..
+  Chunk qo[NQ][kSteps];
+  auto load_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int row = row0 + wrow + 16 * i + n;
+      const bool live = row < rows;
+      const int token = live ? row / G : 0;
+      const E* p = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+        qo[i][s] = live ? *reinterpret_cast<const Chunk*>(p + kE * (4 * s + quad)) : Op::zero();
+    }
+  };
   const int page = 1 << shift;
   const int64_t page_elems = (int64_t)H * page * D;
   const E* Kh = static_cast<const E*>(a.K) + (int64_t)it.head * page * D;
@@ -482,6 +487,8 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       pages_of(t0, pa, pb);
       load_k(t0, pa, pb, k);
     }
+    load_q();
+    __syncthreads();  // the limits are there, and the last group's sums are out of LDS
     for (int t = t0; t < t1; ++t) {
       load_v(t, pa, pb, v);
       const int ma = pa, mb = pb;
@@ -543,8 +550,10 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     if (t0 < t1) {
       pages_of(t0, ca, cb);
       fetch(hold[0], t0, ca, cb);
-      put(hold[0], 0, t0, ca, cb);
     }
+    load_q();
+    __syncthreads();  // the limits are there, and the last group's sums are out of LDS
+    if (t0 < t1) put(hold[0], 0, t0, ca, cb);
 #pragma unroll
     for (int i = 1; i <= kAhead; ++i) {
       ha[i % kAhead] = hb[i % kAhead] = -1;
@@ -592,68 +601,65 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
   }
 
-  // ---- the sums of the key parts joined ----
+  // ---- the sums of the key parts joined: the other parts leave theirs in LDS in the
+  // registers' order, the first part's waves add them and write the rows ----
+  f32x4* const sh_o = reinterpret_cast<f32x4*>(sh);
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     l[i] += __shfl_xor(l[i], 16, 64);
     l[i] += __shfl_xor(l[i], 32, 64);
-    if (quad == 0) {
-      sh_ml[(part * kRows + wrow + 16 * i + n) * 2] = m[i];
-      sh_ml[(part * kRows + wrow + 16 * i + n) * 2 + 1] = l[i];
-    }
   }
-  __syncthreads();
+  if constexpr (KW > 1) {
+    if (part > 0) {
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    float mn = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + wrow + 16 * i + n) * 2]);
-    const float f = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] - mn);
-#pragma unroll
-    for (int d = 0; d < kDT; ++d) o[i][d] *= f;
-  }
-  constexpr int kPart = 32;        // dimensions joined at a time
-  constexpr int kLd = kPart + 4;   // row stride, against bank conflicts
-#pragma unroll
-  for (int d0 = 0; d0 < D; d0 += kPart) {
-#pragma unroll
-    for (int i = 0; i < NQ; ++i)
-#pragma unroll
-      for (int d = 0; d < kPart / 16; ++d)
-        *reinterpret_cast<f32x4*>(sh_o + (part * kRows + wrow + 16 * i + n) * kLd + 16 * d + 4 * quad) =
-            o[i][d0 / 16 + d];
-    __syncthreads();
-    for (int x = threadIdx.x; x < kRows * (kPart / 4); x += kThreads) {
-      const int r = x / (kPart / 4), c = x % (kPart / 4);
-      const int row = row0 + r;
-      if (row < rows) {
-        f32x4 sum = *reinterpret_cast<const f32x4*>(sh_o + r * kLd + 4 * c);
-#pragma unroll
-        for (int w = 1; w < KW; ++w)
-          sum += *reinterpret_cast<const f32x4*>(sh_o + (w * kRows + r) * kLd + 4 * c);
-        float mn = -INFINITY, ls = 0.f;
-#pragma unroll
-        for (int w = 0; w < KW; ++w) mn = fmaxf(mn, sh_ml[(w * kRows + r) * 2]);
-#pragma unroll
-        for (int w = 0; w < KW; ++w) {
-          const float mw = sh_ml[(w * kRows + r) * 2];
-          if (mw != -INFINITY) ls += sh_ml[(w * kRows + r) * 2 + 1] * __builtin_amdgcn_exp2f(mw - mn);
+      for (int i = 0; i < NQ; ++i) {
+        if (quad == 0) {
+          sh_ml[(part * kRows + wrow + 16 * i + n) * 2] = m[i];
+          sh_ml[(part * kRows + wrow + 16 * i + n) * 2 + 1] = l[i];
         }
-        if (rec < 0) {
-          const int token = row / G;
-          E* to = static_cast<E*>(a.out) +
-                  ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row - token * G)) * D + d0 + 4 * c;
-          store4<E>(to, sum * (ls > 0.f ? 1.f / ls : 0.f));
-        } else {
-          *reinterpret_cast<f32x4*>(a.part_o + (rec * kRows + r) * D + d0 + 4 * c) = sum;
-          if (d0 == 0 && c == 0) {
-            a.part_ml[(rec * kRows + r) * 2] = mn;
-            a.part_ml[(rec * kRows + r) * 2 + 1] = ls;
-          }
-        }
+#pragma unroll
+        for (int d = 0; d < kDT; ++d)
+          sh_o[(((wave - RW) * NQ + i) * kDT + d) * 64 + lane] = o[i][d];
       }
     }
     __syncthreads();
+    if (part > 0) return;
+  }
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    float f[KW], mn = m[i];
+#pragma unroll
+    for (int w = 1; w < KW; ++w) {
+      f[w] = sh_ml[(w * kRows + wrow + 16 * i + n) * 2];
+      mn = fmaxf(mn, f[w]);
+    }
+    f[0] = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] - mn);
+    float ls = l[i] * f[0];
+#pragma unroll
+    for (int w = 1; w < KW; ++w) {
+      f[w] = f[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(f[w] - mn);
+      ls += sh_ml[(w * kRows + wrow + 16 * i + n) * 2 + 1] * f[w];
+    }
+    const int r = wrow + 16 * i + n, row = row0 + r;
+    if (row >= rows) continue;
+    const int token = row / G;
+    E* to = static_cast<E*>(a.out) +
+            ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row - token * G)) * D + 4 * quad;
+    float* part_to = a.part_o + (rec * kRows + r) * D + 4 * quad;
+    const float norm = ls > 0.f ? 1.f / ls : 0.f;
+#pragma unroll
+    for (int d = 0; d < kDT; ++d) {
+      f32x4 sum = o[i][d] * f[0];
+#pragma unroll
+      for (int w = 1; w < KW; ++w)
+        sum += sh_o[(((w - 1) * RW + wave) * NQ * kDT + i * kDT + d) * 64 + lane] * f[w];
+      if (rec < 0) store4<E>(to + 16 * d, sum * norm);
+      else *reinterpret_cast<f32x4*>(part_to + 16 * d) = sum;
+    }
+    if (rec >= 0 && quad == 0) {
+      a.part_ml[(rec * kRows + r) * 2] = mn;
+      a.part_ml[(rec * kRows + r) * 2 + 1] = ls;
+    }
   }
 }
 
@@ -678,8 +684,10 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   const int idx = (int)(blockIdx.x >> 3), span = (int)(blockIdx.x & 7) * per_xcd + idx;
   if (idx >= per_xcd || span >= plan.spans) return;
   const int64_t x0 = span * plan.span, x1 = min(x0 + plan.span, total);
+  Group g;
+  g.slot_end = 0;
   for (int64_t x = x0; x < x1;) {
-    const Group g = find_group(a, kRows, plan, x);
+    find_group(a, kRows, plan, x, g);
     if (g.units == 0) {
       x = g.next;
       continue;
@@ -702,7 +710,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int 
   const int k = (int)blockIdx.x + 1;
   if (k >= plan.spans) return;
   const int64_t x = k * plan.span;
-  const Group g = find_group(a, rows_per_tile, plan, x);
+  Group g;
+  g.slot_end = 0;
+  find_group(a, rows_per_tile, plan, x, g);
   if (g.units == 0 || g.start == x || g.start < x - plan.span) return;
   const int D = a.c.head_dim, G = a.group;
   const int per_row = D / 4;
