@@ -33,6 +33,10 @@ constexpr int kPlanThreads = 256;  // the workgroup's first threads work out the
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kKeys = 32;      // keys per step of a wave
 constexpr int kMinSpan = 4;    // shortest span of a workgroup, in steps
+// All loads have arrived.  Placed where a load's result is first used in a loop or
+// behind a branch: the compiler would otherwise wait for it inside the loop, and as
+// loads return in order, for the newest ones that the loop has just started.
+__device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
 constexpr float kRise = 8.f;   // the running maximum may lag by this (in log2)
 
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -254,11 +258,22 @@ template <typename E, int D, int RW>
 __host__ __device__ constexpr bool staged() {
   return sizeof(E) == 2 && RW > 1;
 }
-// LDS of a workgroup: two steps' operands of every key part, then (at the same
-// place) the outputs of all parts but the first.
+template <typename E, int D>
+__host__ __device__ constexpr int step_bytes() {
+  return kKeys * D * 2 * (int)sizeof(E);
+}
+// Whether a step's values are added one step late, between the exponentials of the
+// next: matrix and vector instructions of one wave then run side by side.
+template <typename E, int D, int RW, int KW>
+__host__ __device__ constexpr bool late_values() {
+  return staged<E, D, RW>() && RW * KW == 8 && 3 * KW * step_bytes<E, D>() <= (128 << 10);
+}
+// LDS of a workgroup: two steps' operands of every key part (three if values are
+// added late), then (at the same place) the outputs of all parts but the first.
 template <typename E, int D, int NQ, int RW, int KW>
 __host__ __device__ constexpr int lds_bytes() {
-  const int stages = staged<E, D, RW>() ? 2 * KW * kKeys * D * 2 * (int)sizeof(E) : 0;
+  const int stages =
+      staged<E, D, RW>() ? (late_values<E, D, RW, KW>() ? 3 : 2) * KW * step_bytes<E, D>() : 0;
   const int join = KW > 1 ? (KW - 1) * 16 * NQ * RW * D * 4 : 16;
   return stages > join ? stages : join;
 }
@@ -347,6 +362,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     if (cb >= col0 + 64) {
       col0 = ca;
       ids = columns(col0);
+      wait_loads();
     }
     pa = __builtin_amdgcn_readlane(ids, ca - col0);
     pb = __builtin_amdgcn_readlane(ids, cb - col0);
@@ -402,8 +418,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
 #pragma unroll
       for (int i = 0; i < NQ; ++i) s[i][u] = Op::score(k[c], qo[i][c], s[i][u]);
   };
-  // a step's weights p from its scores
-  auto weights = [&](f32x4 (&s)[NQ][2], int t, int ma, int mb, bool partial, Chunk (&p)[NQ][kVC]) {
+  // masks a step's scores and lets the running maxima follow them; `before_rescale`
+  // runs before the sums so far are scaled down
+  auto follow = [&](f32x4 (&s)[NQ][2], int t, int ma, int mb, bool partial, auto&& before_rescale) {
     if (partial) {
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -430,6 +447,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       risen |= mx[i] > m[i] + kRise;
     }
     if (__ballot(risen)) {
+      before_rescale();
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         float mn = fmaxf(m[i], mx[i]);
@@ -442,6 +460,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
         for (int d = 0; d < kDT; ++d) o[i][d] *= f;
       }
     }
+  };
+  // a step's weights p from its scores
+  auto weights = [&](const f32x4 (&s)[NQ][2], Chunk (&p)[NQ][kVC]) {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const float ref = m[i] == -INFINITY ? 0.f : m[i];
@@ -489,6 +510,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
     load_q();
     __syncthreads();  // the limits are there, and the last group's sums are out of LDS
+    wait_loads();
     for (int t = t0; t < t1; ++t) {
       load_v(t, pa, pb, v);
       const int ma = pa, mb = pb;
@@ -499,7 +521,8 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
         pages_of(t + 1, pa, pb);
         load_k(t + 1, pa, pb, k);
       }
-      weights(s, t, ma, mb, partial, p);
+      follow(s, t, ma, mb, partial, [] {});
+      weights(s, p);
       if (partial) {
 #pragma unroll
         for (int u = 0; u < kVC; ++u) {
@@ -553,6 +576,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
     load_q();
     __syncthreads();  // the limits are there, and the last group's sums are out of LDS
+    wait_loads();
     if (t0 < t1) put(hold[0], 0, t0, ca, cb);
 #pragma unroll
     for (int i = 1; i <= kAhead; ++i) {
@@ -564,6 +588,18 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
     __syncthreads();
     const int stages = (count + KW - 1) / KW;  // of the longest part
+    constexpr bool kLate = late_values<E, D, RW, KW>();
+    constexpr int kBufs = kLate ? 3 : 2;
+    auto values = [&](int buf, const Chunk (&w)[NQ][kVC]) {
+      const Chunk* from = tile + buf * KW * kLoads * 64;
+      Chunk v[kVC][kDT];
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
+      add_values(v, w);
+    };
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) p[i][0] = Op::zero();
+    int buf = 0, last = 0;  // buffers of this step and of the last one
     for (int st0 = 0; st0 < stages; st0 += kAhead) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
@@ -573,13 +609,14 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
           int& na = ha[(j + 1) % kAhead];
           int& nb = hb[(j + 1) % kAhead];
           const int xa = na, xb = nb;
-          if (t + 1 < t1) put(h, (st + 1) & 1, t + 1, xa, xb);
+          const int next = buf + 1 == kBufs ? 0 : buf + 1;
+          if (t + 1 < t1) put(h, next, t + 1, xa, xb);
           if (t + 1 + kAhead < t1) {
             pages_of(t + 1 + kAhead, na, nb);
             fetch(h, t + 1 + kAhead, na, nb);
           }
           if (t < t1) {
-            const Chunk* from = tile + (st & 1) * KW * kLoads * 64;
+            const Chunk* from = tile + buf * KW * kLoads * 64;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
               Chunk k[kSteps];
@@ -587,17 +624,47 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
               for (int c = 0; c < kSteps; ++c) k[c] = from[(u * kSteps + c) * 64];
               scores(k, u, s);
             }
-            weights(s, t, ca, cb, is_partial(t, ca, cb), p);
-            __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
-            Chunk v[kVC][kDT];
+            if constexpr (kLate) {
+              follow(s, t, ca, cb, is_partial(t, ca, cb), [&] {
+                values(last, p);
 #pragma unroll
-            for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
-            add_values(v, p);
+                for (int i = 0; i < NQ; ++i) p[i][0] = Op::zero();
+              });
+              // the last step's values between this step's exponentials
+              Chunk w[NQ][kVC];
+              __builtin_amdgcn_sched_barrier(0);
+              values(last, p);
+              weights(s, w);
+              __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+              for (int x = 0; x < kDT; ++x) {
+#pragma unroll
+                for (int i = 0; i < NQ; ++i) {
+                  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                  __builtin_amdgcn_sched_group_barrier(0x402, 5, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+              }
+              __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+              for (int i = 0; i < NQ; ++i) p[i][0] = w[i][0];
+              last = buf;
+            } else {
+              follow(s, t, ca, cb, is_partial(t, ca, cb), [] {});
+              weights(s, p);
+              __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
+              values(buf, p);
+            }
           }
           ca = xa, cb = xb;
+          buf = next;
           __syncthreads();
         }
       }
+    }
+    if constexpr (kLate) {
+      if (t0 < t1) values(last, p);
+      if (KW > 1) __syncthreads();
     }
   }
 
