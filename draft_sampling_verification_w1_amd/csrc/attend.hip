@@ -37,7 +37,9 @@ constexpr int kMinSpan = 4;    // shortest span of a workgroup, in steps
 // behind a branch: the compiler would otherwise wait for it inside the loop, and as
 // loads return in order, for the newest ones that the loop has just started.
 __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70); }
-constexpr float kRise = 8.f;   // the running maximum may lag by this (in log2)
+constexpr float kRise = 8.f;      // how far scores may pass the running maximum (in log2) ...
+constexpr float kRiseSum = 1024.f;  // ... and the sum of a lane's eight weights
+constexpr float kNone = -1e30f;  // maximum of a row that has seen no key
 
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -262,18 +264,11 @@ template <typename E, int D>
 __host__ __device__ constexpr int step_bytes() {
   return kKeys * D * 2 * (int)sizeof(E);
 }
-// Whether a step's values are added one step late, between the exponentials of the
-// next: matrix and vector instructions of one wave then run side by side.
-template <typename E, int D, int RW, int KW>
-__host__ __device__ constexpr bool late_values() {
-  return staged<E, D, RW>() && RW * KW == 8 && 3 * KW * step_bytes<E, D>() <= (128 << 10);
-}
-// LDS of a workgroup: two steps' operands of every key part (three if values are
-// added late), then (at the same place) the outputs of all parts but the first.
+// LDS of a workgroup: two steps' operands of every key part, then (at the same
+// place) the outputs of all parts but the first.
 template <typename E, int D, int NQ, int RW, int KW>
 __host__ __device__ constexpr int lds_bytes() {
-  const int stages =
-      staged<E, D, RW>() ? (late_values<E, D, RW, KW>() ? 3 : 2) * KW * step_bytes<E, D>() : 0;
+  const int stages = staged<E, D, RW>() ? 2 * KW * step_bytes<E, D>() : 0;
   const int join = KW > 1 ? (KW - 1) * 16 * NQ * RW * D * 4 : 16;
   return stages > join ? stages : join;
 }
@@ -317,7 +312,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
   float m[NQ], l[NQ];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    m[i] = -INFINITY;
+    m[i] = kNone;
     l[i] = 0.f;
 #pragma unroll
     for (int d = 0; d < kDT; ++d) o[i][d] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -409,6 +404,8 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
   };
 
+  f32x4 s[NQ][2];
+  Chunk p[NQ][kVC];
   // scores of a 16-key block with every row block
   auto scores = [&](const Chunk (&k)[kSteps], int u, f32x4 (&s)[NQ][2]) {
 #pragma unroll
@@ -418,10 +415,12 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
 #pragma unroll
       for (int i = 0; i < NQ; ++i) s[i][u] = Op::score(k[c], qo[i][c], s[i][u]);
   };
-  // masks a step's scores and lets the running maxima follow them; `before_rescale`
-  // runs before the sums so far are scaled down
-  auto follow = [&](f32x4 (&s)[NQ][2], int t, int ma, int mb, bool partial, auto&& before_rescale) {
-    if (partial) {
+  // keys that some row does not see: behind its position, or on no page
+  auto is_partial = [&](int t, int ma, int mb) {
+    return (t + 1) * kKeys > common || ma < 0 || mb < 0;
+  };
+  auto mask = [&](f32x4 (&s)[NQ][2], int t, int ma, int mb) {
+    if (is_partial(t, ma, mb)) {
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         const int left = sh_limit[wrow + 16 * i + n] - t * kKeys;  // of this step's keys
@@ -435,9 +434,10 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
           }
       }
     }
-    // the maximum moves only when some row has passed it by 2^kRise: until then the
-    // sums grow past 1, far from binary32's end, and nothing is rescaled
-    float mx[NQ];
+  };
+  // A step's largest scores; true if one lies far above its row's maximum.
+  float mx[NQ], sums[NQ];
+  auto largest = [&]() {
     bool risen = false;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
@@ -446,37 +446,62 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
               a.scale_log2;
       risen |= mx[i] > m[i] + kRise;
     }
-    if (__ballot(risen)) {
-      before_rescale();
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        float mn = fmaxf(m[i], mx[i]);
-        mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
-        mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
-        const float f = mn == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(m[i] - mn);
-        m[i] = mn;
-        l[i] *= f;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) o[i][d] *= f;
-      }
-    }
+    return __ballot(risen) != 0;
   };
-  // a step's weights p from its scores
-  auto weights = [&](const f32x4 (&s)[NQ][2], Chunk (&p)[NQ][kVC]) {
+  // The maxima brought up to a step's scores, and the sums so far scaled down.
+  auto follow = [&]() {
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const float ref = m[i] == -INFINITY ? 0.f : m[i];
+      float mn = fmaxf(m[i], mx[i]);
+      mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
+      mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
+      const float f = __builtin_amdgcn_exp2f(m[i] - mn);
+      m[i] = mn;
+      l[i] *= f;
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) o[i][d] *= f;
+    }
+  };
+  // A step's weights p and their sums, against the maxima as they are; true if a sum
+  // shows that some score lies far above its row's maximum.
+  auto weights = [&]() {
+    bool risen = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
       float e[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        e[j] = __builtin_amdgcn_exp2f(fmaf(s[i][j >> 2][j & 3], a.scale_log2, -ref));
-      l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        e[j] = __builtin_amdgcn_exp2f(fmaf(s[i][j >> 2][j & 3], a.scale_log2, -m[i]));
+      sums[i] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      risen |= sums[i] > kRiseSum;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if constexpr (sizeof(E) == 2) p[i][0][j] = (__bf16)e[j];
         else p[i][j >> 2][j & 3] = e[j];
       }
     }
+    return __ballot(risen) != 0;
+  };
+  // The maxima move at the first step, and when a score is far above all before it;
+  // otherwise they stay behind (the sums are far from binary32's end) and a step needs
+  // neither a rescaling nor an exchange between lanes.  Large tiles are bound by
+  // arithmetic and learn it from the weights' sums, without a maximum over the scores;
+  // the others by memory, and go without keeping scores and weights side by side.
+  auto step_weights = [&]() {
+    if constexpr (KW == 1) {
+      if (weights()) {
+        largest();
+        follow();
+        weights();
+      }
+    } else {
+      if (largest()) follow();
+      weights();
+    }
+  };
+  auto add_sums = [&]() {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) l[i] += sums[i];
   };
   // rows of the pages behind the last key seen hold anything: 0 * NaN is NaN.  Keys of
   // V operand u that lane group q may use:
@@ -492,13 +517,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
 #pragma unroll
         for (int i = 0; i < NQ; ++i) o[i][d] = Op::score(v[u][d], p[i][u], o[i][d]);
   };
-  // keys that some row does not see: behind its position, or on no page
-  auto is_partial = [&](int t, int ma, int mb) {
-    return (t + 1) * kKeys > common || ma < 0 || mb < 0;
-  };
 
-  f32x4 s[NQ][2];
-  Chunk p[NQ][kVC];
   if constexpr (!kStaged) {
     // one row group: the keys go from memory to the operands' registers, the next
     // step's while this one is worked on
@@ -521,8 +540,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
         pages_of(t + 1, pa, pb);
         load_k(t + 1, pa, pb, k);
       }
-      follow(s, t, ma, mb, partial, [] {});
-      weights(s, p);
+      mask(s, t, ma, mb);
+      step_weights();
+      add_sums();
       if (partial) {
 #pragma unroll
         for (int u = 0; u < kVC; ++u) {
@@ -588,8 +608,6 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
     __syncthreads();
     const int stages = (count + KW - 1) / KW;  // of the longest part
-    constexpr bool kLate = late_values<E, D, RW, KW>();
-    constexpr int kBufs = kLate ? 3 : 2;
     auto values = [&](int buf, const Chunk (&w)[NQ][kVC]) {
       const Chunk* from = tile + buf * KW * kLoads * 64;
       Chunk v[kVC][kDT];
@@ -597,9 +615,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       for (int d = 0; d < kDT; ++d) v[0][d] = from[(2 * kSteps + d) * 64];
       add_values(v, w);
     };
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) p[i][0] = Op::zero();
-    int buf = 0, last = 0;  // buffers of this step and of the last one
+    int buf = 0;
     for (int st0 = 0; st0 < stages; st0 += kAhead) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
@@ -609,7 +625,7 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
           int& na = ha[(j + 1) % kAhead];
           int& nb = hb[(j + 1) % kAhead];
           const int xa = na, xb = nb;
-          const int next = buf + 1 == kBufs ? 0 : buf + 1;
+          const int next = buf ^ 1;
           if (t + 1 < t1) put(h, next, t + 1, xa, xb);
           if (t + 1 + kAhead < t1) {
             pages_of(t + 1 + kAhead, na, nb);
@@ -624,47 +640,17 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
               for (int c = 0; c < kSteps; ++c) k[c] = from[(u * kSteps + c) * 64];
               scores(k, u, s);
             }
-            if constexpr (kLate) {
-              follow(s, t, ca, cb, is_partial(t, ca, cb), [&] {
-                values(last, p);
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) p[i][0] = Op::zero();
-              });
-              // the last step's values between this step's exponentials
-              Chunk w[NQ][kVC];
-              __builtin_amdgcn_sched_barrier(0);
-              values(last, p);
-              weights(s, w);
-              __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
-#pragma unroll
-              for (int x = 0; x < kDT; ++x) {
-#pragma unroll
-                for (int i = 0; i < NQ; ++i) {
-                  __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                  __builtin_amdgcn_sched_group_barrier(0x402, 5, 0);
-                }
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-              }
-              __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-              for (int i = 0; i < NQ; ++i) p[i][0] = w[i][0];
-              last = buf;
-            } else {
-              follow(s, t, ca, cb, is_partial(t, ca, cb), [] {});
-              weights(s, p);
-              __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
-              values(buf, p);
-            }
+            mask(s, t, ca, cb);
+            step_weights();
+            add_sums();
+            __builtin_amdgcn_sched_barrier(0);  // V's registers are the scores'
+            values(buf, p);
           }
           ca = xa, cb = xb;
           buf = next;
           __syncthreads();
         }
       }
-    }
-    if constexpr (kLate) {
-      if (t0 < t1) values(last, p);
-      if (KW > 1) __syncthreads();
     }
   }
 
@@ -700,11 +686,11 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       f[w] = sh_ml[(w * kRows + wrow + 16 * i + n) * 2];
       mn = fmaxf(mn, f[w]);
     }
-    f[0] = m[i] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m[i] - mn);
+    f[0] = __builtin_amdgcn_exp2f(m[i] - mn);
     float ls = l[i] * f[0];
 #pragma unroll
     for (int w = 1; w < KW; ++w) {
-      f[w] = f[w] == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(f[w] - mn);
+      f[w] = __builtin_amdgcn_exp2f(f[w] - mn);
       ls += sh_ml[(w * kRows + wrow + 16 * i + n) * 2 + 1] * f[w];
     }
     const int r = wrow + 16 * i + n, row = row0 + r;
@@ -791,15 +777,14 @@ __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int 
   const int64_t head = 2 * (int64_t)(k - 1) + (g.start != (k - 1) * plan.span);
   for (int y = threadIdx.x; y < (r1 - r0) * per_row; y += kPlanThreads) {
     const int r = r0 + y / per_row, c = y % per_row;
-    float m = -INFINITY, l = 0.f;
+    float m = kNone, l = 0.f;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     for (int p = k - 1; p <= last; ++p) {
       const int64_t o = (p == k - 1 ? head : 2 * (int64_t)p) * rows_per_tile + r;
       const float mp = a.part_ml[o * 2], lp = a.part_ml[o * 2 + 1];
       const f32x4 op = *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c);
       const float mn = fmaxf(m, mp);
-      const float f = m == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(m - mn);
-      const float fp = mp == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(mp - mn);
+      const float f = __builtin_amdgcn_exp2f(m - mn), fp = __builtin_amdgcn_exp2f(mp - mn);
       l = l * f + lp * fp;
       sum = sum * f + op * fp;
       m = mn;
