@@ -317,7 +317,7 @@ void* layer_of(const dspark_cache* c, void* pool, int layer) {
 
 struct AttendLayout {
   int rows, grid;
-  size_t o, ml, bytes;
+  size_t o, ml, cuts, bytes;
 };
 
 // Records of the groups that spans cut: two per span at most.
@@ -328,14 +328,17 @@ AttendLayout attend_layout(const dspark_cache* c, int N, int heads, int max_chun
   L.rows = attend_rows(bf16, c->head_dim, heads / c->kv_heads, longest);
   L.grid = attend_grid(bf16, c->head_dim, L.rows);
   // sized for any tile, whatever chunk a call names
-  size_t records = 0;
+  size_t records = 0, most = 0;
   for (int rows = 16; rows <= attend_max_rows(bf16, c->head_dim); rows += 16) {
     const size_t n = (size_t)2 * attend_grid(bf16, c->head_dim, rows) * rows;
     records = records > n ? records : n;
+    const size_t g = attend_grid(bf16, c->head_dim, rows);
+    most = most > g ? most : g;
   }
   Carver v;
   L.o = v.take(records * c->head_dim * sizeof(float));
   L.ml = v.take(records * 2 * sizeof(float));
+  L.cuts = v.take((1 + most) * sizeof(AttendCut));
   L.bytes = v.off;
   return L;
 }
@@ -1106,6 +1109,7 @@ __attribute__((visibility("default"))) int dspark_attend(
   a.grid = L.grid;
   a.part_o = at<float>(ws, L.o);
   a.part_ml = at<float>(ws, L.ml);
+  a.cuts = at<AttendCut>(ws, L.cuts);
   hipError_t e = launch_attend(c->dtype == DSPARK_BF16, L.rows, a, (hipStream_t)stream);
   if (e != hipSuccess) return hip_fail(e, "attend");
   return ok();

@@ -733,12 +733,14 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   const int64_t total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
   // spans, so that row tiles that read the same keys share its L2.
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.cuts[0].first = plan.spans;
   const int per_xcd = (plan.spans + 7) >> 3;
   const int idx = (int)(blockIdx.x >> 3), span = (int)(blockIdx.x & 7) * per_xcd + idx;
   if (idx >= per_xcd || span >= plan.spans) return;
   const int64_t x0 = span * plan.span, x1 = min(x0 + plan.span, total);
   Group g;
   g.slot_end = 0;
+  AttendCut cut = {};
   for (int64_t x = x0; x < x1;) {
     find_group(a, kRows, plan, x, g);
     if (g.units == 0) {
@@ -749,38 +751,37 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
     const int end = (int)min((int64_t)g.units, first + (x1 - x));
     // a cut group's record: a span has two at most, of its first and of its last group
     const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
+    if (first == 0 && end < g.units) {  // it goes on in the next span
+      cut.row0 = g.tile * kRows;
+      cut.rows = min(kRows, g.w.chunk * a.group - cut.row0);
+      cut.token0 = g.w.o0;
+      cut.head = g.head;
+      cut.first = (int)rec;
+      cut.last = (int)((g.start + g.units - 1) / plan.span);
+    }
     attend_steps<E, D, NQ, RW, KW, kAhead, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh);
     x += end - first;
   }
+  if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }
 
-// Joins the groups that spans cut.  Workgroup (k, b): the group that lies across the
-// start of span k + 1, if that is the first such place in it; rows 16 b to 16 b + 15.
+// Joins the groups that spans cut: workgroup (k, b) rows 16 b to 16 b + 15 of the
+// group that starts in span k and goes on behind it.  Its pieces: record `first`, then
+// the first records of spans k + 1 to `last`.
 template <typename E>
 __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int rows_per_tile) {
-  __shared__ Plan plan;
-  make_plan(a, rows_per_tile, plan);
-  const int k = (int)blockIdx.x + 1;
-  if (k >= plan.spans) return;
-  const int64_t x = k * plan.span;
-  Group g;
-  g.slot_end = 0;
-  find_group(a, rows_per_tile, plan, x, g);
-  if (g.units == 0 || g.start == x || g.start < x - plan.span) return;
+  const int k = (int)blockIdx.x;
+  if (k >= a.cuts[0].first) return;
+  const AttendCut cut = a.cuts[1 + k];
   const int D = a.c.head_dim, G = a.group;
   const int per_row = D / 4;
-  const int row0 = g.tile * rows_per_tile;
-  const int r0 = 16 * (int)blockIdx.y;
-  const int r1 = min(r0 + 16, min(rows_per_tile, g.w.chunk * G - row0));
-  // pieces: the end of span k - 1 (its only or its last group), then first groups
-  const int last = (int)((g.start + g.units - 1) / plan.span);
-  const int64_t head = 2 * (int64_t)(k - 1) + (g.start != (k - 1) * plan.span);
+  const int r0 = 16 * (int)blockIdx.y, r1 = min(r0 + 16, cut.rows);
   for (int y = threadIdx.x; y < (r1 - r0) * per_row; y += kPlanThreads) {
     const int r = r0 + y / per_row, c = y % per_row;
     float m = kNone, l = 0.f;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int p = k - 1; p <= last; ++p) {
-      const int64_t o = (p == k - 1 ? head : 2 * (int64_t)p) * rows_per_tile + r;
+    for (int p = k; p <= cut.last; ++p) {
+      const int64_t o = (p == k ? (int64_t)cut.first : 2 * (int64_t)p) * rows_per_tile + r;
       const float mp = a.part_ml[o * 2], lp = a.part_ml[o * 2 + 1];
       const f32x4 op = *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c);
       const float mn = fmaxf(m, mp);
@@ -789,9 +790,9 @@ __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int 
       sum = sum * f + op * fp;
       m = mn;
     }
-    const int row = row0 + r, token = row / G;
+    const int row = cut.row0 + r, token = row / G;
     E* to = static_cast<E*>(a.out) +
-            ((int64_t)(g.w.o0 + token) * a.heads + g.head * G + (row - token * G)) * D + 4 * c;
+            ((int64_t)(cut.token0 + token) * a.heads + cut.head * G + (row - token * G)) * D + 4 * c;
     store4<E>(to, sum * (l > 0.f ? 1.f / l : 0.f));
   }
 }
@@ -876,7 +877,7 @@ hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t s
   }
   {
     TimingScope t("attend_join", stream);
-    const dim3 join((unsigned)(a.grid - 1), (unsigned)(rows / 16));
+    const dim3 join((unsigned)a.grid, (unsigned)(rows / 16));
     if (bf16)
       hipLaunchKernelGGL(k_attend_join<uint16_t>, join, dim3(kPlanThreads), 0, stream, a, rows);
     else

@@ -413,59 +413,69 @@ __global__ __launch_bounds__(256) void k_cache_copy(CacheArgs a, uint8_t* K, uin
   }
 }
 
-// A chunk's keys and values into the pages.  Workgroup i belongs to token i; the
-// first token of a slot's chunk in a group of E positions (E = 16 bytes of
-// elements, the group that V stores side by side) writes the group.  K goes in 16-byte
-// pieces; V is turned: a thread gathers one dimension of the group's tokens.
+// A chunk's keys and values into the pages.  A workgroup takes one kv head of one
+// group of E positions (E = 16 bytes of elements, what V stores side by side) of a
+// slot; slot s's groups are numbered from offsets[s] / E + 3 s on, which leaves room
+// for a group that is cut at either end.  K goes in 16-byte pieces (the first half of
+// the threads); V is turned, a thread gathers one dimension of the group's tokens.
 template <typename E>
 __global__ __launch_bounds__(256) void k_cache_append(CacheArgs a, E* K, E* V, int N, const E* k,
                                                       const E* v, const int32_t* offsets) {
   constexpr int kE = 16 / (int)sizeof(E);
-  __shared__ int found[3];
-  const int i = blockIdx.x;
+  __shared__ int found[4];
+  const int w = blockIdx.x;
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
-  // the last slot that starts at or before token i and has tokens behind it
   for (int s = threadIdx.x; s < a.slots; s += 256) {
-    const int o0 = offsets[s], o1 = offsets[s + 1];
-    if (o0 <= i && i < o1) {
+    const int o0 = min(max(offsets[s], 0), N), o1 = min(max(offsets[s + 1], o0), N);
+    const int first = o0 / kE + 3 * s;
+    if (o0 < o1 && first <= w && w < o1 / kE + 3 * (s + 1)) {
       found[0] = s;
-      found[1] = max(o0, 0);
-      found[2] = min(o1, N);
+      found[1] = o0;
+      found[2] = o1;
+      found[3] = w - first;
     }
   }
   __syncthreads();
   const int s = found[0], o0 = found[1], o1 = found[2];
   if (s < 0) return;
   const int64_t len = a.t.lens[s];
-  const int64_t pos = len + (i - o0);
-  if (i != o0 && (pos & (kE - 1)) != 0) return;
-  const int e0 = (int)(pos & (kE - 1));
-  const int n = min(kE - e0, o1 - i);  // tokens of the group
+  if (len < 0) return;
+  const int64_t start = (len / kE + found[3]) * kE;  // of the group
+  const int e0 = start < len ? (int)(len - start) : 0;
+  const int64_t pos = start + e0;
+  const int64_t i = o0 + (pos - len);  // first token of the group
+  if (i >= o1) return;
+  const int n = (int)min((int64_t)(kE - e0), o1 - i);
   const int64_t j = pos >> a.page_shift;
-  if (pos < 0 || j >= min(a.t.held[s], a.max_pages)) return;
+  if (j >= min(a.t.held[s], a.max_pages)) return;
   const int p = a.t.table[(int64_t)s * a.max_pages + j];
   if (!page_ok(a, p)) return;
   const int D = a.head_dim, H = a.kv_heads, C = D / kE, page = 1 << a.page_shift;
+  const int h = blockIdx.y;
   const int t0 = (int)(pos & (page - 1));
-  const int64_t base = (int64_t)p * H * page * D;
-  const E* kt = k + (int64_t)i * H * D;
-  const E* vt = v + (int64_t)i * H * D;
-  for (int x = threadIdx.x; x < n * H * C; x += 256) {
-    const int c = x % C, h = (x / C) % H, t = x / (C * H);
-    const u32x4 w = *reinterpret_cast<const u32x4*>(kt + ((int64_t)t * H + h) * D + c * kE);
-    *reinterpret_cast<u32x4*>(K + base + (((int64_t)h * C + c) * page + t0 + t) * kE) = w;
-  }
-  for (int x = threadIdx.x; x < H * D; x += 256) {
-    const int d = x % D, h = x / D;
-    E* to = V + base + (((int64_t)h * (page / kE) + t0 / kE) * D + d) * kE;
-    if (n == kE) {
-      alignas(16) E w[kE];
+  const int64_t base = ((int64_t)p * H + h) * page * D;
+  const E* kt = k + (i * H + h) * D;
+  const E* vt = v + (i * H + h) * D;
+  if (threadIdx.x < 128) {
+    for (int x = threadIdx.x; x < n * C; x += 128) {
+      const int c = x % C, t = x / C;
+      const u32x4 q = *reinterpret_cast<const u32x4*>(kt + (int64_t)t * H * D + c * kE);
+      *reinterpret_cast<u32x4*>(K + base + ((int64_t)c * page + t0 + t) * kE) = q;
+    }
+  } else {
+    for (int d = threadIdx.x - 128; d < D; d += 128) {
+      E* to = V + base + ((int64_t)(t0 / kE) * D + d) * kE;
+      alignas(16) E q[kE];
 #pragma unroll
-      for (int t = 0; t < kE; ++t) w[t] = vt[(int64_t)t * H * D + x];
-      *reinterpret_cast<u32x4*>(to) = *reinterpret_cast<const u32x4*>(w);
-    } else {
-      for (int t = 0; t < n; ++t) to[e0 + t] = vt[(int64_t)t * H * D + x];
+      for (int t = 0; t < kE; ++t) q[t] = vt[(int64_t)min(t, n - 1) * H * D + d];
+      if (n == kE) {
+        *reinterpret_cast<u32x4*>(to) = *reinterpret_cast<const u32x4*>(q);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kE; ++t)
+          if (t < n) to[e0 + t] = q[t];
+      }
     }
   }
 }
@@ -541,12 +551,13 @@ hipError_t launch_cache_append(const CacheArgs& a, bool bf16, void* K, void* V, 
                                const void* k, const void* v, const int32_t* offsets,
                                hipStream_t stream) {
   TimingScope t("cache_append", stream);
+  const dim3 grid((unsigned)(N / (bf16 ? 8 : 4) + 3 * a.slots), (unsigned)a.kv_heads);
   if (bf16)
-    hipLaunchKernelGGL(k_cache_append<uint16_t>, dim3(N), dim3(256), 0, stream, a,
+    hipLaunchKernelGGL(k_cache_append<uint16_t>, grid, dim3(256), 0, stream, a,
                        static_cast<uint16_t*>(K), static_cast<uint16_t*>(V), N,
                        static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), offsets);
   else
-    hipLaunchKernelGGL(k_cache_append<float>, dim3(N), dim3(256), 0, stream, a,
+    hipLaunchKernelGGL(k_cache_append<float>, grid, dim3(256), 0, stream, a,
                        static_cast<float*>(K), static_cast<float*>(V), N,
                        static_cast<const float*>(k), static_cast<const float*>(v), offsets);
   return hipGetLastError();

@@ -324,6 +324,12 @@ hipError_t launch_cache_append(const CacheArgs& a, bool bf16, void* K, void* V, 
                                const void* k, const void* v, const int32_t* offsets,
                                hipStream_t stream);
 
+// A group of rows whose key steps lie in several spans (attend.hip); rows 0: none.
+struct AttendCut {
+  int32_t row0, rows, token0, head;
+  int32_t first, last;  // first record, last span
+  int32_t spare[2];
+};
 // Attention of a chunk of new tokens per slot over the pages.
 struct AttendArgs {
   CacheArgs c;
@@ -337,6 +343,7 @@ struct AttendArgs {
   int grid;                // workgroups = spans of the batch's work at most (attend_grid)
   float* part_o;           // [2 * grid][rows][head_dim] of cut groups
   float* part_ml;          // [2 * grid][rows][2] largest score and sum
+  AttendCut* cuts;         // [1 + grid]: the number of spans (first), then one per span
 };
 int attend_grid(bool bf16, int head_dim, int rows);
 int attend_max_rows(bool bf16, int head_dim);
