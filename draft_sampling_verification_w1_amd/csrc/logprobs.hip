@@ -23,102 +23,135 @@ __device__ __forceinline__ bool ahead(float v1, int i1, float v2, int i2) {
   return v1 > v2 || (v1 == v2 && i1 < i2);
 }
 
-// A wave's candidates, best first: lane l holds the (l + 1)-th best entry seen.
-// -inf entries are no candidates (value -inf, index kNoIndex marks an empty place).
-struct WaveTop {
+// A value's place among binary32 values as an unsigned number (0: below them all).
+__device__ __forceinline__ uint32_t order_of(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+  return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+
+// A wave's candidates for the n best: an unordered list in LDS of entries that were
+// above the bar when they came.  The bar is a lower bound of the n-th best entry so
+// far; it rises when the list is cut down to its n best.  For logits in no particular
+// order a list of kCut takes the entries of some five steps before its first cut and
+// few afterwards, so that most steps cost a compare or seventeen.  The n-th best is
+// found by bisecting the bits of its value: a compare per 64 entries and bit, no
+// sorting and no exchange between lanes.
+constexpr int kCut = 128;            // entries above which a list is cut
+constexpr int kRoom = kCut + 64;     // one more instruction's worth
+struct Candidate {
   float v;
   int i;
-
-  __device__ void clear() {
-    v = -INFINITY;
-    i = kNoIndex;
-  }
-
-  // One entry per lane, sorted: a bitonic network over the wave (21 exchanges).
-  __device__ void sort(float x, int idx) {
-    v = x;
-    i = idx;
-    const int lane = (int)threadIdx.x & 63;
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1) {
-#pragma unroll
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        const float ov = __shfl_xor(v, j, 64);
-        const int oi = __shfl_xor(i, j, 64);
-        // blocks of k alternate direction; the lower lane of a pair keeps the
-        // better entry in a descending block, the worse one in an ascending one
-        const bool keep_better = ((lane & k) == 0) == ((lane & j) == 0);
-        if (ahead(v, i, ov, oi) != keep_better) {
-          v = ov;
-          i = oi;
-        }
-      }
-    }
-  }
-
-  // Insert the wave-uniform entry (x, idx); the worst one falls off the end.
-  __device__ void insert(float x, int idx) {
-    const int lane = (int)threadIdx.x & 63;
-    const int place = __popcll(__ballot(ahead(v, i, x, idx)));
-    const float pv = __shfl_up(v, 1, 64);
-    const int pi = __shfl_up(i, 1, 64);
-    if (lane > place) {
-      v = pv;
-      i = pi;
-    } else if (lane == place) {
-      v = x;
-      i = idx;
-    }
-  }
-
-  // The n-th best entry (wave uniform).
-  __device__ void bar(int n, float* bv, int* bi) const {
-    *bv = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), n - 1));
-    *bi = __builtin_amdgcn_readlane(i, n - 1);
-  }
 };
 
-// Takes a lane's entries x[j] with index idx(j) into the wave's list, as far as
-// they are among the n best.  `mine` is the lane's largest entry.  With n
-// places filled, a step none of whose entries passes the n-th best costs one
-// compare and one ballot; for logits in no particular order that is all but
-// ~n ln(entries) of the entries.  While the list is empty, a step sorts the
-// lanes' largest entries, whose n-th bounds the list from below at once.
-template <int N, typename Index>
-__device__ __forceinline__ void take(WaveTop& top, int n, const float (&x)[N], float mine,
-                                     Index idx) {
-  float bv;
-  int bi, own = -1;
-  top.bar(n, &bv, &bi);
-  if (__ballot(mine >= bv && mine > -INFINITY) == 0) return;
-  if (__int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(top.v))) == -INFINITY) {
-    // the lane's best entry: the first that reaches its maximum
-#pragma unroll
-    for (int j = N - 1; j >= 0; --j)
-      if (x[j] == mine) own = j;
-    if (mine == -INFINITY) own = -1;
-    int at = kNoIndex;
-#pragma unroll
-    for (int j = 0; j < N; ++j)
-      if (j == own) at = idx(j);
-    top.sort(mine, at);
-    top.bar(n, &bv, &bi);
+template <int kBits>                 // of a value that can differ: 16 (bf16) or 32
+struct WaveTop {
+  Candidate* list;
+  int n, count;
+  float bar;       // entries not above it are no candidates
+  float exact;     // the n-th best value after a cut, -inf before
+
+  __device__ void start(Candidate* room, int places) {
+    list = room;
+    n = places;
+    count = 0;
+    bar = exact = -INFINITY;
   }
+
+  __device__ static float below(float v) { return value_of(order_of(v) - 1); }
+
+  // The first bar: the n-th best of the lanes' largest entries is a lower bound.
+  // Its value's upper 16 bits are enough.
+  __device__ void first_bar(float mine) {
+    const uint32_t o = mine > -INFINITY ? order_of(mine) : 0u;
+    uint32_t t = 0;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const int id = idx(j);
-    uint64_t left = __ballot(j != own && x[j] > -INFINITY && ahead(x[j], id, bv, bi));
-    while (left) {
-      const int lane = __ffsll((unsigned long long)left) - 1;
-      const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x[j]), lane));
-      const int i = __builtin_amdgcn_readlane(id, lane);
-      left &= left - 1;
-      if (!ahead(v, i, bv, bi)) continue;  // the bar has risen past it
-      top.insert(v, i);
-      top.bar(n, &bv, &bi);
+    for (int b = 31; b >= 16; --b) {
+      const uint32_t c = t | (1u << b);
+      if (__popcll(__ballot(o >= c)) >= n) t = c;
     }
+    // fewer than n lanes with a finite entry: no bound
+    if (t > 0x007FFFFFu) bar = below(value_of(t));
   }
-}
+
+  // A step begins: its entries come behind all earlier ones in the vocabulary, so that
+  // one that only equals the n-th best is no candidate any more.
+  __device__ void step() { bar = fmaxf(bar, exact); }
+
+  __device__ void add(float v, int i) {
+    const uint64_t hit = __ballot(v > bar);
+    if (!hit) return;
+    if (v > bar) {
+      const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(hit >> 32),
+                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)hit, 0u));
+      list[at] = Candidate{v + 0.f, i};  // + 0: the two zeros are equal
+    }
+    count += __popcll(hit);
+    if (count > kCut) cut();
+  }
+
+  // Keeps the n best of the list: all above the n-th best value, and of those equal to
+  // it the lowest indices.
+  __device__ void cut() {
+    if (count <= n) return;
+    constexpr int kR = kRoom / 64;
+    const int lane = (int)threadIdx.x & 63;
+    Candidate e[kR];
+    uint32_t o[kR];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const bool there = lane + 64 * r < count;
+      e[r] = list[there ? lane + 64 * r : 0];
+      o[r] = there ? order_of(e[r].v) : 0u;
+    }
+    uint32_t t = 0;
+#pragma unroll
+    for (int b = 31; b >= 32 - kBits; --b) {
+      const uint32_t c = t | (1u << b);
+      int m = 0;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) m += __popcll(__ballot(o[r] >= c));
+      if (m >= n) t = c;
+    }
+    if (kBits < 32 && t < 0x80000000u) t |= (1u << (32 - kBits)) - 1u;  // the low bits of negative values
+    int above = 0, equal = 0;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      above += __popcll(__ballot(o[r] > t));
+      equal += __popcll(__ballot(o[r] == t));
+    }
+    int last = kNoIndex;  // highest index kept among equal values
+    if (above + equal > n) {
+      const int want = n - above;
+      int low = 0;        // largest number with fewer than `want` equal entries below it
+#pragma unroll
+      for (int b = 25; b >= 0; --b) {
+        const int c = low | (1 << b);
+        int m = 0;
+#pragma unroll
+        for (int r = 0; r < kR; ++r) m += __popcll(__ballot(o[r] == t && e[r].i < c));
+        if (m < want) low = c;
+      }
+      last = low;
+    }
+    count = 0;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const bool keep = o[r] > t || (o[r] == t && e[r].i <= last);
+      const uint64_t kept = __ballot(keep);
+      if (keep)
+        list[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(kept >> 32),
+                                               __builtin_amdgcn_mbcnt_lo((uint32_t)kept, 0u))] = e[r];
+      count += __popcll(kept);
+    }
+    __builtin_amdgcn_wave_barrier();
+    exact = value_of(t);
+    bar = below(exact);  // until the step's end an equal entry may have a lower index
+  }
+};
 
 // Sums over entries of one row: m the largest entry, s = sum e^(z - m),
 // t = sum e^(z - m) (z - m), in binary64.
@@ -187,13 +220,17 @@ __device__ __forceinline__ RowSums block_sums(float m, float kf, double s, doubl
 
 // The n best of the waves' lists, in order: entry e of the 4 n listed ones goes
 // to the place given by how many others are ahead of it.
-__device__ __forceinline__ void block_top(const WaveTop& top, int n, float* ov, int* oi) {
+template <int kBits>
+__device__ __forceinline__ void block_top(WaveTop<kBits>& top, int n, float* ov, int* oi) {
   __shared__ float lv[kThreads];
   __shared__ int li[kThreads];
   const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  top.cut();
+  __builtin_amdgcn_wave_barrier();
   if (lane < n) {
-    lv[wave * n + lane] = top.v;
-    li[wave * n + lane] = top.i;
+    const Candidate c = top.list[lane];
+    lv[wave * n + lane] = lane < top.count ? c.v : -INFINITY;
+    li[wave * n + lane] = lane < top.count ? c.i : kNoIndex;
   }
   __syncthreads();
   const int e = (int)threadIdx.x;
@@ -305,6 +342,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
   __shared__ RowSums sums;
   __shared__ float tv[64];
   __shared__ int ti[64];
+  __shared__ Candidate room[kTop ? kWaves * kRoom : 1];
   const int r = (int)blockIdx.x;
   const int split = (int)blockIdx.y;
   const int id = a.ids[r];
@@ -316,8 +354,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
   const int skew = (int)(((uintptr_t)row / sizeof(E)) & (Group<E>::size - 1));
   const int u0 = split * a.chunk;  // a whole number of steps
   const int u1 = min(a.V + skew, u0 + a.chunk);
-  WaveTop top;
-  top.clear();
+  WaveTop<8 * (int)sizeof(E)> top;
+  if (kTop) top.start(room + ((int)threadIdx.x >> 6) * kRoom, a.n_top);
   // Running sums s = sum 2^y, t = sum 2^y y with y = z L - K, against an integer
   // reference K >= max z L that only rises: each exponent is one fma and a rise
   // rescales by an exact power of two.  y is held above -200, where 2^y is zero
@@ -359,9 +397,13 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
       t += (double)((t4[0] + t4[1]) + (t4[2] + t4[3]));
     }
     if (kTop) {
-      take(top, a.n_top, x, mt, [&](int j) {
-        return ul + (j / Group<E>::size) * Group<E>::apart + (j % Group<E>::size) - skew;
-      });
+      top.step();
+      if (__ballot(mt > top.bar)) {
+        if (top.bar == -INFINITY) top.first_bar(mt);
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          top.add(x[j], ul + (j / Group<E>::size) * Group<E>::apart + (j % Group<E>::size) - skew);
+      }
     }
   }
   const RowSums b = block_sums(m, kf, s, t);
@@ -391,6 +433,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
   __shared__ RowSums sums;
   __shared__ float tv[64];
   __shared__ int ti[64];
+  __shared__ Candidate room[kTop ? kWaves * kRoom : 1];
   const int r = (int)blockIdx.x;
   const int id = a.ids[r];
   if (id < 0 || id >= a.V) {
@@ -418,47 +461,17 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
   }
   if (lane == 0) part[wave] = b;
   if (kTop) {
-    WaveTop top;
-    top.clear();
+    // the splits' entries, a wave's share of the splits at a time; an entry that equals
+    // the n-th best may still come with a lower index, so that no step is ever begun
+    WaveTop<8 * (int)sizeof(E)> top;
+    top.start(room + wave * kRoom, a.n_top);
     const int total = a.nsplit * a.n_top;
     const float* pv = a.part_v + o * a.n_top;
     const int* pi = a.part_i + o * a.n_top;
-    // four entries per thread and step: wave w's part of a step is contiguous
-    for (int c = 0; c < total; c += 4 * kThreads) {
-      float x[4];
-      int ix[4];
-      float mt = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = c + j * kThreads + (int)threadIdx.x;
-        x[j] = e < total ? pv[e] : -INFINITY;
-        ix[j] = e < total ? pi[e] : kNoIndex;
-        mt = fmaxf(mt, x[j]);
-      }
-      // entries come in no index order: among equal ones of a lane the first
-      // listed is not always the lowest, so every step goes through the list
-      float bv;
-      int bi;
-      top.bar(a.n_top, &bv, &bi);
-      if (__ballot(mt >= bv && mt > -INFINITY) == 0) continue;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (c == 0 && j == 0) {
-          top.sort(x[0], ix[0]);
-          top.bar(a.n_top, &bv, &bi);
-          continue;
-        }
-        uint64_t left = __ballot(x[j] > -INFINITY && ahead(x[j], ix[j], bv, bi));
-        while (left) {
-          const int l = __ffsll((unsigned long long)left) - 1;
-          const float v = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x[j]), l));
-          const int i = __builtin_amdgcn_readlane(ix[j], l);
-          left &= left - 1;
-          if (!ahead(v, i, bv, bi)) continue;
-          top.insert(v, i);
-          top.bar(a.n_top, &bv, &bi);
-        }
-      }
+    for (int c = 64 * wave; c < total; c += kThreads) {
+      const int e = c + lane;
+      const float x = e < total ? pv[e] : -INFINITY;
+      top.add(x, e < total ? pi[e] : kNoIndex);
     }
     block_top(top, a.n_top, tv, ti);
   }
