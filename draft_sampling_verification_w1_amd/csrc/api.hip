@@ -234,7 +234,7 @@ LogprobLayout logprob_layout(int N, int V, int n_top) {
   if (L.nsplit == 1) return L;
   const size_t n = (size_t)N * L.nsplit;
   Carver c;
-  L.m = c.take(n * sizeof(float));
+  L.m = c.take(n * 2 * sizeof(float));
   L.st = c.take(n * 2 * sizeof(double));
   L.v = c.take(n * n_top * sizeof(float));
   L.i = c.take(n * n_top * sizeof(int32_t));
@@ -948,7 +948,7 @@ __attribute__((visibility("default"))) int dspark_token_logprobs(
   a.nsplit = L.nsplit;
   a.chunk = L.chunk;
   if (L.bytes) {
-    a.part_m = at<float>(ws, L.m);
+    a.part_mk = at<float>(ws, L.m);
     a.part_st = at<double>(ws, L.st);
     a.part_v = at<float>(ws, L.v);
     a.part_i = at<int32_t>(ws, L.i);

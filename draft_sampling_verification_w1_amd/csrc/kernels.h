@@ -282,9 +282,9 @@ struct LogprobArgs {
   int32_t* top_ids;      // [N, n_top]
   float* top_logprobs;   // [N, n_top]
   int nsplit, chunk;     // vocabulary splits per row, entries per split
-  float* part_m;         // [N * nsplit] largest entry of a split
+  float* part_mk;        // [2 * N * nsplit] largest entry of a split and reference of its sums
   double* part_st;       // [2 * N * nsplit] its two sums
-  float* part_v;         // [N * nsplit * n_top] its best entries, in order
+  float* part_v;         // [N * nsplit * n_top] its best entries, best of every split first
   int32_t* part_i;
 };
 int logprob_splits(int N, int V, int* chunk);

@@ -14,9 +14,16 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / 64;
-constexpr int kPer = 16;                       // entries per thread and step
-constexpr int kStep = kThreads * kPer;         // entries per workgroup and step
+constexpr int kPer = 16;               // entries per thread and step
+constexpr int kStep = kThreads * kPer; // entries per workgroup and step
 constexpr int kNoIndex = 0x7FFFFFFF;
+
+__device__ __forceinline__ uint64_t ballot(bool b) { return __builtin_amdgcn_ballot_w64(b); }
+// Lanes below this one among those of a mask.
+__device__ __forceinline__ int rank_in(uint64_t mask) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                   __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
+}
 
 // Order of the alternatives: larger value first, then the lower index.
 __device__ __forceinline__ bool ahead(float v1, int i1, float v2, int i2) {
@@ -31,72 +38,133 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
+__device__ __forceinline__ float below(float v) { return value_of(order_of(v) - 1); }
 
-// A wave's candidates for the n best: an unordered list in LDS of entries that were
-// above the bar when they came.  The bar is a lower bound of the n-th best entry so
-// far; it rises when the list is cut down to its n best.  For logits in no particular
-// order a list of kCut takes the entries of some five steps before its first cut and
-// few afterwards, so that most steps cost a compare or seventeen.  The n-th best is
-// found by bisecting the bits of its value: a compare per 64 entries and bit, no
-// sorting and no exchange between lanes.
-constexpr int kCut = 128;            // entries above which a list is cut
-constexpr int kRoom = kCut + 64;     // one more instruction's worth
 struct Candidate {
   float v;
   int i;
 };
 
-template <int kBits>                 // of a value that can differ: 16 (bf16) or 32
+// A wave's candidates for the n best of its workgroup's entries: an unordered list in
+// LDS of the entries that were above the bar when they came.  The bar is a lower bound
+// of the workgroup's n-th best entry so far.  Each wave publishes the n'-th best of its
+// own list, n' = ceil(n / waves): at least n entries of the workgroup reach the smallest
+// of these.  (n below the number of waves: the n-th best of any wave is a bound, the
+// largest is taken.)  A published value only rises, so that an old one is a bound too
+// and the waves need not wait for each other.  For logits in no particular order step k
+// of a row then has n / k entries above the bar: a step mostly costs a compare, or one
+// for each of four groups.  Ranks are found by bisecting the bits of a value, a compare
+// per 64 entries and bit: no sorting, no exchange between lanes.  Which entries a list
+// holds at some time depends on the waves' timing, its n best do not.
+constexpr int kCut = 128;              // entries above which a list is cut to its n best
+constexpr int kRoom = kCut + 4 * 64;   // one more group's worth
+
+template <int kBits>                   // of a value that can differ: 16 (bf16) or 32
 struct WaveTop {
   Candidate* list;
-  int n, count;
-  float bar;       // entries not above it are no candidates
-  float exact;     // the n-th best value after a cut, -inf before
+  volatile float* shared;              // the waves' published values
+  int n, rank, count, told;            // told: entries when last published
+  float bar;                           // entries not above it are no candidates
+  float exact;                         // the list's n-th best value at its last cut
 
-  __device__ void start(Candidate* room, int places) {
+  __device__ void start(Candidate* room, volatile float* published, int places) {
     list = room;
+    shared = published;
     n = places;
-    count = 0;
+    rank = n >= kWaves ? (n + kWaves - 1) / kWaves : n;
+    count = told = 0;
     bar = exact = -INFINITY;
   }
 
-  __device__ static float below(float v) { return value_of(order_of(v) - 1); }
-
-  // The first bar: the n-th best of the lanes' largest entries is a lower bound.
-  // Its value's upper 16 bits are enough.
-  __device__ void first_bar(float mine) {
-    const uint32_t o = mine > -INFINITY ? order_of(mine) : 0u;
+  // The order of the k-th best of the lanes' values (its upper 16 bits), 0 if fewer
+  // than k lanes have a finite one.
+  __device__ static uint32_t kth_of_lanes(float v, int k) {
+    const uint32_t o = v > -INFINITY ? order_of(v) : 0u;
     uint32_t t = 0;
 #pragma unroll
     for (int b = 31; b >= 16; --b) {
       const uint32_t c = t | (1u << b);
-      if (__popcll(__ballot(o >= c)) >= n) t = c;
+      if (__popcll(ballot(o >= c)) >= k) t = c;
     }
-    // fewer than n lanes with a finite entry: no bound
-    if (t > 0x007FFFFFu) bar = below(value_of(t));
+    return t > 0x007FFFFFu ? t : 0u;
+  }
+  // A wave's first bar, from the lanes' largest entries.
+  __device__ void first_bar(float mine) {
+    const uint32_t t = kth_of_lanes(mine, n);
+    if (t) bar = below(value_of(t));
   }
 
-  // A step begins: its entries come behind all earlier ones in the vocabulary, so that
-  // one that only equals the n-th best is no candidate any more.
-  __device__ void step() { bar = fmaxf(bar, exact); }
+  // A step begins.  Entries that only equal the n-th best of another wave may have a
+  // lower index; those that equal the own n-th best come behind n better ones.
+  __device__ void step() {
+    const float a = shared[0], b = shared[1], c = shared[2], d = shared[3];
+    const float all = rank < n || n == kWaves ? fminf(fminf(a, b), fminf(c, d))
+                                              : fmaxf(fmaxf(a, b), fmaxf(c, d));
+    if (all > -INFINITY) bar = fmaxf(bar, below(all));
+    bar = fmaxf(bar, exact);
+  }
 
+  // Appends the lanes' entries above the bar.
   __device__ void add(float v, int i) {
-    const uint64_t hit = __ballot(v > bar);
+    const uint64_t hit = ballot(v > bar);
     if (!hit) return;
-    if (v > bar) {
-      const int at = count + __builtin_amdgcn_mbcnt_hi((uint32_t)(hit >> 32),
-                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)hit, 0u));
-      list[at] = Candidate{v + 0.f, i};  // + 0: the two zeros are equal
-    }
+    if (v > bar) list[count + rank_in(hit)] = Candidate{v + 0.f, i};  // + 0: the two zeros are equal
     count += __popcll(hit);
-    if (count > kCut) cut();
+  }
+
+  __device__ void publish(int wave) {
+    if (count < rank || count == told) return;
+    told = count;
+    __builtin_amdgcn_wave_barrier();
+    uint32_t t;
+    if (count <= 64) {
+      uint32_t o[1];
+      orders(o);
+      t = nth(o, rank);
+    } else {
+      uint32_t o[kRoom / 64];
+      orders(o);
+      t = nth(o, rank);
+    }
+    if ((threadIdx.x & 63) == 0) shared[wave] = value_of(t);
+  }
+
+  template <int kR>
+  __device__ void orders(uint32_t (&o)[kR]) const {
+    const int lane = (int)threadIdx.x & 63;
+#pragma unroll
+    for (int r = 0; r < kR; ++r) {
+      const int e = lane + 64 * r;
+      o[r] = e < count ? order_of(list[e < count ? e : 0].v) : 0u;
+    }
+  }
+
+  // The order of the k-th best value of a list of at least k.
+  template <int kR>
+  __device__ static uint32_t nth(const uint32_t (&o)[kR], int k) {
+    uint32_t t = 0;
+#pragma unroll 4
+    for (int b = 31; b >= 32 - kBits; --b) {
+      const uint32_t c = t | (1u << b);
+      int m = 0;
+#pragma unroll
+      for (int r = 0; r < kR; ++r) m += __popcll(ballot(o[r] >= c));
+      if (m >= k) t = c;
+    }
+    // the bits that are the same for all: ones in the order of negative values
+    if (kBits < 32 && t < 0x80000000u) t |= (uint32_t)((uint64_t(1) << (32 - kBits)) - 1);
+    return t;
   }
 
   // Keeps the n best of the list: all above the n-th best value, and of those equal to
   // it the lowest indices.
   __device__ void cut() {
     if (count <= n) return;
-    constexpr int kR = kRoom / 64;
+    if (count <= 64) cut_to<1>();
+    else cut_to<kRoom / 64>();
+  }
+  template <int kR>
+  __device__ void cut_to() {
     const int lane = (int)threadIdx.x & 63;
     Candidate e[kR];
     uint32_t o[kR];
@@ -107,32 +175,23 @@ struct WaveTop {
       e[r] = list[there ? lane + 64 * r : 0];
       o[r] = there ? order_of(e[r].v) : 0u;
     }
-    uint32_t t = 0;
-#pragma unroll
-    for (int b = 31; b >= 32 - kBits; --b) {
-      const uint32_t c = t | (1u << b);
-      int m = 0;
-#pragma unroll
-      for (int r = 0; r < kR; ++r) m += __popcll(__ballot(o[r] >= c));
-      if (m >= n) t = c;
-    }
-    if (kBits < 32 && t < 0x80000000u) t |= (1u << (32 - kBits)) - 1u;  // the low bits of negative values
+    const uint32_t t = nth(o, n);
     int above = 0, equal = 0;
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
-      above += __popcll(__ballot(o[r] > t));
-      equal += __popcll(__ballot(o[r] == t));
+      above += __popcll(ballot(o[r] > t));
+      equal += __popcll(ballot(o[r] == t));
     }
     int last = kNoIndex;  // highest index kept among equal values
     if (above + equal > n) {
       const int want = n - above;
       int low = 0;        // largest number with fewer than `want` equal entries below it
-#pragma unroll
+#pragma unroll 1
       for (int b = 25; b >= 0; --b) {
         const int c = low | (1 << b);
         int m = 0;
 #pragma unroll
-        for (int r = 0; r < kR; ++r) m += __popcll(__ballot(o[r] == t && e[r].i < c));
+        for (int r = 0; r < kR; ++r) m += __popcll(ballot(o[r] == t && e[r].i < c));
         if (m < want) low = c;
       }
       last = low;
@@ -141,348 +200,384 @@ struct WaveTop {
 #pragma unroll
     for (int r = 0; r < kR; ++r) {
       const bool keep = o[r] > t || (o[r] == t && e[r].i <= last);
-      const uint64_t kept = __ballot(keep);
-      if (keep)
-        list[count + __builtin_amdgcn_mbcnt_hi((uint32_t)(kept >> 32),
-                                               __builtin_amdgcn_mbcnt_lo((uint32_t)kept, 0u))] = e[r];
+      const uint64_t kept = ballot(keep);
+      if (keep) list[count + rank_in(kept)] = e[r];
       count += __popcll(kept);
     }
     __builtin_amdgcn_wave_barrier();
+    told = 0;
     exact = value_of(t);
-    bar = below(exact);  // until the step's end an equal entry may have a lower index
+    bar = fmaxf(bar, below(exact));  // until the step's end an equal entry may have a lower index
   }
-};
 
-// Sums over entries of one row: m the largest entry, s = sum e^(z - m),
-// t = sum e^(z - m) (z - m), in binary64.
-struct RowSums {
-  float m;
-  double s, t;
-};
-
-// Joins two sets of entries.
-__device__ __forceinline__ void join(RowSums& a, const RowSums& b) {
-  if (b.m == -INFINITY) return;
-  if (a.m == -INFINITY) {
-    a = b;
-    return;
-  }
-  const float m = fmaxf(a.m, b.m);
-  const double da = (double)a.m - (double)m, db = (double)b.m - (double)m;
-  const double ea = exp(da), eb = exp(db);
-  a.t = ea * (a.t + da * a.s) + eb * (b.t + db * b.s);
-  a.s = ea * a.s + eb * b.s;
-  a.m = m;
-}
-
-// A thread's sums, brought to the workgroup's largest entry and added up;
-// valid in thread 0.  One binary64 exponential per thread.
-__device__ __forceinline__ RowSums block_sums(float m, float kf, double s, double t) {
-  __shared__ float sm[kWaves];
-  __shared__ double ss[kWaves], st[kWaves];
-  const int wave = (int)threadIdx.x >> 6, lane = (int)threadIdx.x & 63;
-  float big = m;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) big = fmaxf(big, __shfl_xor(big, off, 64));
-  if (lane == 0) sm[wave] = big;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) big = fmaxf(big, sm[w]);
-  if (m != -INFINITY) {
-    // s, t hold sum 2^y and sum 2^y y with y = z L - kf; shift y by d = kf - big L
-    // to exponents of z - big.  L is the same binary32 constant as in the pass,
-    // so that only |z - big| times its rounding remains.
-    const double d = (double)kf - (double)big * (double)kLog2e;
-    const double f = exp2(d);
-    t = f * (t + d * s) * (1.0 / (double)kLog2e);
-    s = f * s;
-  }
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    s += __shfl_xor(s, off, 64);
-    t += __shfl_xor(t, off, 64);
-  }
-  if (lane == 0) {
-    ss[wave] = s;
-    st[wave] = t;
-  }
-  __syncthreads();
-  RowSums r = {big, 0.0, 0.0};
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      r.s += ss[w];
-      r.t += st[w];
-    }
-  }
-  return r;
-}
-
-// The n best of the waves' lists, in order: entry e of the 4 n listed ones goes
-// to the place given by how many others are ahead of it.
-template <int kBits>
-__device__ __forceinline__ void block_top(WaveTop<kBits>& top, int n, float* ov, int* oi) {
-  __shared__ float lv[kThreads];
-  __shared__ int li[kThreads];
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
-  top.cut();
-  __builtin_amdgcn_wave_barrier();
-  if (lane < n) {
-    const Candidate c = top.list[lane];
-    lv[wave * n + lane] = lane < top.count ? c.v : -INFINITY;
-    li[wave * n + lane] = lane < top.count ? c.i : kNoIndex;
-  }
-  __syncthreads();
-  const int e = (int)threadIdx.x;
-  if (e < kWaves * n) {
-    const float v = lv[e];
-    const int i = li[e];
+  // The n best, best first (places left over: -inf, kNoIndex), to the wave's lanes.
+  __device__ Candidate sorted() {
+    cut();
+    const int lane = (int)threadIdx.x & 63;
+    Candidate c = list[lane < count ? lane : 0];
+    if (lane >= count) c = Candidate{-INFINITY, kNoIndex};
     int place = 0;
-    for (int q = 0; q < kWaves * n; ++q) {
-      // empty places are equal: the lower one is ahead
-      place += (ahead(lv[q], li[q], v, i) || (lv[q] == v && li[q] == i && q < e)) ? 1 : 0;
+#pragma unroll 8
+    for (int q = 0; q < count; ++q) {
+      const Candidate o = list[q];
+      place += ahead(o.v, o.i, c.v, c.i) ? 1 : 0;
     }
-    if (place < n) {
-      ov[place] = v;
-      oi[place] = i;
-    }
+    __builtin_amdgcn_wave_barrier();
+    if (lane < count) list[place] = c;
+    __builtin_amdgcn_wave_barrier();
+    return lane < count ? list[lane] : Candidate{-INFINITY, kNoIndex};
   }
+};
+
+// Sums over entries z of one row: m the largest entry, and with y = z L - k, L = log2 e
+// in binary32, k an integer at or above m L: s = sum 2^y, t = sum 2^y y, in binary64.
+// Sums of two sets are brought to one k by a power of two: exact, and no exponential.
+struct RowSums {
+  float m, k;
+  double s, t;
+
+  __device__ void none() {
+    m = k = -INFINITY;
+    s = t = 0.0;
+  }
+  __device__ void to(float kn) {
+    if (m == -INFINITY || kn == k) {
+      k = kn;
+      return;
+    }
+    const double d = (double)kn - (double)k;
+    const int e = (int)fmax(-d, -2000.0);
+    t = ldexp(t - d * s, e);
+    s = ldexp(s, e);
+    k = kn;
+  }
+};
+
+// Maximum and sum over a wave by lane shifts within the vector unit; valid in lane 63.
+template <int kCtrl, int kRows>
+__device__ __forceinline__ uint32_t shifted(uint32_t old, uint32_t x) {
+  return __builtin_amdgcn_update_dpp(old, x, kCtrl, kRows, 0xF, false);
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ float step_max(float m) {
+  return fmaxf(m, __uint_as_float(shifted<kCtrl, kRows>(__float_as_uint(m), __float_as_uint(m))));
+}
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double step_sum(double s) {
+  const uint64_t b = __double_as_longlong(s);
+  const uint64_t o = (uint64_t)shifted<kCtrl, kRows>(0u, (uint32_t)(b >> 32)) << 32 |
+                     shifted<kCtrl, kRows>(0u, (uint32_t)b);
+  return s + __longlong_as_double(o);
+}
+__device__ __forceinline__ float wave_max(float m) {  // in every lane
+  m = step_max<0x111, 0xF>(m);
+  m = step_max<0x112, 0xF>(m);
+  m = step_max<0x114, 0xF>(m);
+  m = step_max<0x118, 0xF>(m);
+  m = step_max<0x142, 0xA>(m);
+  m = step_max<0x143, 0xC>(m);
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(m), 63));
+}
+__device__ __forceinline__ double wave_sum(double s) {  // in lane 63
+  s = step_sum<0x111, 0xF>(s);
+  s = step_sum<0x112, 0xF>(s);
+  s = step_sum<0x114, 0xF>(s);
+  s = step_sum<0x118, 0xF>(s);
+  s = step_sum<0x142, 0xA>(s);
+  return step_sum<0x143, 0xC>(s);
+}
+// The lanes' sums as one; valid in lane 63.
+__device__ __forceinline__ void wave_sums(RowSums& b) {
+  b.m = wave_max(b.m);
+  const float k = wave_max(b.k);
+  if (b.k != -INFINITY) b.to(k);
+  b.k = k;
+  b.s = wave_sum(b.s);
+  b.t = wave_sum(b.t);
 }
 
-__device__ __forceinline__ float at_or_masked(const uint16_t* row, int v, int end) {
-  return v >= 0 && v < end ? bf16_at(row, v) : -INFINITY;
-}
-__device__ __forceinline__ float at_or_masked(const float* row, int v, int end) {
-  return v >= 0 && v < end ? row[v] : -INFINITY;
-}
-
-// Group g of a thread's entries in a step: 16 bytes, so that a wave's load
-// instruction covers one contiguous kilobyte.  `u` counts entries from the
-// 16-byte boundary at or before the row's start (`skew` entries before it): a
-// row may start at any element, and whole groups inside it are still aligned.
-__device__ __forceinline__ void load_step(const uint16_t* row, int u, int skew, int end, float* out) {
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    const int v = u + 2048 * g - skew;
-    if (v >= 0 && v + 8 <= end) {
-      const u32x4 a = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + v));
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        out[8 * g + 2 * i] = bf16_lo(w[i]);
-        out[8 * g + 2 * i + 1] = bf16_hi(w[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) out[8 * g + i] = at_or_masked(row, v + i, end);
-    }
-  }
-}
-__device__ __forceinline__ void load_step(const float* row, int u, int skew, int end, float* out) {
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const int v = u + 1024 * g - skew;
-    if (v >= 0 && v + 4 <= end) {
-      const f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row + v));
-      out[4 * g] = q.x;
-      out[4 * g + 1] = q.y;
-      out[4 * g + 2] = q.z;
-      out[4 * g + 3] = q.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) out[4 * g + i] = at_or_masked(row, v + i, end);
-    }
-  }
-}
 template <typename E>
-struct Group;
+struct Group;  // 16 bytes of a row
 template <>
 struct Group<uint16_t> {
-  static constexpr int size = 8, apart = 2048;
+  static constexpr int size = 8, count = kPer / size, apart = kThreads * size;
+  static constexpr uint32_t masked = 0xFF80FF80u;  // two entries of -inf
+  static __device__ __forceinline__ void unpack(u32x4 q, float* x) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = bf16_lo(w[i]);
+      x[2 * i + 1] = bf16_hi(w[i]);
+    }
+  }
 };
 template <>
 struct Group<float> {
-  static constexpr int size = 4, apart = 1024;
+  static constexpr int size = 4, count = kPer / size, apart = kThreads * size;
+  static constexpr uint32_t masked = 0xFF800000u;
+  static __device__ __forceinline__ void unpack(u32x4 q, float* x) {
+    x[0] = __uint_as_float(q.x);
+    x[1] = __uint_as_float(q.y);
+    x[2] = __uint_as_float(q.z);
+    x[3] = __uint_as_float(q.w);
+  }
 };
 
-// The row's results from its sums and best entries (one thread per alternative).
+// Group g of a thread's entries in a step lies g * apart behind entry u, so that a
+// wave's load instruction covers one contiguous kilobyte.  `u` counts entries from the
+// 16-byte boundary at or before the row's start (`skew` entries before it): a row may
+// start at any element, and whole groups inside it are still aligned.  Entries outside
+// the row are masked.
 template <typename E>
-__device__ __forceinline__ void finish(const LogprobArgs& a, int r, int id, const E* row,
-                                       const RowSums& sums, const float* tv, const int* ti) {
-  const double ln_s = log(sums.s);
-  const double lse = (double)sums.m + ln_s;  // NaN for a row without a finite entry
-  const bool none = sums.m == -INFINITY;
-  if (threadIdx.x == 0) {
-    a.logprob[r] = none ? NAN : (float)((double)elem_at(row, id) - lse);
-    a.entropy[r] = none ? NAN : (float)(ln_s - sums.t / sums.s);
+__device__ __forceinline__ void load_step(const E* row, int u, int skew, int end,
+                                          u32x4 (&q)[Group<E>::count]) {
+#pragma unroll
+  for (int g = 0; g < Group<E>::count; ++g) {
+    const int v = u + Group<E>::apart * g - skew;
+    if (v >= 0 && v + Group<E>::size <= end) {
+      q[g] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + v));
+    } else {
+      constexpr uint32_t none = Group<E>::masked;
+      union {
+        u32x4 q;
+        E e[Group<E>::size];
+      } part = {u32x4{none, none, none, none}};
+#pragma unroll
+      for (int i = 0; i < Group<E>::size; ++i)
+        if (v + i >= 0 && v + i < end) part.e[i] = row[v + i];
+      q[g] = part.q;
+    }
   }
-  for (int j = (int)threadIdx.x; j < a.n_top; j += kThreads) {
-    const bool there = ti[j] != kNoIndex;
-    a.top_ids[(int64_t)r * a.n_top + j] = there ? ti[j] : -1;
-    a.top_logprobs[(int64_t)r * a.n_top + j] =
-        none ? NAN : (there ? (float)((double)tv[j] - lse) : -INFINITY);
+}
+
+// The row's results, lane by lane: the sums, and the lane's alternative.  With
+// d = k - m L the sums are those of e^(z - m) times 2^-d, so that
+//   lse = m + ln s + d ln 2,  H = ln s + d ln 2 - (t / s + d) / L;
+// only |z - m| times the rounding of L remains.
+__device__ __forceinline__ void finish(const LogprobArgs& a, int r, float given, const RowSums& sums,
+                                       const Candidate& best) {
+  const int lane = (int)threadIdx.x & 63;
+  const bool none = sums.m == -INFINITY;  // no finite entry, no distribution
+  const double d = (double)sums.k - (double)sums.m * (double)kLog2e;
+  const double ln_s = log(sums.s) + d * 0.69314718055994530942;
+  const double lse = (double)sums.m + ln_s;
+  if (lane == 0) {
+    a.logprob[r] = none ? NAN : (float)((double)given - lse);
+    a.entropy[r] = none ? NAN : (float)(ln_s - (sums.t / sums.s + d) / (double)kLog2e);
+  }
+  if (lane < a.n_top) {
+    const bool there = best.i != kNoIndex;
+    a.top_ids[(int64_t)r * a.n_top + lane] = there ? best.i : -1;
+    a.top_logprobs[(int64_t)r * a.n_top + lane] =
+        none ? NAN : (there ? (float)((double)best.v - lse) : -INFINITY);
   }
 }
 
 __device__ __forceinline__ void skip(const LogprobArgs& a, int r) {
-  if (threadIdx.x == 0) {
+  const int lane = (int)threadIdx.x & 63;
+  if (lane == 0) {
     a.logprob[r] = NAN;
     a.entropy[r] = NAN;
   }
-  for (int j = (int)threadIdx.x; j < a.n_top; j += kThreads) {
-    a.top_ids[(int64_t)r * a.n_top + j] = -1;
-    a.top_logprobs[(int64_t)r * a.n_top + j] = NAN;
+  if (lane < a.n_top) {
+    a.top_ids[(int64_t)r * a.n_top + lane] = -1;
+    a.top_logprobs[(int64_t)r * a.n_top + lane] = NAN;
   }
 }
 
-// One workgroup per (row, vocabulary split).  With one split it finishes the
-// row; with more it leaves the split's sums and best entries to k_logprobs_join.
+// The waves' sums (each in its lane 63) and best entries joined; valid in wave 0.
+template <int kBits>
+__device__ __forceinline__ Candidate join_waves(WaveTop<kBits>& top, bool with_top, RowSums& b,
+                                                Candidate* room, RowSums* parts, int* counts) {
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  if (with_top) top.cut();
+  if (lane == 63) {
+    parts[wave] = b;
+    counts[wave] = with_top ? top.count : 0;
+  }
+  __syncthreads();
+  Candidate best = {-INFINITY, kNoIndex};
+  if (wave != 0) return best;
+  float m = parts[0].m, k = parts[0].k;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) {
+    m = fmaxf(m, parts[w].m);
+    k = fmaxf(k, parts[w].k);
+  }
+  b.m = m;
+  b.k = k;
+  b.s = b.t = 0.0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    RowSums part = parts[w];
+    if (part.m == -INFINITY) continue;
+    part.to(k);
+    b.s += part.s;
+    b.t += part.t;
+  }
+  if (with_top) {
+    for (int w = 1; w < kWaves; ++w) {
+      const Candidate c = lane < counts[w] ? room[w * kRoom + lane] : Candidate{-INFINITY, kNoIndex};
+      top.add(c.v, c.i);
+      if (top.count > kCut) top.cut();
+    }
+    best = top.sorted();
+  }
+  return best;
+}
+
+// One workgroup per (row, vocabulary split).  With one split it finishes the row; with
+// more it leaves the split's sums and best entries to k_logprobs_join.
 template <typename E, bool kTop>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
-  __shared__ RowSums sums;
-  __shared__ float tv[64];
-  __shared__ int ti[64];
   __shared__ Candidate room[kTop ? kWaves * kRoom : 1];
+  __shared__ float published[kWaves];
+  __shared__ RowSums parts[kWaves];
+  __shared__ int counts[kWaves];
   const int r = (int)blockIdx.x;
   const int split = (int)blockIdx.y;
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
   const int id = a.ids[r];
   if (id < 0 || id >= a.V) {
-    if (a.nsplit == 1) skip(a, r);
+    if (a.nsplit == 1 && wave == 0) skip(a, r);
     return;
   }
   const E* row = static_cast<const E*>(a.logits) + (int64_t)r * a.ld;
   const int skew = (int)(((uintptr_t)row / sizeof(E)) & (Group<E>::size - 1));
   const int u0 = split * a.chunk;  // a whole number of steps
   const int u1 = min(a.V + skew, u0 + a.chunk);
+  const int ul = Group<E>::size * (int)threadIdx.x;
+  const float given = elem_at(row, id);
+  u32x4 q[Group<E>::count];
+  load_step(row, u0 + ul, skew, u1 - skew, q);
   WaveTop<8 * (int)sizeof(E)> top;
-  if (kTop) top.start(room + ((int)threadIdx.x >> 6) * kRoom, a.n_top);
-  // Running sums s = sum 2^y, t = sum 2^y y with y = z L - K, against an integer
-  // reference K >= max z L that only rises: each exponent is one fma and a rise
-  // rescales by an exact power of two.  y is held above -200, where 2^y is zero
-  // in binary32, so that masked entries add 0 and not 0 * inf.
-  float m = -INFINITY, kf = 0.f;
-  double s = 0.0, t = 0.0;
+  if (kTop) {
+    top.start(room + wave * kRoom, published, a.n_top);
+    if (threadIdx.x < kWaves) published[threadIdx.x] = -INFINITY;
+    __syncthreads();
+  }
+  // Running sums: each exponent is one fma against a reference k that only rises, by
+  // an exact power of two.  y is held above -200, where 2^y is zero in binary32, so that
+  // masked entries add 0 and not 0 * inf.
+  RowSums b;
+  b.none();
+  int steps = 0;
   for (int u = u0; u < u1; u += kStep) {
     float x[kPer];
-    const int ul = u + Group<E>::size * (int)threadIdx.x;
-    load_step(row, ul, skew, u1 - skew, x);
-    float mt = x[0];
 #pragma unroll
-    for (int j = 1; j < kPer; ++j) mt = fmaxf(mt, x[j]);
-    if (mt > m) {
+    for (int g = 0; g < Group<E>::count; ++g) Group<E>::unpack(q[g], x + g * Group<E>::size);
+    // the next step's entries are on their way while this one is worked on
+    if (u + kStep < u1) load_step(row, u + kStep + ul, skew, u1 - skew, q);
+    if (kTop) top.step();
+    float m4[4];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) m4[g] = fmaxf(fmaxf(x[4 * g], x[4 * g + 1]), fmaxf(x[4 * g + 2], x[4 * g + 3]));
+    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    if (mt > b.m) {
       const float kn = ceilf(mt * kLog2e);
-      if (m != -INFINITY && kn > kf) {
-        const double d = (double)kn - (double)kf;
-        const int e = (int)fmax(-d, -2000.0);
-        t = ldexp(t - d * s, e);
-        s = ldexp(s, e);
-      }
-      if (m == -INFINITY || kn > kf) kf = kn;
-      m = mt;
+      if (kn > b.k) b.to(kn);
+      b.m = mt;
     }
-    if (m != -INFINITY) {
-      float e[kPer], y[kPer];
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        y[j] = fmaxf(fmaf(x[j], kLog2e, -kf), -200.f);
-        e[j] = __builtin_amdgcn_exp2f(y[j]);
-      }
+    if (b.m != -INFINITY) {
       float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
-        s4[j & 3] += e[j];
-        t4[j & 3] = fmaf(e[j], y[j], t4[j & 3]);
+        const float y = fmaxf(fmaf(x[j], kLog2e, -b.k), -200.f);
+        const float e = __builtin_amdgcn_exp2f(y);
+        s4[j & 3] += e;
+        t4[j & 3] = fmaf(e, y, t4[j & 3]);
       }
-      s += (double)((s4[0] + s4[1]) + (s4[2] + s4[3]));
-      t += (double)((t4[0] + t4[1]) + (t4[2] + t4[3]));
+      b.s += (double)((s4[0] + s4[1]) + (s4[2] + s4[3]));
+      b.t += (double)((t4[0] + t4[1]) + (t4[2] + t4[3]));
     }
     if (kTop) {
-      top.step();
-      if (__ballot(mt > top.bar)) {
+      if (ballot(mt > top.bar)) {
         if (top.bar == -INFINITY) top.first_bar(mt);
 #pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          top.add(x[j], ul + (j / Group<E>::size) * Group<E>::apart + (j % Group<E>::size) - skew);
+        for (int g = 0; g < 4; ++g) {
+          if (ballot(m4[g] > top.bar)) {
+#pragma unroll
+            for (int j = 4 * g; j < 4 * g + 4; ++j)
+              top.add(x[j], u + ul + (j / Group<E>::size) * Group<E>::apart + (j % Group<E>::size) - skew);
+            if (top.count > kCut) top.cut();
+          }
+        }
       }
+      // after steps 1, 2, 4, 8, ...: between them the bar falls behind by half at most
+      ++steps;
+      if ((steps & (steps - 1)) == 0) top.publish(wave);
     }
   }
-  const RowSums b = block_sums(m, kf, s, t);
-  if (threadIdx.x == 0) sums = b;
-  if (kTop) block_top(top, a.n_top, tv, ti);
-  __syncthreads();
+  wave_sums(b);
+  const Candidate best = join_waves(top, kTop, b, room, parts, counts);
+  if (wave != 0) return;
   if (a.nsplit == 1) {
-    finish(a, r, id, row, sums, tv, ti);
+    finish(a, r, given, b, best);
     return;
   }
   const int64_t o = (int64_t)r * a.nsplit + split;
-  if (threadIdx.x == 0) {
-    a.part_m[o] = sums.m;
-    a.part_st[2 * o] = sums.s;
-    a.part_st[2 * o + 1] = sums.t;
+  if (lane == 0) {
+    a.part_mk[2 * o] = b.m;
+    a.part_mk[2 * o + 1] = b.k;
+    a.part_st[2 * o] = b.s;
+    a.part_st[2 * o + 1] = b.t;
   }
-  if (kTop && (int)threadIdx.x < a.n_top) {
-    a.part_v[o * a.n_top + threadIdx.x] = tv[threadIdx.x];
-    a.part_i[o * a.n_top + threadIdx.x] = ti[threadIdx.x];
+  if (kTop && lane < a.n_top) {  // place by place, so that the splits' best come first
+    const int64_t p = ((int64_t)r * a.n_top + lane) * a.nsplit + split;
+    a.part_v[p] = best.v;
+    a.part_i[p] = best.i;
   }
 }
 
 // One workgroup per row: joins the splits' sums and best entries.
 template <typename E, bool kTop>
 __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
-  __shared__ RowSums part[kWaves];
-  __shared__ RowSums sums;
-  __shared__ float tv[64];
-  __shared__ int ti[64];
   __shared__ Candidate room[kTop ? kWaves * kRoom : 1];
+  __shared__ float published[kWaves];
+  __shared__ RowSums parts[kWaves];
+  __shared__ int counts[kWaves];
   const int r = (int)blockIdx.x;
   const int id = a.ids[r];
+  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
   if (id < 0 || id >= a.V) {
-    skip(a, r);
+    if (wave == 0) skip(a, r);
     return;
   }
-  const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
   const int64_t o = (int64_t)r * a.nsplit;
-  RowSums b = {-INFINITY, 0.0, 0.0};
-  for (int j = (int)threadIdx.x; j < a.nsplit; j += kThreads)
-    join(b, RowSums{a.part_m[o + j], a.part_st[2 * (o + j)], a.part_st[2 * (o + j) + 1]});
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    // the pair's lower lane goes first on both sides, so that they agree
-    RowSums lo = b, hi;
-    hi.m = __shfl_xor(b.m, off, 64);
-    hi.s = __shfl_xor(b.s, off, 64);
-    hi.t = __shfl_xor(b.t, off, 64);
-    if (lane & off) {
-      lo = hi;
-      hi = b;
-    }
-    join(lo, hi);
-    b = lo;
+  const float given = elem_at(static_cast<const E*>(a.logits) + (int64_t)r * a.ld, id);
+  RowSums b;
+  b.none();
+  for (int j = (int)threadIdx.x; j < a.nsplit; j += kThreads) {
+    RowSums p = {a.part_mk[2 * (o + j)], a.part_mk[2 * (o + j) + 1], a.part_st[2 * (o + j)],
+                 a.part_st[2 * (o + j) + 1]};
+    if (p.m == -INFINITY) continue;
+    const float k = fmaxf(b.k, p.k);
+    p.to(k);
+    b.to(k);
+    b.m = fmaxf(b.m, p.m);
+    b.s += p.s;
+    b.t += p.t;
   }
-  if (lane == 0) part[wave] = b;
+  wave_sums(b);
+  WaveTop<8 * (int)sizeof(E)> top;
   if (kTop) {
-    // the splits' entries, a wave's share of the splits at a time; an entry that equals
-    // the n-th best may still come with a lower index, so that no step is ever begun
-    WaveTop<8 * (int)sizeof(E)> top;
-    top.start(room + wave * kRoom, a.n_top);
+    // a wave's share of the entries; they come in no order, so that one that equals the
+    // n-th best may still have a lower index: the bar is never made exact
+    top.start(room + wave * kRoom, published, a.n_top);
     const int total = a.nsplit * a.n_top;
     const float* pv = a.part_v + o * a.n_top;
     const int* pi = a.part_i + o * a.n_top;
     for (int c = 64 * wave; c < total; c += kThreads) {
       const int e = c + lane;
       const float x = e < total ? pv[e] : -INFINITY;
+      if (c < kThreads) top.first_bar(x);
       top.add(x, e < total ? pi[e] : kNoIndex);
+      if (top.count > kCut) top.cut();
     }
-    block_top(top, a.n_top, tv, ti);
   }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < kWaves; ++w) join(b, part[w]);
-    sums = b;
-  }
-  __syncthreads();
-  const E* row = static_cast<const E*>(a.logits) + (int64_t)r * a.ld;
-  finish(a, r, id, row, sums, tv, ti);
+  const Candidate best = join_waves(top, kTop, b, room, parts, counts);
+  if (wave != 0) return;
+  finish(a, r, given, b, best);
 }
 
 __global__ __launch_bounds__(256) void k_emitted(int R, int gamma, const int32_t* tokens,
