@@ -471,8 +471,8 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
     if (kTop) top.step();
     float m4[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) m4[g] = fmaxf(fmaxf(x[4 * g], x[4 * g + 1]), fmaxf(x[4 * g + 2], x[4 * g + 3]));
-    const float mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    for (int g = 0; g < 4; ++g) m4[g] = fmaxf(fmaxf(fmaxf(x[4 * g], x[4 * g + 1]), x[4 * g + 2]), x[4 * g + 3]);
+    const float mt = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), m4[2]), m4[3]);
     if (mt > b.m) {
       const float kn = ceilf(mt * kLog2e);
       if (kn > b.k) b.to(kn);
