@@ -66,12 +66,15 @@ class PagedCache:
         self.K, self.V, self.device = K, V, K.device
         self.slots, self.max_pages, self.pages, self.page_size = slots, max_pages, pages, page
         self.layers, self.kv_heads, self.head_dim, self.dtype = layers, heads, chunks * e, K.dtype
+        self._index = K.get_device()
         self._tables = self._table_ptrs(tables)
+        self._t = ctypes.byref(self._tables)
         for n in TABLES:
             setattr(self, n, tables[n])
         self._c = dspark.Cache(slots, max_pages, pages, page, layers, heads, chunks * e,
                                dspark._DTYPES[K.dtype])
-        if dspark.lib().dspark_cache_compact_workspace_bytes(ctypes.byref(self._c)) == 0:
+        self._p = ctypes.byref(self._c)
+        if dspark.lib().dspark_cache_compact_workspace_bytes(self._p) == 0:
             dspark._check(-2)
 
     def _table_ptrs(self, tables):
@@ -80,9 +83,7 @@ class PagedCache:
         return dspark.CacheTables(*(tables[n].data_ptr() for n in TABLES))
 
     def _need(self, t, name, dtype, shape):
-        dspark._need(t, name, dtype=dtype, shape=shape)
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+        dspark._need_on(self._index, t, name, dtype, shape)
 
     def _ints(self, *shape):
         return torch.empty(shape, dtype=torch.int32, device=self.device)
@@ -90,13 +91,12 @@ class PagedCache:
     def tables(self) -> dict:
         return {n: getattr(self, n) for n in TABLES}
 
-    def _call(self, name, *args):
-        with dspark._on(self.device):
-            dspark._check(getattr(dspark.lib(), name)(ctypes.byref(self._c), *args, dspark._stream()))
+    def _call(self, fn, *args):
+        dspark._call_on(self._index, fn, self._p, *args)
 
     def clear(self):
         """Empty tables (dspark_cache_init)."""
-        self._call("dspark_cache_init", ctypes.byref(self._tables))
+        self._call(dspark.lib().dspark_cache_init, self._t)
 
     def fork(self, src, dst):
         """Slots dst [n] get the tokens of slots src [n] by sharing pages
@@ -105,8 +105,8 @@ class PagedCache:
         self._need(src, "src", torch.int32, (n,))
         self._need(dst, "dst", torch.int32, (n,))
         status = self._ints(n)
-        self._call("dspark_cache_fork", ctypes.byref(self._tables), n, dspark._ptr(src),
-                   dspark._ptr(dst), dspark._ptr(status))
+        self._call(dspark.lib().dspark_cache_fork, self._t, n, src.data_ptr(),
+                   dst.data_ptr(), status.data_ptr())
         return status
 
     def reserve(self, add, out=None):
@@ -115,27 +115,26 @@ class PagedCache:
         status, cow_src and cow_dst [slots]; ``out`` may supply it."""
         self._need(add, "add", torch.int32, (self.slots,))
         if out is None:
-            r = self._ints(3, self.slots)
-            out = {"status": r[0], "cow_src": r[1], "cow_dst": r[2]}
+            out = dict(zip(("status", "cow_src", "cow_dst"), self._ints(3, self.slots).unbind(0)))
         else:
             for name in ("status", "cow_src", "cow_dst"):
                 self._need(out[name], name, torch.int32, (self.slots,))
-        self._call("dspark_cache_reserve", ctypes.byref(self._tables), dspark._ptr(add),
-                   dspark._ptr(out["status"]), dspark._ptr(out["cow_src"]), dspark._ptr(out["cow_dst"]))
-        self.copy_pages(out["cow_src"], out["cow_dst"])
+        self._call(dspark.lib().dspark_cache_reserve, self._t, add.data_ptr(),
+                   out["status"].data_ptr(), out["cow_src"].data_ptr(), out["cow_dst"].data_ptr())
+        self._copy(self.slots, out["cow_src"], out["cow_dst"], None)
         return out
 
     def commit(self, keep, plus: int = 0):
         """lens += keep + plus, pages behind the new lengths released
         (dspark_cache_commit)."""
         self._need(keep, "keep", torch.int32, (self.slots,))
-        self._call("dspark_cache_commit", ctypes.byref(self._tables), dspark._ptr(keep), plus)
+        self._call(dspark.lib().dspark_cache_commit, self._t, keep.data_ptr(), plus)
 
     def free(self, slots):
         """Releases the listed slots (dspark_cache_free)."""
         n = slots.numel()
         self._need(slots, "slots", torch.int32, (n,))
-        self._call("dspark_cache_free", ctypes.byref(self._tables), n, dspark._ptr(slots))
+        self._call(dspark.lib().dspark_cache_free, self._t, n, slots.data_ptr())
 
     def copy_pages(self, src, dst, count=None):
         """Copies pages src [n] to dst [n] in every layer (dspark_cache_copy_pages);
@@ -145,24 +144,27 @@ class PagedCache:
         self._need(dst, "dst", torch.int32, (n,))
         if count is not None:
             self._need(count, "count", torch.int32, (1,))
-        self._call("dspark_cache_copy_pages", dspark._ptr(self.K), dspark._ptr(self.V), n,
-                   dspark._ptr(src), dspark._ptr(dst), dspark._ptr(count))
+        self._copy(n, src, dst, count)
+
+    def _copy(self, n, src, dst, count):
+        self._call(dspark.lib().dspark_cache_copy_pages, self.K.data_ptr(), self.V.data_ptr(), n,
+                   src.data_ptr(), dst.data_ptr(), None if count is None else count.data_ptr())
 
     def compact(self, into=None, ws=None):
         """Moves the used pages to the front of the pool (dspark_cache_compact) and
         copies them.  ``into``: a dict of other tables that receive the new state, while
         this cache's own stay valid for rounds in flight; by default its own change.
         Returns a dict of the moves: src, dst [pages], n_moves [1]."""
-        new = self._tables if into is None else self._table_ptrs(into)
+        new = self._t if into is None else ctypes.byref(self._table_ptrs(into))
         if ws is None:
-            n = dspark.lib().dspark_cache_compact_workspace_bytes(ctypes.byref(self._c))
+            n = dspark.lib().dspark_cache_compact_workspace_bytes(self._p)
             ws = torch.empty(n, dtype=torch.uint8, device=self.device)
-        r = self._ints(2, self.pages)
-        out = {"src": r[0], "dst": r[1], "n_moves": self._ints(1)}
-        self._call("dspark_cache_compact", ctypes.byref(self._tables), ctypes.byref(new),
-                   dspark._ptr(out["src"]), dspark._ptr(out["dst"]), dspark._ptr(out["n_moves"]),
-                   dspark._ptr(ws), ws.numel())
-        self.copy_pages(out["src"], out["dst"], out["n_moves"])
+        src, dst = self._ints(2, self.pages).unbind(0)
+        out = {"src": src, "dst": dst, "n_moves": self._ints(1)}
+        self._call(dspark.lib().dspark_cache_compact, self._t, new,
+                   out["src"].data_ptr(), out["dst"].data_ptr(), out["n_moves"].data_ptr(),
+                   *dspark._ws_on(self._index, ws))
+        self._copy(self.pages, src, dst, out["n_moves"])
         return out
 
     def append(self, layer: int, k, v, offsets):
@@ -172,12 +174,12 @@ class PagedCache:
         self._need(k, "k", self.dtype, (N, self.kv_heads, self.head_dim))
         self._need(v, "v", self.dtype, (N, self.kv_heads, self.head_dim))
         self._need(offsets, "offsets", torch.int32, (self.slots + 1,))
-        self._call("dspark_cache_append", ctypes.byref(self._tables), layer, dspark._ptr(self.K),
-                   dspark._ptr(self.V), N, dspark._ptr(k), dspark._ptr(v), dspark._ptr(offsets))
+        self._call(dspark.lib().dspark_cache_append, self._t, layer, self.K.data_ptr(),
+                   self.V.data_ptr(), N, k.data_ptr(), v.data_ptr(), offsets.data_ptr())
 
     def attend_workspace(self, N: int, heads: int):
         """Workspace of attend for N rows of q."""
-        n = dspark.lib().dspark_attend_workspace_bytes(ctypes.byref(self._c), N, heads)
+        n = dspark.lib().dspark_attend_workspace_bytes(self._p, N, heads)
         if n == 0:
             dspark._check(-2)
         return torch.empty(n, dtype=torch.uint8, device=self.device)
@@ -193,11 +195,12 @@ class PagedCache:
         self._need(offsets, "offsets", torch.int32, (self.slots + 1,))
         if out is None:
             out = torch.empty_like(q)
-        self._need(out, "out", self.dtype, tuple(q.shape))
+        else:
+            self._need(out, "out", self.dtype, q.shape)
         if ws is None:
             ws = self.attend_workspace(N, heads)
-        self._call("dspark_attend", ctypes.byref(self._tables), layer, dspark._ptr(self.K),
-                   dspark._ptr(self.V), N, heads, dspark._ptr(q), dspark._ptr(offsets),
-                   self.head_dim ** -0.5 if scale is None else scale, max_chunk or N,
-                   dspark._ptr(out), dspark._ptr(ws), ws.numel())
+        self._call(dspark.lib().dspark_attend, self._t, layer, self.K.data_ptr(),
+                   self.V.data_ptr(), N, heads, q.data_ptr(), offsets.data_ptr(),
+                   self.head_dim ** -0.5 if scale is None else scale, N if max_chunk is None else max_chunk,
+                   out.data_ptr(), *dspark._ws_on(self._index, ws))
         return out

@@ -7,7 +7,6 @@ library has not been built this module raises instead of falling back.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -141,24 +140,46 @@ def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _on(device):
-    """The context in which calls go to `device` (none needed if it is the current one)."""
-    if device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _call_on(index: int, fn, *args):
+    """Calls an entry point with the current stream of device `index` as its last
+    argument, that device current.  For calls whose launch costs less than its Python
+    around it: the raw stream is looked up without a torch.cuda.Stream object, and the
+    device is switched only if another one is current."""
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _check(status)
 
 
 def _need(t, name, dtype=None, shape=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on the GPU")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_on(index, t, name, dtype, shape):
+    """_need, on device `index` too."""
+    _need(t, name, dtype, shape)
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on device {index}, got {t.device}")
+
+
+def _ws_on(index, ws):
+    """Address and bytes of a workspace on device `index`."""
+    _need(ws, "ws")
+    if ws.get_device() != index:
+        raise ValueError(f"ws must be on device {index}, got {ws.device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def problem(R: int, gamma: int, V: int, dtype: torch.dtype, seed: int, rank: int = 256) -> Problem:
@@ -467,14 +488,15 @@ def emitted_tokens(tokens, n_accept, out_token, out=None):
     gamma + 1], -1 behind each request's last one."""
     R, gamma = tokens.shape
     _need(tokens, "tokens", dtype=torch.int32)
-    _need(n_accept, "n_accept", dtype=torch.int32, shape=(R,))
-    _need(out_token, "out_token", dtype=torch.int32, shape=(R,))
+    dev = tokens.get_device()
+    _need_on(dev, n_accept, "n_accept", torch.int32, (R,))
+    _need_on(dev, out_token, "out_token", torch.int32, (R,))
     if out is None:
         out = torch.empty((R, gamma + 1), dtype=torch.int32, device=tokens.device)
-    _need(out, "out", dtype=torch.int32, shape=(R, gamma + 1))
-    with _on(tokens.device):
-        _check(lib().dspark_emitted_tokens(R, gamma, _ptr(tokens), _ptr(n_accept), _ptr(out_token),
-                                           _ptr(out), _stream()))
+    else:
+        _need_on(dev, out, "out", torch.int32, (R, gamma + 1))
+    _call_on(dev, lib().dspark_emitted_tokens, R, gamma, tokens.data_ptr(), n_accept.data_ptr(),
+             out_token.data_ptr(), out.data_ptr())
     return out
 
 
@@ -490,39 +512,36 @@ def token_logprobs(logits, ids, n_top: int = 0, ws=None, out=None):
     [N, V] with rows any distance >= V apart; ids [...] int32 (outside [0, V): the
     row is skipped).  Returns a dict of logprob and entropy [...] fp32, top_ids
     int32 and top_logprobs fp32 [..., n_top]; ``out`` may supply it preallocated."""
-    if not isinstance(logits, torch.Tensor) or logits.device.type != "cuda":
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
         raise ValueError("logits must be a torch.Tensor on the GPU")
-    if logits.dtype not in _DTYPES:
+    dtype = _DTYPES.get(logits.dtype)
+    if dtype is None:
         raise ValueError(f"dtype must be float32 or bfloat16, got {logits.dtype}")
     if logits.dim() < 2:
         raise ValueError("logits must have shape [..., V]")
-    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
-    N = ids.numel()
-    if logits.dim() == 2 and logits.stride(1) == 1 and logits.stride(0) >= V:
+    *lead, V = logits.shape
+    lead = tuple(lead)
+    ld = V
+    if not logits.is_contiguous():
+        if logits.dim() != 2 or logits.stride(1) != 1 or logits.stride(0) < V:
+            raise ValueError("logits must be contiguous, or [N, V] with rows at least V apart")
         ld = logits.stride(0)
-    else:
-        _need(logits, "logits")
-        ld = V
-    _need(ids, "ids", dtype=torch.int32, shape=lead)
-    dev = logits.device
-    if ids.device != dev:
-        raise ValueError("ids must be on the device of logits")
+    index, dev = logits.get_device(), logits.device
+    _need_on(index, ids, "ids", torch.int32, lead)
+    N = ids.numel()
     if out is None:
         out = {"logprob": torch.empty(lead, dtype=torch.float32, device=dev),
                "entropy": torch.empty(lead, dtype=torch.float32, device=dev),
                "top_ids": torch.empty((*lead, n_top), dtype=torch.int32, device=dev),
                "top_logprobs": torch.empty((*lead, n_top), dtype=torch.float32, device=dev)}
-    for name, dt, shape in (("logprob", torch.float32, lead), ("entropy", torch.float32, lead),
-                            ("top_ids", torch.int32, (*lead, n_top)),
-                            ("top_logprobs", torch.float32, (*lead, n_top))):
-        _need(out[name], name, dtype=dt, shape=shape)
-        if out[name].device != dev:
-            raise ValueError(f"{name} must be on the device of logits")
-    with _on(dev):
-        if ws is None:
-            ws = logprobs_workspace(N, V, n_top, dev)
-        _check(lib().dspark_token_logprobs(_DTYPES[logits.dtype], N, V, ld, _ptr(logits), _ptr(ids),
-                                           n_top, _ptr(out["logprob"]), _ptr(out["entropy"]),
-                                           _ptr(out["top_ids"]), _ptr(out["top_logprobs"]),
-                                           _ptr(ws), ws.numel(), _stream()))
+    else:
+        for name, dt, shape in (("logprob", torch.float32, lead), ("entropy", torch.float32, lead),
+                                ("top_ids", torch.int32, (*lead, n_top)),
+                                ("top_logprobs", torch.float32, (*lead, n_top))):
+            _need_on(index, out[name], name, dt, shape)
+    if ws is None:
+        ws = logprobs_workspace(N, V, n_top, dev)
+    _call_on(index, lib().dspark_token_logprobs, dtype, N, V, ld, logits.data_ptr(), ids.data_ptr(),
+             n_top, out["logprob"].data_ptr(), out["entropy"].data_ptr(), out["top_ids"].data_ptr(),
+             out["top_logprobs"].data_ptr(), *_ws_on(index, ws))
     return out
