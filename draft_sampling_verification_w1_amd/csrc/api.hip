@@ -255,10 +255,10 @@ int check_cache(const dspark_cache* c) {
     return fail(DSPARK_ERR_SHAPE, "page_size=%d is not 16, 32, 64, 128 or 256", c->page_size);
   if (c->max_pages < 1 || c->max_pages > (1 << 20) ||
       (int64_t)c->slots * c->max_pages > (1 << 30) ||
-      (int64_t)c->max_pages * c->page_size >= ((int64_t)1 << 31))
+      (int64_t)c->max_pages * c->page_size > (1 << 30))
     return fail(DSPARK_ERR_SHAPE,
                 "max_pages=%d outside [1, 2^20], or slots*max_pages above 2^30, or "
-                "max_pages*page_size at 2^31 or above",
+                "max_pages*page_size above 2^30",
                 c->max_pages);
   if (c->layers < 1 || c->layers > 1024 || c->kv_heads < 1 || c->kv_heads > 1024)
     return fail(DSPARK_ERR_SHAPE, "layers=%d, kv_heads=%d outside [1, 1024]", c->layers, c->kv_heads);

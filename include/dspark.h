@@ -314,7 +314,7 @@ int dspark_token_logprobs(int32_t dtype, int32_t N, int32_t V, int64_t ld, const
  * an invalid page holds no keys, and what would be written to it is dropped.
  * Limits: 1 <= slots <= 4096, 1 <= pages <= 2^24, page_size 16, 32, 64, 128 or
  * 256, 1 <= max_pages <= 2^20, slots * max_pages <= 2^30, max_pages * page_size
- * < 2^31, 1 <= layers, kv_heads <= 1024, head_dim 64, 128 or 256. */
+ * <= 2^30, 1 <= layers, kv_heads <= 1024, head_dim 64, 128 or 256. */
 typedef struct {
   int32_t slots;
   int32_t max_pages;
