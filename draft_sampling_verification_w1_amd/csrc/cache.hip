@@ -184,7 +184,7 @@ __global__ __launch_bounds__(kBig) void k_cache_reserve(CacheArgs a, const int32
     int t = -1;
     if (add[s] > 0) {
       const int len = a.t.lens[s], j = len >> a.page_shift;
-      if ((len & (page - 1)) != 0 && j < min(a.t.held[s], a.max_pages)) {
+      if (len > 0 && (len & (page - 1)) != 0 && j < min(a.t.held[s], a.max_pages)) {
         const int p = a.t.table[(int64_t)s * a.max_pages + j];
         if (page_ok(a, p) && a.t.refs[p] > 1) t = p;
       }

@@ -203,3 +203,15 @@ def test_replayed_round(C):
         m.commit(k, 1)
         same(c, m)
         np.testing.assert_array_equal(out["status"].cpu().numpy(), st[0])
+
+
+def test_impossible_lengths(C):
+    """Negative lengths in the tables index nothing: no page is taken or looked at."""
+    c = C.PagedCache(3, 4, 8, 16, 1, 1, 64)
+    c.reserve(ints([20, 20, 0]))
+    c.lens.copy_(ints([-5, -100000, -1]))
+    r = c.reserve(ints([3, 3, 3]))
+    assert r["status"].tolist() == [0, 0, 0] and r["cow_src"].tolist() == [-1, -1, -1]
+    assert c.held.tolist() == [2, 2, 1] and c.n_free.tolist() == [3]
+    c.commit(ints([0, 0, 0]))
+    assert c.lens.tolist() == [0, 0, 0] and c.n_free.tolist() == [8]
