@@ -350,7 +350,8 @@ int dspark_cache_fork(const dspark_cache* c, const dspark_cache_tables* t, int32
  * alone; lens does not change).  A slot whose next token falls into a page that it
  * shares gets a page of its own for it: cow_src[s], cow_dst[s] name the copy to
  * make (dspark_cache_copy_pages, before the next reserve), -1 for none; when
- * every sharer of the page is served in the call, the lowest slot keeps it.
+ * every sharer of the page has an add[s] > 0, the one with the most tokens in it (the
+ * lowest slot of several) keeps it: it writes behind the tokens of all others.
  * status[s]: 0; 1 out of pages (slots are served in order until one does not
  * fit; it and the later ones that need pages get none); 2 the table row is too
  * short (the slot gets none).  A slot with a status other than 0 must not

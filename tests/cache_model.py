@@ -46,7 +46,9 @@ class CacheModel:
                 status[s] = 2
                 continue
             p = tails[s]
-            copy = p >= 0 and not (tails.count(p) == refs[p] and tails.index(p) == s)
+            # the writer with the most tokens in the page keeps it, if all who share it write
+            longest = max((q for q in range(self.S) if tails[q] == p), key=lambda q: (self.lens[q], -q))
+            copy = p >= 0 and not (tails.count(p) == refs[p] and longest == s)
             want = max(0, upto - len(self.rows[s])) + copy
             if want and (full or taken + want > len(free)):
                 status[s], full = 1, True

@@ -215,3 +215,30 @@ def test_impossible_lengths(C):
     assert c.held.tolist() == [2, 2, 1] and c.n_free.tolist() == [3]
     c.commit(ints([0, 0, 0]))
     assert c.lens.tolist() == [0, 0, 0] and c.n_free.tolist() == [8]
+
+
+@pytest.mark.parametrize("first", [0, 1])
+def test_shared_page_of_a_refused_slot(C, first):
+    """Two slots share a page and both want to write to it, but one of them, with more
+    tokens in the page, gets nothing (its row is too short): the other one must not
+    write over its tokens."""
+    import torch
+    a, b = first, 1 - first
+    c = C.PagedCache(2, 2, 8, 16, 1, 1, 64, torch.float32)
+    c.reserve(ints([9 if s == b else 0 for s in range(2)]))
+    k = torch.arange(9 * 64, dtype=torch.float32, device="cuda").view(9, 1, 64)
+    c.append(0, k, k, ints([0, 0, 9] if b else [0, 9, 9]))
+    c.commit(ints([9 if s == b else 0 for s in range(2)]))
+    assert c.fork(ints([b]), ints([a])).tolist() == [0]
+    c.commit(ints([-4 if s == a else -2 ** 31 for s in range(2)]))
+    page = int(c.table[b, 0])
+    before = c.K[0, page].clone(), c.V[0, page].clone()
+    r = c.reserve(ints([1 if s == a else 100 for s in range(2)]))
+    assert r["status"][a] == 0 and r["status"][b] == 2
+    assert r["cow_src"][a] == page and c.table[a, 0] != page
+    one = -torch.ones((1, 1, 64), device="cuda")
+    c.append(0, one, one, ints([0, 1, 1] if a == 0 else [0, 0, 1]))
+    # (positions 9 to 15 of the page belong to nobody)
+    seen = lambda K, V: (K.view(16, 16, 4)[:, :9], V.view(4, 64, 4).transpose(1, 2).reshape(16, 64)[:9])  # noqa: E731
+    for x, y in zip(seen(c.K[0, page], c.V[0, page]), seen(*before)):
+        assert torch.equal(x, y)
