@@ -228,9 +228,10 @@ struct LogprobLayout {
   size_t m, st, v, i, bytes;
 };
 
-LogprobLayout logprob_layout(int N, int V, int n_top) {
+// skew: the most entries that a row starts behind a 16-byte boundary.
+LogprobLayout logprob_layout(int N, int V, int n_top, int skew) {
   LogprobLayout L = {};
-  L.nsplit = logprob_splits(N, V, &L.chunk);
+  L.nsplit = logprob_splits(N, V, skew, &L.chunk);
   if (L.nsplit == 1) return L;
   const size_t n = (size_t)N * L.nsplit;
   Carver c;
@@ -916,7 +917,12 @@ __attribute__((visibility("default"))) int dspark_emitted_tokens(
 __attribute__((visibility("default"))) size_t dspark_logprobs_workspace_bytes(int32_t N, int32_t V,
                                                                              int32_t n_top) {
   if (check_logprobs_shape(N, V, n_top) != DSPARK_OK) return 0;
-  return logprob_layout(N, V, n_top).bytes;
+  size_t most = 0;  // whatever start and stride the rows have
+  for (int skew : {0, 3, 7}) {
+    const size_t n = logprob_layout(N, V, n_top, skew).bytes;
+    most = most > n ? most : n;
+  }
+  return most;
 }
 
 __attribute__((visibility("default"))) int dspark_token_logprobs(
@@ -931,7 +937,9 @@ __attribute__((visibility("default"))) int dspark_token_logprobs(
     return fail(DSPARK_ERR_ARG, "token_logprobs: tensor pointers must be non-NULL");
   if ((uintptr_t)logits % (dtype == DSPARK_BF16 ? 2 : 4))
     return fail(DSPARK_ERR_ARG, "token_logprobs: logits must be aligned to their element size");
-  const LogprobLayout L = logprob_layout(N, V, n_top);
+  const int64_t size = dtype == DSPARK_BF16 ? 2 : 4;
+  const bool even = aligned16(logits) && (N == 1 || ld * size % 16 == 0);
+  const LogprobLayout L = logprob_layout(N, V, n_top, even ? 0 : (int)(16 / size) - 1);
   if (L.bytes)
     if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
   LogprobArgs a = {};

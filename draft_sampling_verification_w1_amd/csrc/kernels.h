@@ -287,7 +287,7 @@ struct LogprobArgs {
   float* part_v;         // [N * nsplit * n_top] its best entries, best of every split first
   int32_t* part_i;
 };
-int logprob_splits(int N, int V, int* chunk);
+int logprob_splits(int N, int V, int skew, int* chunk);
 hipError_t launch_logprobs(bool bf16, const LogprobArgs& a, hipStream_t stream);
 hipError_t launch_emitted(int R, int gamma, const int32_t* tokens, const int32_t* n_accept,
                           const int32_t* out_token, int32_t* ids, hipStream_t stream);
