@@ -224,16 +224,16 @@ int check_logprobs_shape(int N, int V, int n_top) {
 
 // Split records; none (0 bytes) where a workgroup takes a whole row.
 struct LogprobLayout {
-  int nsplit, chunk;
+  int steps;
   size_t m, st, v, i, bytes;
 };
 
 // skew: the most entries that a row starts behind a 16-byte boundary.
 LogprobLayout logprob_layout(int N, int V, int n_top, int skew) {
   LogprobLayout L = {};
-  L.nsplit = logprob_splits(N, V, skew, &L.chunk);
-  if (L.nsplit == 1) return L;
-  const size_t n = (size_t)N * L.nsplit;
+  L.steps = logprob_steps(N, V, skew);
+  if (L.steps == 0) return L;
+  const size_t n = (size_t)logprob_units(N, L.steps);
   Carver c;
   L.m = c.take(n * 2 * sizeof(float));
   L.st = c.take(n * 2 * sizeof(double));
@@ -953,8 +953,7 @@ __attribute__((visibility("default"))) int dspark_token_logprobs(
   a.entropy = entropy;
   a.top_ids = top_ids;
   a.top_logprobs = top_logprobs;
-  a.nsplit = L.nsplit;
-  a.chunk = L.chunk;
+  a.steps = L.steps;
   if (L.bytes) {
     a.part_mk = at<float>(ws, L.m);
     a.part_st = at<double>(ws, L.st);

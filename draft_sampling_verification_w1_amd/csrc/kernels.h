@@ -281,13 +281,14 @@ struct LogprobArgs {
   float* entropy;        // [N]
   int32_t* top_ids;      // [N, n_top]
   float* top_logprobs;   // [N, n_top]
-  int nsplit, chunk;     // vocabulary splits per row, entries per split
-  float* part_mk;        // [2 * N * nsplit] largest entry of a split and reference of its sums
-  double* part_st;       // [2 * N * nsplit] its two sums
-  float* part_v;         // [N * nsplit * n_top] its best entries, best of every split first
+  int steps;             // of a row that is split, or 0: a workgroup takes a whole row
+  float* part_mk;        // [2 * units] largest entry of a split and reference of its sums
+  double* part_st;       // [2 * units] its two sums
+  float* part_v;         // [units * n_top] its best entries, best of every split first
   int32_t* part_i;
 };
-int logprob_splits(int N, int V, int skew, int* chunk);
+int logprob_steps(int N, int V, int skew);
+int logprob_units(int N, int steps);
 hipError_t launch_logprobs(bool bf16, const LogprobArgs& a, hipStream_t stream);
 hipError_t launch_emitted(int R, int gamma, const int32_t* tokens, const int32_t* n_accept,
                           const int32_t* out_token, int32_t* ids, hipStream_t stream);

@@ -426,26 +426,99 @@ __device__ __forceinline__ Candidate join_waves(WaveTop<kBits>& top, bool with_t
   return best;
 }
 
-// One workgroup per (row, vocabulary split).  With one split it finishes the row; with
-// more it leaves the split's sums and best entries to k_logprobs_join.
+// ---- rows cut into splits --------------------------------------------------------------
+// About 1,536 workgroups (6 per CU, what the registers hold) share the rows that have a
+// token to look up, in whole steps.  Which rows these are is known on the device alone (a
+// round emits fewer tokens than it has rows): every wave counts them.  245 of 544 rows of
+// 151,936 entries, 20 alternatives: 49 us with 6 splits, 52 us with 8 (2,048 workgroups),
+// 54 us with 3 splits of every row, 72 us with whole rows.
+constexpr int kTarget = 1536;
+constexpr int kMaxSplitRows = 1024;  // two splits each
+constexpr int kUnits = kTarget + kMaxSplitRows / 2;
+
+__host__ __device__ __forceinline__ int steps_per_split(int rows, int steps) {
+  int ns = (kTarget + rows / 2) / rows;
+  ns = ns < 1 ? 1 : (ns > steps ? steps : ns);
+  return (steps + ns - 1) / ns;
+}
+
+// Rows to look up, 64 to a word; a.N <= kMaxSplitRows.
+struct LiveRows {
+  uint64_t word[kMaxSplitRows / 64];
+  int count;
+
+  __device__ __forceinline__ void find(const LogprobArgs& a) {
+    const int lane = (int)threadIdx.x & 63;
+    int id[kMaxSplitRows / 64];
+#pragma unroll
+    for (int c = 0; c < kMaxSplitRows / 64; ++c)
+      if (64 * c < a.N) id[c] = a.ids[min(64 * c + lane, a.N - 1)];
+    count = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxSplitRows / 64; ++c) {
+      word[c] = 0;
+      if (64 * c < a.N) word[c] = ballot(64 * c + lane < a.N && id[c] >= 0 && id[c] < a.V);
+      count += __popcll(word[c]);
+    }
+  }
+  // the n-th one, n < count
+  __device__ __forceinline__ int row(int n) const {
+    const int lane = (int)threadIdx.x & 63;
+    int r = -1;
+#pragma unroll
+    for (int c = 0; c < kMaxSplitRows / 64; ++c) {
+      const int here = __popcll(word[c]);
+      if (r < 0 && n < here) {
+        const bool hit = (word[c] >> lane & 1) && __popcll(word[c] & ((1ull << lane) - 1)) == n;
+        r = 64 * c + __ffsll((unsigned long long)ballot(hit)) - 1;
+      }
+      n -= here;
+    }
+    return r;
+  }
+  // how many lie before row r
+  __device__ __forceinline__ int before(int r) const {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < kMaxSplitRows / 64; ++c) {
+      const int k = r - 64 * c;
+      if (k > 0) n += __popcll(k >= 64 ? word[c] : word[c] & ((1ull << k) - 1));
+    }
+    return n;
+  }
+};
+
+// One workgroup per row, which it finishes, or (a.steps > 0) per split of a row: it
+// leaves the split's sums and best entries to k_logprobs_join.
 template <typename E, bool kTop>
 __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
   __shared__ Candidate room[kTop ? kWaves * kRoom : 1];
   __shared__ float published[kWaves];
   __shared__ RowSums parts[kWaves];
   __shared__ int counts[kWaves];
-  const int r = (int)blockIdx.x;
-  const int split = (int)blockIdx.y;
   const int lane = (int)threadIdx.x & 63, wave = (int)threadIdx.x >> 6;
+  int r = (int)blockIdx.x, split = 0, nsplit = 1, chunk = 0x7FFFFFFF, place = 0;
+  if (a.steps > 0) {
+    LiveRows rows;
+    rows.find(a);
+    if (rows.count == 0) return;
+    const int per = steps_per_split(rows.count, a.steps);
+    nsplit = (a.steps + per - 1) / per;
+    chunk = per * kStep;
+    split = (int)blockIdx.x / rows.count;
+    place = (int)blockIdx.x - split * rows.count;
+    if (split >= nsplit) return;
+    r = rows.row(place);
+  }
   const int id = a.ids[r];
   if (id < 0 || id >= a.V) {
-    if (a.nsplit == 1 && wave == 0) skip(a, r);
+    if (wave == 0) skip(a, r);
     return;
   }
   const E* row = static_cast<const E*>(a.logits) + (int64_t)r * a.ld;
   const int skew = (int)(((uintptr_t)row / sizeof(E)) & (Group<E>::size - 1));
-  const int u0 = split * a.chunk;  // a whole number of steps
-  const int u1 = min(a.V + skew, u0 + a.chunk);
+  const int u0 = split * chunk;  // a whole number of steps
+  const int u1 = min(a.V + skew - u0, chunk) + u0;
   const int ul = Group<E>::size * (int)threadIdx.x;
   const float given = elem_at(row, id);
   u32x4 q[Group<E>::count];
@@ -511,11 +584,11 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
   wave_sums(b);
   const Candidate best = join_waves(top, kTop, b, room, parts, counts);
   if (wave != 0) return;
-  if (a.nsplit == 1) {
+  if (a.steps == 0) {
     finish(a, r, given, b, best);
     return;
   }
-  const int64_t o = (int64_t)r * a.nsplit + split;
+  const int o = place * nsplit + split;
   if (lane == 0) {
     a.part_mk[2 * o] = b.m;
     a.part_mk[2 * o + 1] = b.k;
@@ -523,7 +596,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
     a.part_st[2 * o + 1] = b.t;
   }
   if (kTop && lane < a.n_top) {  // place by place, so that the splits' best come first
-    const int64_t p = ((int64_t)r * a.n_top + lane) * a.nsplit + split;
+    const int p = (place * a.n_top + lane) * nsplit + split;
     a.part_v[p] = best.v;
     a.part_i[p] = best.i;
   }
@@ -543,11 +616,15 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
     if (wave == 0) skip(a, r);
     return;
   }
-  const int64_t o = (int64_t)r * a.nsplit;
+  LiveRows rows;
+  rows.find(a);
+  const int per = steps_per_split(rows.count, a.steps);
+  const int nsplit = (a.steps + per - 1) / per;
+  const int o = rows.before(r) * nsplit;
   const float given = elem_at(static_cast<const E*>(a.logits) + (int64_t)r * a.ld, id);
   RowSums b;
   b.none();
-  for (int j = (int)threadIdx.x; j < a.nsplit; j += kThreads) {
+  for (int j = (int)threadIdx.x; j < nsplit; j += kThreads) {
     RowSums p = {a.part_mk[2 * (o + j)], a.part_mk[2 * (o + j) + 1], a.part_st[2 * (o + j)],
                  a.part_st[2 * (o + j) + 1]};
     if (p.m == -INFINITY) continue;
@@ -564,7 +641,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
     // a wave's share of the entries; they come in no order, so that one that equals the
     // n-th best may still have a lower index: the bar is never made exact
     top.start(room + wave * kRoom, published, a.n_top);
-    const int total = a.nsplit * a.n_top;
+    const int total = nsplit * a.n_top;
     const float* pv = a.part_v + o * a.n_top;
     const int* pi = a.part_i + o * a.n_top;
     for (int c = 64 * wave; c < total; c += kThreads) {
@@ -592,7 +669,7 @@ __global__ __launch_bounds__(256) void k_emitted(int R, int gamma, const int32_t
 
 template <typename E>
 hipError_t launch_typed(const LogprobArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)a.N, (unsigned)a.nsplit);
+  const dim3 grid((unsigned)(a.steps > 0 ? logprob_units(a.N, a.steps) : a.N));
   {
     TimingScope t("logprobs", stream);
     if (a.n_top > 0)
@@ -600,7 +677,7 @@ hipError_t launch_typed(const LogprobArgs& a, hipStream_t stream) {
     else
       hipLaunchKernelGGL((k_logprobs<E, false>), grid, dim3(kThreads), 0, stream, a);
   }
-  if (a.nsplit > 1) {
+  if (a.steps > 0) {
     TimingScope t("logprobs_join", stream);
     if (a.n_top > 0)
       hipLaunchKernelGGL((k_logprobs_join<E, true>), dim3((unsigned)a.N), dim3(kThreads), 0, stream, a);
@@ -612,19 +689,21 @@ hipError_t launch_typed(const LogprobArgs& a, hipStream_t stream) {
 
 }  // namespace
 
-// Vocabulary splits per row: about 2,048 workgroups in all (8 per CU), whole steps of
-// 4,096 entries.  A row that this would shorten by few steps stays whole: a step takes
-// 1.5 us, the join 5 us, and 8 us for enough rows to fill the CUs.  36 rows of 20,480
-// (5 steps): bf16 14.6 us whole and 16.6 split, f32 16.9 and 15.2; 500 rows of 32,768
-// (8 steps): bf16 22 and 30, f32 26 and 34.
-int logprob_splits(int N, int V, int skew, int* chunk) {
+// Steps of a row (4,096 entries) if rows are split, 0 if they stay whole: splits are
+// worth it where they shorten a row by more than its join costs.  A step takes 1.5 us,
+// the join 5 us, and 8 us for enough rows to fill the CUs.  36 rows of 20,480 (5 steps):
+// bf16 14.6 us whole and 16.6 split, f32 16.9 and 15.2; 500 rows of 32,768 (8 steps):
+// bf16 22 and 30, f32 26 and 34.
+int logprob_steps(int N, int V, int skew) {
   const int steps = (V + skew + kStep - 1) / kStep;
-  int ns = 2048 / N;
-  ns = ns < 1 ? 1 : (ns > steps ? steps : ns);
-  int per = (steps + ns - 1) / ns;
-  if (steps - per <= (N < 256 ? 4 : 8)) per = steps;
-  *chunk = per * kStep;
-  return (steps + per - 1) / per;
+  if (N > kMaxSplitRows) return 0;
+  return steps - steps_per_split(N, steps) > (N < 256 ? 4 : 8) ? steps : 0;
+}
+
+// Workgroups of a split call: as many as steps_per_split gives for any number of rows up to
+// N (rows * ns <= kTarget + rows / 2).
+int logprob_units(int N, int steps) {
+  return (int64_t)N * steps < kUnits ? N * steps : kUnits;
 }
 
 hipError_t launch_logprobs(bool bf16, const LogprobArgs& a, hipStream_t stream) {

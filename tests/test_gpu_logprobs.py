@@ -143,6 +143,40 @@ def test_row_starts_and_strides(dev, dtype, offset):
     check(got, reference(z.double().numpy(), ids.numpy(), 5))
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["normal", "ties", "falling", "front", "sparse", "sure"])
+@pytest.mark.parametrize("offset", [0, 3])
+def test_split_rows(dev, dtype, kind, offset):
+    """Rows that several workgroups share: splits without a finite entry, masked rows,
+    skipped ids, rows that start at any element."""
+    import torch
+    N, V = 5, 40009
+    z, ids = make(N, V, dtype, 41, kind=kind)
+    z[1] = -math.inf
+    z[2, :30000] = -math.inf
+    ids[2], ids[3] = 17, V
+    ld = V + offset
+    view = torch.full((N * ld + offset,), 1e30, dtype=z.dtype, device="cuda")[offset:].view(N, ld)[:, :V]
+    view.copy_(z)
+    got = dev.token_logprobs(view, ids.cuda(), 20)
+    check(got, reference(z.double().numpy(), ids.numpy(), 20))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,live", [(1000, 0), (1000, 1), (1024, 40), (63, 62), (64, 64), (65, 1), (1025, 9)])
+def test_few_rows_of_many(dev, dtype, N, live):
+    """Most rows are skipped: the others, the first and the last row among them, are
+    shared by all workgroups."""
+    import torch
+    V = 57345
+    z, ids = make(N, V, dtype, N + live)
+    at = torch.randperm(N, generator=torch.Generator().manual_seed(live))
+    at = torch.cat([torch.tensor([N - 1, 0]), at[(at > 0) & (at < N - 1)]])
+    ids[at[live:]] = torch.tensor([-1, V])[torch.arange(N - live) % 2].to(torch.int32)
+    got = dev.token_logprobs(z.cuda(), ids.cuda(), 6)
+    check(got, reference(z.double().numpy(), ids.numpy(), 6))
+
+
 def test_replayed_graph_and_streams(dev):
     """The call inside a graph, replayed with new inputs between eager calls, and
     on a stream of its own: the eager call's bits."""
