@@ -8,20 +8,36 @@
 // Layout.  A page stores K as [kv_head][D / E][token][E] and V as
 // [kv_head][token / E][D][E] (E elements = 16 bytes), which are the matrix cores'
 // operand orders: the pass computes S^T = K Q^T and O^T = V^T P^T, so that
-//   - a wave's load of a K or V operand is 64 lanes x 16 contiguous-by-row bytes,
-//     straight from HBM to the registers that feed the matrix instruction (no LDS,
-//     no barrier, no transposition), and
+//   - a wave's load of a K or V operand is 64 lanes x 16 bytes, 256 contiguous bytes
+//     per lane group, and needs no transposition, and
 //   - S^T's accumulator already is P^T's operand: a lane holds the scores of one
 //     query (column l % 16); which keys it holds is settled by the order in which
 //     the key rows of K are loaded (key_of), chosen to match V's 16-byte groups.
 //
-// Work.  A row of a tile is one (token, query head of the kv head's group) pair, so
-// that the group shares every key it reads.  An item is (slot, kv head, row tile,
-// range of keys); its four waves take a quarter of the range each and join their
-// sums through LDS.  Slots and lengths are known on the device only: each workgroup
-// works out the whole batch's items from lens and offsets (one round trip), cut to
-// ranges of about equal length, and walks over its share.  Ranges of one slot are
-// joined by k_attend_join.
+// Tiles.  A row of a tile is one (token, query head of the kv head's group) pair, so
+// that the group shares every key it reads.  A workgroup is RW x KW waves: RW row groups
+// of 16 NQ rows, KW parts of the key range whose sums are joined through LDS.  Few rows
+// (a decoded token, a short chunk) are bound by HBM: one row group, the keys go from
+// memory straight to registers, no LDS and no barrier in the loop.  Many rows are bound
+// by the matrix products: the row groups share a step's operands through LDS, where they
+// lie in operand order (no bank conflicts), loaded one or two steps ahead.
+//
+// Work.  Slots and lengths are known on the device only.  The key steps of all
+// (slot, kv head, row tile) groups lie on one line, which is cut into equal spans, one
+// per workgroup, so that any mix of lengths keeps all CUs busy to the end; each
+// workgroup works out the line from lens and offsets (one round trip).  Groups that a
+// cut goes through are joined by k_attend_join.
+//
+// Measured (bf16, 32 heads on 8, 128 dimensions), append + attention + join:
+//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 65 us, 2.8 TB/s (attention alone
+//     43 us, 4.2 TB/s; the rest are the two other launches);
+//   256 slots, up to 4,096 cached, 17 new tokens: 605 us, 4.6 TB/s (a large copy: 5.1);
+//   2 prompts, 2,048 tokens behind up to 8,192: 494 us, 917 TFLOP/s (a large library
+//     matrix product: 1,240).  The matrix units are busy 40% of the time: a step's
+//     exponentials and its products do not overlap within a wave, and two waves per SIMD
+//     fill half of the gaps.  Tried without gain: values one step late with 4 waves, one
+//     wave per SIMD on 64 rows each, 192- and 256-row tiles (561, 577 us for 494),
+//     operands two steps ahead.
 #include "device_common.h"
 #include "kernels.h"
 

@@ -410,8 +410,8 @@ int dspark_cache_append(const dspark_cache* c, const dspark_cache_tables* t, int
  * dspark_cache_append; rows behind offsets[slots] are left as they were.  A
  * slot may have no rows.  Scores, sums and outputs accumulate in binary32 (bf16:
  * the weights are rounded to bf16 for the product with v; one rounding at the
- * end).  Keys and values that any of the chunk's tokens sees must be finite; what
- * else the pages hold does not matter.
+ * end).  Keys and values that any of the chunk's tokens sees must be finite and the
+ * scaled scores below 5e29 in magnitude; what else the pages hold does not matter.
  * max_chunk: the longest chunk expected, >= 1; it chooses the tiling only, any
  * chunk is computed.  scale > 0.  heads a multiple of kv_heads, N * heads <= 2^30.
  * ws: dspark_attend_workspace_bytes(c, N, heads) bytes, 256-byte aligned. */
