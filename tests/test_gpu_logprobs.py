@@ -162,6 +162,20 @@ def test_split_rows(dev, dtype, kind, offset):
     check(got, reference(z.double().numpy(), ids.numpy(), 20))
 
 
+@pytest.mark.parametrize("V", [3001, 30011])
+def test_far_rows(dev, V):
+    """Rows whose starts lie 2^32 entries apart."""
+    import torch
+    ld = 2 ** 32 + 5
+    if torch.cuda.mem_get_info()[0] < 2 * (2 * ld + V) + (1 << 30):
+        pytest.skip("not enough memory")
+    z, ids = make(3, V, "bf16", 51)
+    view = torch.empty(2 * ld + V, dtype=torch.bfloat16, device="cuda").as_strided((3, V), (ld, 1))
+    view.copy_(z)
+    got = dev.token_logprobs(view, ids.cuda(), 5)
+    check(got, reference(z.double().numpy(), ids.numpy(), 5))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("N,live", [(1000, 0), (1000, 1), (1024, 40), (63, 62), (64, 64), (65, 1), (1025, 9)])
 def test_few_rows_of_many(dev, dtype, N, live):
