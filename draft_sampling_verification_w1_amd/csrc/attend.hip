@@ -48,7 +48,10 @@ namespace {
 constexpr int kPlanThreads = 256;  // the workgroup's first threads work out the plan
 constexpr int kPlanWaves = kPlanThreads / 64;
 constexpr int kKeys = 32;      // keys per step of a wave
-constexpr int kMinSpan = 4;    // shortest span of a workgroup, in steps
+// Shortest span of a workgroup in steps, and what a pair of row tiles takes on the line at
+// least: a group costs several steps' time before its first one (21 slots of one cached
+// and up to 7 new tokens: 24 us if a workgroup takes four such groups, 11 us with one each).
+constexpr int kMinSpan = 4;
 // All loads have arrived.  Placed where a load's result is first used in a loop or
 // behind a branch: the compiler would otherwise wait for it inside the loop, and as
 // loads return in order, for the newest ones that the loop has just started.
@@ -159,6 +162,7 @@ __device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int ro
     // one or two tiles: exact; more: two steps' rounding at most above the outer pair
     w.pair_units = w.tiles == 1 ? last
                                 : tile_units(w, a.group, rows, 0) + last + (w.tiles == 2 ? 0 : 2);
+    w.pair_units = max(w.pair_units, kMinSpan);
     w.units = (int64_t)w.pair_units * w.pairs * a.c.kv_heads;
   }
   return w;
@@ -781,9 +785,13 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }
 
-// Joins the groups that spans cut: workgroup (k, b) rows 16 b to 16 b + 15 of the
-// group that starts in span k and goes on behind it.  Its pieces: record `first`, then
-// the first records of spans k + 1 to `last`.
+// Rows that a workgroup of k_attend_join takes, four dimensions a thread.
+__host__ __device__ constexpr int join_rows(int D) { return kPlanThreads / (D / 4); }
+
+// Joins the groups that spans cut: workgroup (k, b) the b-th join_rows rows of the group
+// that starts in span k and goes on behind it.  Its pieces: record `first`, then the first
+// records of spans k + 1 to `last`.  The largest maximum first, then the sums: the pieces'
+// loads do not wait for each other (5 groups of 38 pieces: 32 us one after the other).
 template <typename E>
 __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int rows_per_tile) {
   const int k = (int)blockIdx.x;
@@ -791,26 +799,28 @@ __global__ __launch_bounds__(kPlanThreads) void k_attend_join(AttendArgs a, int 
   const AttendCut cut = a.cuts[1 + k];
   const int D = a.c.head_dim, G = a.group;
   const int per_row = D / 4;
-  const int r0 = 16 * (int)blockIdx.y, r1 = min(r0 + 16, cut.rows);
-  for (int y = threadIdx.x; y < (r1 - r0) * per_row; y += kPlanThreads) {
-    const int r = r0 + y / per_row, c = y % per_row;
-    float m = kNone, l = 0.f;
-    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    for (int p = k; p <= cut.last; ++p) {
-      const int64_t o = (p == k ? (int64_t)cut.first : 2 * (int64_t)p) * rows_per_tile + r;
-      const float mp = a.part_ml[o * 2], lp = a.part_ml[o * 2 + 1];
-      const f32x4 op = *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c);
-      const float mn = fmaxf(m, mp);
-      const float f = __builtin_amdgcn_exp2f(m - mn), fp = __builtin_amdgcn_exp2f(mp - mn);
-      l = l * f + lp * fp;
-      sum = sum * f + op * fp;
-      m = mn;
-    }
-    const int row = cut.row0 + r, token = row / G;
-    E* to = static_cast<E*>(a.out) +
-            ((int64_t)(cut.token0 + token) * a.heads + cut.head * G + (row - token * G)) * D + 4 * c;
-    store4<E>(to, sum * (l > 0.f ? 1.f / l : 0.f));
+  const int r = join_rows(D) * (int)blockIdx.y + (int)threadIdx.x / per_row;
+  const int c = (int)threadIdx.x % per_row;
+  if (r >= cut.rows) return;
+  const auto record = [&](int p) {
+    return (p == k ? (int64_t)cut.first : 2 * (int64_t)p) * rows_per_tile + r;
+  };
+  float m = kNone;
+#pragma unroll 8
+  for (int p = k; p <= cut.last; ++p) m = fmaxf(m, a.part_ml[record(p) * 2]);
+  float l = 0.f;
+  f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = k; p <= cut.last; ++p) {
+    const int64_t o = record(p);
+    const float f = __builtin_amdgcn_exp2f(a.part_ml[o * 2] - m);
+    l += a.part_ml[o * 2 + 1] * f;
+    sum += *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c) * f;
   }
+  const int row = cut.row0 + r, token = row / G;
+  E* to = static_cast<E*>(a.out) +
+          ((int64_t)(cut.token0 + token) * a.heads + cut.head * G + (row - token * G)) * D + 4 * c;
+  store4<E>(to, sum * (l > 0.f ? 1.f / l : 0.f));
 }
 
 template <typename E, int D, int NQ, int RW, int KW, int kAhead>
@@ -893,7 +903,8 @@ hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t s
   }
   {
     TimingScope t("attend_join", stream);
-    const dim3 join((unsigned)a.grid, (unsigned)(rows / 16));
+    const int per = join_rows(a.c.head_dim);
+    const dim3 join((unsigned)a.grid, (unsigned)((rows + per - 1) / per));
     if (bf16)
       hipLaunchKernelGGL(k_attend_join<uint16_t>, join, dim3(kPlanThreads), 0, stream, a, rows);
     else

@@ -100,6 +100,17 @@ struct WaveTop {
     if (t) bar = below(value_of(t));
   }
 
+  // The first bar of all waves, from the lanes' largest entries: `rank` lanes of a wave
+  // reach what it publishes.  (Each wave's own n-th largest instead lets a quarter of a
+  // step's entries through for n = 64, and the cuts take most of the time.)
+  __device__ void first_shared(float mine, int wave) {
+    const uint32_t t = kth_of_lanes(mine, rank);
+    if ((threadIdx.x & 63) == 0) shared[wave] = t ? value_of(t) : -INFINITY;
+    __syncthreads();
+    step();
+    if (bar == -INFINITY) first_bar(mine);
+  }
+
   // A step begins.  Entries that only equal the n-th best of another wave may have a
   // lower index; those that equal the own n-th best come behind n better ones.
   __device__ void step() {
@@ -532,8 +543,6 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
   WaveTop<8 * (int)sizeof(E)> top;
   if (kTop) {
     top.start(room + wave * kRoom, published, a.n_top);
-    if (threadIdx.x < kWaves) published[threadIdx.x] = -INFINITY;
-    __syncthreads();
   }
   // Running sums: each exponent is one fma against a reference k that only rises, by
   // an exact power of two.  y is held above -200, where 2^y is zero in binary32, so that
@@ -547,7 +556,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
     for (int g = 0; g < Group<E>::count; ++g) Group<E>::unpack(q[g], x + g * Group<E>::size);
     // the next step's entries are on their way while this one is worked on
     if (u + kStep < u1) load_step(row, u + kStep + ul, skew, u1 - skew, q);
-    if (kTop) top.step();
+    if (kTop && u != u0) top.step();
     float m4[4];
 #pragma unroll
     for (int g = 0; g < 4; ++g) m4[g] = fmaxf(fmaxf(fmaxf(x[4 * g], x[4 * g + 1]), x[4 * g + 2]), x[4 * g + 3]);
@@ -570,6 +579,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs(LogprobArgs a) {
       b.t += (double)((t4[0] + t4[1]) + (t4[2] + t4[3]));
     }
     if (kTop) {
+      if (u == u0) top.first_shared(mt, wave);
       if (ballot(mt > top.bar)) {
         if (top.bar == -INFINITY) top.first_bar(mt);
 #pragma unroll
@@ -650,10 +660,10 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
     const int total = nsplit * a.n_top;
     const float* pv = a.part_v + o * a.n_top;
     const int* pi = a.part_i + o * a.n_top;
-    for (int c = 64 * wave; c < total; c += kThreads) {
-      const int e = c + lane;
+    for (int c = 0; c < total; c += kThreads) {
+      const int e = c + (int)threadIdx.x;
       const float x = e < total ? pv[e] : -INFINITY;
-      if (c < kThreads) top.first_bar(x);
+      if (c == 0) top.first_shared(x, wave);
       top.add(x, e < total ? pi[e] : kNoIndex);
       if (top.count > kCut) top.cut();
     }
