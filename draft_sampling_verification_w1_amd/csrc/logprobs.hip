@@ -660,11 +660,19 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
     const int total = nsplit * a.n_top;
     const float* pv = a.part_v + o * a.n_top;
     const int* pi = a.part_i + o * a.n_top;
-    for (int c = 0; c < total; c += kThreads) {
-      const int e = c + (int)threadIdx.x;
-      const float x = e < total ? pv[e] : -INFINITY;
-      if (c == 0) top.first_shared(x, wave);
-      top.add(x, e < total ? pi[e] : kNoIndex);
+    constexpr int kRounds = 4;  // on their way together
+    for (int c = 0; c < total; c += kRounds * kThreads) {
+      float x[kRounds];
+      int i[kRounds];
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) {
+        const int e = c + q * kThreads + (int)threadIdx.x;
+        x[q] = e < total ? pv[e] : -INFINITY;
+        i[q] = e < total ? pi[e] : kNoIndex;
+      }
+      if (c == 0) top.first_shared(x[0], wave);
+#pragma unroll
+      for (int q = 0; q < kRounds; ++q) top.add(x[q], i[q]);
       if (top.count > kCut) top.cut();
     }
   }
