@@ -10,7 +10,7 @@
 // one of them writes to it (reserve names the pairs, copy_pages moves the bytes).
 //
 // Bookkeeping is bound by latency (one dependent memory round trip after the other):
-// fork, reserve, free of 6 slots with 5 pages 4, 8 and 4 us, of 448 slots with up to 63
+// fork, reserve, free of 6 slots with 5 pages 4, 9 and 4 us, of 448 slots with up to 63
 // pages 5, 11 and 8 us.  Copies are bound by HBM: 3,932 pages (32 KB each in K and
 // V of 4 layers) 404 us, 5.1 TB/s like a large copy; the shared last pages of 448 forks of
 // 64 parents 51 us, the sources from cache.

@@ -8,9 +8,9 @@
 // in LDS, which is cut back to n by bisection over the values' bits when it fills.
 //
 // Many rows are bound by HBM: 4,352 rows of 151,936 bf16 logits with 20 alternatives take
-// 268 us, 4.9 TB/s of a large copy's 5.1.  Few rows are bound by the first steps of every
-// split, where the bar is low and many entries pass it (245 rows: 50 us, 1.5 TB/s), and a
-// single row by two dependent launches (15 us).
+// 259 us, 5.1 TB/s like a large copy.  Few rows are bound by what a split costs before its
+// first and behind its last step (245 rows: 47 us, 1.6 TB/s), and a single row by two
+// dependent launches (16 us).
 #include "device_common.h"
 #include "kernels.h"
 
@@ -447,8 +447,8 @@ __device__ __forceinline__ Candidate join_waves(WaveTop<kBits>& top, bool with_t
 // About 1,536 workgroups (6 per CU, what the registers hold) share the rows that have a
 // token to look up, in whole steps.  Which rows these are is known on the device alone (a
 // round emits fewer tokens than it has rows): every wave counts them.  245 of 544 rows of
-// 151,936 entries, 20 alternatives: 49 us with 6 splits, 52 us with 8 (2,048 workgroups),
-// 54 us with 3 splits of every row, 72 us with whole rows.
+// 151,936 entries, 20 alternatives: 47 us with 5 or 6 splits, 49 us with 8 (2,048
+// workgroups), 70 us with whole rows.
 constexpr int kTarget = 1536;
 constexpr int kMaxSplitRows = 1024;  // two splits each
 constexpr int kUnits = kTarget + kMaxSplitRows / 2;
