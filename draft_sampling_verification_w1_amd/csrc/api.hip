@@ -1102,6 +1102,9 @@ __attribute__((visibility("default"))) int dspark_attend(
     return fail(DSPARK_ERR_ARG, "attend: K, V, q and out must be 16-byte aligned");
   const AttendLayout L = attend_layout(c, N, heads, max_chunk);
   if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
+  const size_t q_bytes = (size_t)N * heads * c->head_dim * (c->dtype == DSPARK_BF16 ? 2 : 4);
+  if ((uintptr_t)q < (uintptr_t)out + q_bytes && (uintptr_t)out < (uintptr_t)q + q_bytes)
+    return fail(DSPARK_ERR_ARG, "attend: q and out must not overlap");
   AttendArgs a = {};
   a.c = cache_args(c, t);
   a.N = N;

@@ -412,6 +412,7 @@ int dspark_cache_append(const dspark_cache* c, const dspark_cache_tables* t, int
  * the weights are rounded to bf16 for the product with v; one rounding at the
  * end).  Keys and values that any of the chunk's tokens sees must be finite and the
  * scaled scores below 5e29 in magnitude; what else the pages hold does not matter.
+ * out must not overlap q (a row's keys are shared out over workgroups).
  * max_chunk: the longest chunk expected, >= 1; it chooses the tiling only, any
  * chunk is computed.  scale > 0.  heads a multiple of kv_heads, N * heads <= 2^30.
  * ws: dspark_attend_workspace_bytes(c, N, heads) bytes, 256-byte aligned. */

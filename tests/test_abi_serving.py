@@ -183,6 +183,9 @@ def test_append_and_attend_arguments(D):
     refused(D, ERR_ARG, attend(off=None))
     for kw in (dict(ws=None), dict(ws=P + 16), dict(nb=need - 1)):
         refused(D, ERR_WS, attend(**kw))
+    for off in (0, 16, 40 * 4 * 128 * 2 - 16):  # out over q
+        refused(D, ERR_ARG, attend(q=P + off))
+        refused(D, ERR_ARG, attend(out=P + off))
 
 
 def test_binding_refuses_cpu_tensors(D):

@@ -150,6 +150,24 @@ def test_many_slots(C, slots):
     b.check(b.run(max_chunk=3))
 
 
+@pytest.mark.parametrize("dtype,heads,kv,dim", [("bf16", 4, 1, 64), ("bf16", 8, 4, 128), ("bf16", 12, 1, 256),
+                                                ("f32", 6, 3, 128)])
+@pytest.mark.parametrize("chunk", [1, 9, 60])
+def test_short_beside_long(C, dtype, heads, kv, dim, chunk):
+    """Groups of one key step next to groups of a hundred, slots without rows between."""
+    lens = [0, 0, 3300, 1, 40, 5, 1200, 31, 0, 64, 2]
+    chunks = [1, chunk, chunk, 0, 1, chunk, 1, min(chunk, 2), 0, chunk, 1]
+    b = Batch(C, dtype, 32, heads, kv, dim, lens, chunks, seed=chunk)
+    b.check(b.run(max_chunk=chunk))
+    b.check(b.run(max_chunk=1))
+
+
+def test_most_slots(C):
+    rng = np.random.default_rng(4096)
+    b = Batch(C, "bf16", 16, 2, 1, 64, rng.integers(0, 20, 4096).tolist(), rng.integers(0, 3, 4096).tolist())
+    b.check(b.run(max_chunk=2))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_large_scores(C, dtype):
     """Scores far apart: the running maximum moves often and by much."""

@@ -242,3 +242,37 @@ def test_shared_page_of_a_refused_slot(C, first):
     seen = lambda K, V: (K.view(16, 16, 4)[:, :9], V.view(4, 64, 4).transpose(1, 2).reshape(16, 64)[:9])  # noqa: E731
     for x, y in zip(seen(c.K[0, page], c.V[0, page]), seen(*before)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("slots,groups", [(4096, 1), (4096, 1000), (4096, 2048), (3, 1)])
+def test_all_sharers_write(C, slots, groups):
+    """Forks of `groups` slots, all about to write: one of each group keeps the shared
+    page, the lowest unless another one has more tokens in it."""
+    import torch
+    c = C.PagedCache(slots, 2, slots + 10, 16, 1, 1, 64)
+    first = torch.arange(slots) < groups
+    c.reserve(first.to(torch.int32).cuda() * 7)
+    c.commit(first.to(torch.int32).cuda() * 7)
+    src = (torch.arange(groups, slots) % groups).to(torch.int32)
+    assert c.fork(src.cuda(), torch.arange(groups, slots, dtype=torch.int32).cuda()).sum() == 0
+    back = torch.zeros(slots, dtype=torch.int32)
+    back[::5] = -2  # the lowest slot is behind the others then
+    c.commit(back.cuda())
+    group = torch.arange(slots) % groups
+    lens = 7 + back
+    keeper = {}
+    for s in range(slots):
+        k = keeper.setdefault(int(group[s]), s)
+        if lens[s] > lens[k]:
+            keeper[int(group[s])] = s
+    alone = {int(x) for x in torch.nonzero(torch.bincount(group) == 1).view(-1)}
+    want = torch.tensor([-1 if keeper[int(g)] == s or int(g) in alone else int(g)
+                         for s, g in enumerate(group)])
+    r = c.reserve(torch.ones(slots, dtype=torch.int32, device="cuda"))
+    assert r["status"].sum() == 0
+    assert torch.equal(r["cow_src"].cpu().long(), want)
+    new = (want >= 0).sum().item()
+    taken = r["cow_dst"].cpu()[want >= 0]
+    assert torch.equal(taken.long(), torch.arange(groups, groups + new))
+    assert c.n_free.item() == slots + 10 - groups - new
+    assert (c.refs[:groups + new] == 1).all() and c.refs.sum().item() == groups + new

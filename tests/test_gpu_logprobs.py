@@ -222,6 +222,32 @@ def test_replayed_graph_and_streams(dev):
         check(got, reference(z2.double().numpy(), ids2.numpy(), 7))
 
 
+def test_replayed_graph_with_other_rows(dev):
+    """Replays in which other rows, and other numbers of rows, are looked up."""
+    import torch
+    z, _ = make(70, 40009, "bf16", 61)
+    zd, idd = z.cuda(), torch.zeros(70, dtype=torch.int32, device="cuda")
+    out = dev.token_logprobs(zd, idd, 4)
+    ws = dev.logprobs_workspace(70, 40009, 4)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dev.token_logprobs(zd, idd, 4, ws=ws, out=out)
+    gen = torch.Generator().manual_seed(62)
+    for live in (0, 3, 70, 1, 41):
+        ids = torch.full((70,), -1, dtype=torch.int32)
+        at = torch.randperm(70, generator=gen)[:live]
+        ids[at] = torch.randint(0, 40009, (live,), generator=gen).to(torch.int32)
+        idd.copy_(ids)
+        g.replay()
+        torch.cuda.synchronize()
+        got = {k: v.clone() for k, v in out.items()}
+        eager = dev.token_logprobs(zd, idd, 4)
+        for k in got:
+            assert torch.equal(got[k].view(torch.int32), eager[k].view(torch.int32)), (live, k)
+        check(got, reference(z.double().numpy(), ids.numpy(), 4))
+
+
 @pytest.mark.parametrize("R,gamma", [(1, 1), (4, 8), (300, 16), (5, 64)])
 def test_emitted_tokens(dev, R, gamma):
     import torch
