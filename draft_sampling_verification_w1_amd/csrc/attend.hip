@@ -37,7 +37,7 @@
 //     exponentials and its products do not overlap within a wave, and two waves per SIMD
 //     fill half of the gaps.  Tried without gain: values one step late with 4 waves, one
 //     wave per SIMD on 64 rows each, 192- and 256-row tiles (561, 577 us for 494),
-//     operands two steps ahead.
+//     operands two steps ahead, half of the waves half a step behind the others (545).
 #include "device_common.h"
 #include "kernels.h"
 
