@@ -40,6 +40,8 @@
 //     operands two steps ahead, half of the waves half a step behind the others (545).
 #include "device_common.h"
 #include "kernels.h"
+#define PLAN_FN __device__ __forceinline__
+#include "attend_plan.h"
 
 namespace dspark {
 
@@ -47,11 +49,6 @@ namespace {
 
 constexpr int kPlanThreads = 256;  // the workgroup's first threads work out the plan
 constexpr int kPlanWaves = kPlanThreads / 64;
-constexpr int kKeys = 32;      // keys per step of a wave
-// Shortest span of a workgroup in steps, and what a pair of row tiles takes on the line at
-// least: a group costs several steps' time before its first one (21 slots of one cached
-// and up to 7 new tokens: 24 us if a workgroup takes four such groups, 11 us with one each).
-constexpr int kMinSpan = 4;
 // All loads have arrived.  Placed where a load's result is first used in a loop or
 // behind a branch: the compiler would otherwise wait for it inside the loop, and as
 // loads return in order, for the newest ones that the loop has just started.
@@ -121,51 +118,12 @@ struct Ops<float> {
   }
 };
 
-// ---- the batch's work, cut into equal spans -----------------------------------------
-// A group is one (slot, kv head, row tile) and has as many units as its rows see key
-// steps.  Row tile i of a slot is put together with the slot's i-th last one: what a
-// chunk's later tokens see more than its earlier ones evens out, so that every pair
-// has `pair_units` units (a bound; a pair may end before it) and a slot's work has a
-// closed form.  All units of the batch lie on a line in the order slot, head, pair; a
-// workgroup takes a span of it, a group that spans cut is joined afterwards.
-struct SlotWork {
-  int o0, chunk;  // first token row and tokens of the chunk
-  int len;        // cached tokens before it
-  int keys;       // keys that exist: len + chunk, at most the table's width
-  int tiles, pairs;
-  int pair_units;
-  int64_t units;
-};
-
-// Key steps that the rows up to the end of row tile i see.
-__device__ __forceinline__ int tile_units(const SlotWork& w, int group, int rows, int i) {
-  const int last = min((i + 1) * rows, w.chunk * group) - 1;
-  return (min(w.len + last / group + 1, w.keys) + kKeys - 1) / kKeys;
-}
-
+// ---- the batch's work, cut into equal spans (attend_plan.h) --------------------------
 __device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int rows) {
-  SlotWork w;
-  w.o0 = min(max(a.offsets[s], 0), a.N);
-  const int o1 = min(max(a.offsets[s + 1], w.o0), a.N);
-  w.chunk = o1 - w.o0;
-  const int64_t width = (int64_t)a.c.max_pages << a.c.page_shift;
-  const int64_t len = max(a.c.t.lens[s], 0);
-  w.len = (int)(len < width ? len : width);
-  const int64_t keys = (int64_t)w.len + w.chunk;
-  w.keys = (int)(keys < width ? keys : width);
-  w.tiles = (w.chunk * a.group + rows - 1) / rows;
-  w.pairs = (w.tiles + 1) >> 1;
-  w.pair_units = 0;
-  w.units = 0;
-  if (w.tiles > 0) {
-    const int last = tile_units(w, a.group, rows, w.tiles - 1);
-    // one or two tiles: exact; more: two steps' rounding at most above the outer pair
-    w.pair_units = w.tiles == 1 ? last
-                                : tile_units(w, a.group, rows, 0) + last + (w.tiles == 2 ? 0 : 2);
-    w.pair_units = max(w.pair_units, kMinSpan);
-    w.units = (int64_t)w.pair_units * w.pairs * a.c.kv_heads;
-  }
-  return w;
+  const int o0 = min(max(a.offsets[s], 0), a.N);
+  const int o1 = min(max(a.offsets[s + 1], o0), a.N);
+  return plan_slot(o0, o1, a.c.t.lens[s], (int64_t)a.c.max_pages << a.c.page_shift, a.group, rows,
+                   a.c.kv_heads);
 }
 
 // Units before each plan thread's run of slots (thread t: slots [t per, t per + per)).
@@ -199,8 +157,7 @@ __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& p
   }
   if (tid < kPlanThreads) plan.before[tid + 1] = x;
   if (tid == 0) {
-    int64_t span = (total + a.grid - 1) / a.grid;
-    span = span > kMinSpan ? span : kMinSpan;
+    const int64_t span = plan_span(total, a.grid);
     plan.before[0] = 0;
     plan.span = span;
     plan.spans = (int)((total + span - 1) / span);
@@ -241,22 +198,12 @@ __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const 
     g.slot_start = start;
     g.slot_end = start + g.w.units;
   }
-  const int64_t left = x - g.slot_start;
-  const int64_t pair = left / g.w.pair_units;
-  const int off = (int)(left - pair * g.w.pair_units);
-  g.head = (int)(pair / g.w.pairs);
-  const int i = (int)(pair - (int64_t)g.head * g.w.pairs), j = g.w.tiles - 1 - i;
-  const int ui = tile_units(g.w, a.group, rows, i);
-  g.next = x - off + g.w.pair_units;
-  g.tile = i;
-  g.units = ui;
-  g.start = x - off;
-  if (off >= ui) {
-    const int uj = j > i ? tile_units(g.w, a.group, rows, j) : 0;
-    g.tile = j;
-    g.units = off < ui + uj ? uj : 0;
-    g.start = x - off + ui;
-  }
+  const PlanPlace at = plan_place(g.w, a.group, rows, x - g.slot_start);
+  g.head = at.head;
+  g.tile = at.tile;
+  g.units = at.units;
+  g.start = g.slot_start + at.start;
+  g.next = g.slot_start + at.next;
 }
 
 template <typename E>
