@@ -235,7 +235,7 @@ LogprobLayout logprob_layout(int N, int V, int n_top, int skew) {
   if (L.steps == 0) return L;
   const size_t n = (size_t)logprob_units(N, L.steps);
   Carver c;
-  L.m = c.take(n * 2 * sizeof(float));
+  L.m = c.take(n * sizeof(float));
   L.st = c.take(n * 2 * sizeof(double));
   L.v = c.take(n * n_top * sizeof(float));
   L.i = c.take(n * n_top * sizeof(int32_t));
@@ -955,7 +955,7 @@ __attribute__((visibility("default"))) int dspark_token_logprobs(
   a.top_logprobs = top_logprobs;
   a.steps = L.steps;
   if (L.bytes) {
-    a.part_mk = at<float>(ws, L.m);
+    a.part_m = at<float>(ws, L.m);
     a.part_st = at<double>(ws, L.st);
     a.part_v = at<float>(ws, L.v);
     a.part_i = at<int32_t>(ws, L.i);

@@ -282,7 +282,7 @@ struct LogprobArgs {
   int32_t* top_ids;      // [N, n_top]
   float* top_logprobs;   // [N, n_top]
   int steps;             // of a row that is split, or 0: a workgroup takes a whole row
-  float* part_mk;        // [2 * units] largest entry of a split and reference of its sums
+  float* part_m;         // [units] largest entry of a split
   double* part_st;       // [2 * units] its two sums
   float* part_v;         // [units * n_top] its best entries, best of every split first
   int32_t* part_i;

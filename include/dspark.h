@@ -275,7 +275,8 @@ int dspark_emitted_tokens(int32_t R, int32_t gamma, const int32_t* tokens, const
  *   entropy[r] = -sum_v p_v log p_v (nats), p = softmax(z)
  *   top_ids[r, j], top_logprobs[r, j] = the (j + 1)-th most likely token and
  *       its log probability, j < n_top; the lower token first among equal logits.
- * An entry may be -inf (masked): its token has log probability -inf and is no
+ * Finite entries may have any magnitude (masks by the type's lowest value).  An
+ * entry may be -inf (masked): its token has log probability -inf and is no
  * alternative; places without one hold id -1 and -inf.  A row whose id lies
  * outside [0, V) is skipped without being read: NaN, ids -1.  A row without a
  * finite entry has no distribution: NaN, ids -1.

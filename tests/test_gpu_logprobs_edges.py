@@ -1,0 +1,70 @@
+"""Token log probabilities (dspark_token_logprobs) of logits that lie at the ends of their
+types, at zero, and tied, against binary64 with the bounds of test_gpu_logprobs.py.  The
+reference takes the row's maximum off first (exact or far below a bound here), as a sum of
+1e10 and a logarithm would lose more in binary64 than the bounds allow.  The bounds hold
+for far logits too: a difference z - m that matters there is exact, and its product with
+log2 e is rounded once, as the fma elsewhere is."""
+import math
+
+import numpy as np
+import pytest
+
+from test_gpu_logprobs import check, dev, reference  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+# whole rows, rows shared by several workgroups, many short rows
+SHAPES = [(3, 20011), (3, 40009), (2051, 300)]
+
+
+def expect(z, ids, n_top):
+    z = z.double().numpy()
+    m = z.max(1, keepdims=True)
+    r = reference(z - np.where(np.isfinite(m), m, 0.0), ids.numpy(), n_top)
+    for name in ("logprob", "top_logprobs"):
+        # from here on a difference rounds to -inf in binary32
+        r[name] = np.where(r[name] <= -2.0 ** 128 * (1 - 2.0 ** -25), -np.inf, r[name])
+    return r
+
+
+def rand(N, V, seed, scale=4.0):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn((N, V), generator=g) * scale, torch.randint(0, V, (N,), generator=g).to(torch.int32), g
+
+
+def dtype_of(name):
+    import torch
+    return torch.float32 if name == "f32" else torch.bfloat16
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("mask", [-1e6, -1e10, -1e20, -1e30, "lowest bf16", "lowest"])
+@pytest.mark.parametrize("N,V", SHAPES)
+@pytest.mark.parametrize("n_top", [0, 20])
+def test_finite_masks(dev, dtype, mask, N, V, n_top):  # noqa: F811
+    """Masked entries that are finite: whole threads' first entries, nearly all of a row,
+    a whole row (then a uniform distribution)."""
+    import torch
+    dt = dtype_of(dtype)
+    value = {"lowest": torch.finfo(dt).min, "lowest bf16": torch.finfo(torch.bfloat16).min}.get(mask, mask)
+    z, ids, g = rand(N, V, 3)
+    z[0, :V * 2 // 3] = value
+    z[1, torch.rand(V, generator=g) < 0.99] = value
+    z[2] = value
+    if N > 3:
+        z[torch.rand((N, V), generator=g) < 0.5] = value
+    ids[0], ids[2] = V - 1, V // 2
+    z = z.to(dt)
+    check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), expect(z, ids, n_top))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("shift,scale", [(1e5, 4), (3e6, 4), (-3e6, 4), (1e7, 4), (1e10, 4096), (-1e10, 4096),
+                                         (1e20, 0), (0, 1e6), (0, 1e10), (0, 1e30), (0, 5e37), (3.2e38, 0),
+                                         (-3.2e38, 0)])
+@pytest.mark.parametrize("N,V", SHAPES)
+def test_far_logits(dev, dtype, shift, scale, N, V):  # noqa: F811
+    z, ids, g = rand(N, V, 5, 1.0)
+    z = (z * scale + shift).to(dtype_of(dtype))
+    check(dev.token_logprobs(z.cuda(), ids.cuda(), 8), expect(z, ids, 8))
