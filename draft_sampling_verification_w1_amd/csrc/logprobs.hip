@@ -227,6 +227,12 @@ struct WaveTop {
     bar = fmaxf(bar, below(exact));  // until the step's end an equal entry may have a lower index
   }
 
+  // From here on entries may come that lie before the list's: one that equals its n-th
+  // best is a candidate.
+  __device__ void open() {
+    if (exact > -INFINITY) bar = below(exact);
+  }
+
   // The n best, best first (places left over: -inf, kNoIndex), to the wave's lanes.
   __device__ Candidate sorted() {
     cut();
@@ -434,6 +440,7 @@ __device__ __forceinline__ Candidate join_waves(WaveTop<kBits>& top, bool with_t
     b.t += part.t;
   }
   if (with_top) {
+    top.open();
     for (int w = 1; w < kWaves; ++w) {
       const Candidate c = lane < counts[w] ? room[w * kRoom + lane] : Candidate{-INFINITY, kNoIndex};
       top.add(c.v, c.i);

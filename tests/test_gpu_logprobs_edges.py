@@ -68,3 +68,20 @@ def test_far_logits(dev, dtype, shift, scale, N, V):  # noqa: F811
     z, ids, g = rand(N, V, 5, 1.0)
     z = (z * scale + shift).to(dtype_of(dtype))
     check(dev.token_logprobs(z.cuda(), ids.cuda(), 8), expect(z, ids, 8))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("gone", [(5, 512), (1, 1), (3, 2049), (0, 1024), (7, 4100), (2, 16390)])
+@pytest.mark.parametrize("N,V", [(2, 20000), (2, 57345)])
+@pytest.mark.parametrize("n_top", [1, 4, 8, 20, 64])
+def test_ties_over_waves(dev, dtype, gone, N, V, n_top):  # noqa: F811
+    """All entries equal but for a masked range: the lowest tokens lie in several waves'
+    shares.  The second row has few values, in no order."""
+    import torch
+    z, ids, g = rand(N, V, 9)
+    z[0] = 1.5
+    z[1] = torch.randint(-1, 2, (V,), generator=g).float()
+    z[:, gone[0]:gone[1]] = -math.inf
+    ids[:] = V - 1
+    z = z.to(dtype_of(dtype))
+    check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), expect(z, ids, n_top))
