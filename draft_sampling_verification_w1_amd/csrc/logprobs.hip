@@ -44,7 +44,11 @@ __device__ __forceinline__ uint32_t order_of(float v) {
 __device__ __forceinline__ float value_of(uint32_t o) {
   return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
 }
-__device__ __forceinline__ float below(float v) { return value_of(order_of(v) - 1); }
+// The next value that compares as smaller: below +0 lies -0, which does not.
+__device__ __forceinline__ float below(float v) {
+  const uint32_t o = order_of(v);
+  return value_of(o - (o == 0x80000000u ? 2 : 1));
+}
 
 struct Candidate {
   float v;

@@ -85,3 +85,27 @@ def test_ties_over_waves(dev, dtype, gone, N, V, n_top):  # noqa: F811
     ids[:] = V - 1
     z = z.to(dtype_of(dtype))
     check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), expect(z, ids, n_top))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["zeros", "both zeros", "negative zeros", "largest is 0", "falls from 0", "tiny"])
+@pytest.mark.parametrize("N,V", SHAPES + [(5, 7)])
+@pytest.mark.parametrize("n_top", [1, 2, 3, 4, 5, 64])
+def test_zero(dev, dtype, kind, N, V, n_top):  # noqa: F811
+    """The n-th best entry is zero: the entries that equal it, of either sign, count."""
+    import torch
+    z, ids, g = rand(N, V, 7)
+    if kind == "zeros":
+        z = torch.zeros((N, V))
+    elif kind == "both zeros":
+        z = torch.where(torch.rand((N, V), generator=g) < 0.5, 0.0, -0.0)
+    elif kind == "negative zeros":
+        z = -torch.zeros((N, V))
+    elif kind == "largest is 0":
+        z -= z.amax(1, keepdim=True)
+    elif kind == "falls from 0":
+        z = -torch.arange(V).float().repeat(N, 1) / 64
+    else:                        # below the smallest normal number, of both signs
+        z = torch.randint(-3, 4, (N, V), generator=g).float() * 2.0 ** -130
+    z = z.to(dtype_of(dtype))
+    check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), expect(z, ids, n_top))
