@@ -31,6 +31,11 @@ __device__ __forceinline__ int rank_in(uint64_t mask) {
                                    __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0u));
 }
 
+// The larger value; NaN if one is (fmaxf would lose it).  Two of them are one instruction.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  return __builtin_elementwise_maximum(a, b);
+}
+
 // Order of the alternatives: larger value first, then the lower index.
 __device__ __forceinline__ bool ahead(float v1, int i1, float v2, int i2) {
   return v1 > v2 || (v1 == v2 && i1 < i2);
@@ -256,7 +261,7 @@ struct WaveTop {
   }
 };
 
-// Sums over entries z of one row: m the largest entry, and with y = z L - k, L = log2 e
+// Sums over entries z of one row: m the largest entry (NaN if one is), and with y = z L - k, L = log2 e
 // in binary32, k = ceil(m L): s = sum 2^y, t = sum 2^y y, in binary64.  m L is exact in
 // binary64 (24 x 24 bits), and so is k, however far from zero m lies.  Sums of two sets are
 // brought to one k by a power of two: exact, and no exponential.
@@ -268,7 +273,7 @@ struct RowSums {
     m = -INFINITY;
     k = s = t = 0.0;
   }
-  // The sums as those of a set with the largest entry mn >= m.
+  // The sums as those of a set with the largest entry mn >= m (or NaN).
   __device__ void to(float mn) {
     const double kn = ceil((double)mn * (double)kLog2e);
     if (m != -INFINITY && kn != k) {
@@ -295,7 +300,7 @@ __device__ __forceinline__ uint32_t shifted(uint32_t old, uint32_t x) {
 }
 template <int kCtrl, int kRows>
 __device__ __forceinline__ float step_max(float m) {
-  return fmaxf(m, __uint_as_float(shifted<kCtrl, kRows>(__float_as_uint(m), __float_as_uint(m))));
+  return max_or_nan(m, __uint_as_float(shifted<kCtrl, kRows>(__float_as_uint(m), __float_as_uint(m))));
 }
 template <int kCtrl, int kRows>
 __device__ __forceinline__ double step_sum(double s) {
@@ -390,7 +395,8 @@ __device__ __forceinline__ void load_step(const E* row, int u, int skew, int end
 __device__ __forceinline__ void finish(const LogprobArgs& a, int r, float given, const RowSums& sums,
                                        const Candidate& best) {
   const int lane = (int)threadIdx.x & 63;
-  const bool none = sums.m == -INFINITY;  // no finite entry, no distribution
+  // no finite entry, or one that is +inf or NaN: no distribution
+  const bool none = !(fabsf(sums.m) < INFINITY);
   const double d = sums.above();
   const double ln_s = log(sums.s) + d * 0.69314718055994530942;  // lse - m
   if (lane == 0) {
@@ -398,7 +404,7 @@ __device__ __forceinline__ void finish(const LogprobArgs& a, int r, float given,
     a.entropy[r] = none ? NAN : (float)(ln_s - (sums.t / sums.s + d) / (double)kLog2e);
   }
   if (lane < a.n_top) {
-    const bool there = best.i != kNoIndex;
+    const bool there = !none && best.i != kNoIndex;
     a.top_ids[(int64_t)r * a.n_top + lane] = there ? best.i : -1;
     a.top_logprobs[(int64_t)r * a.n_top + lane] =
         none ? NAN : (there ? (float)(((double)best.v - (double)sums.m) - ln_s) : -INFINITY);
@@ -432,7 +438,7 @@ __device__ __forceinline__ Candidate join_waves(WaveTop<kBits>& top, bool with_t
   if (wave != 0) return best;
   float m = parts[0].m;
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, parts[w].m);
+  for (int w = 1; w < kWaves; ++w) m = max_or_nan(m, parts[w].m);
   b.none();
   if (m != -INFINITY) b.to(m);
 #pragma unroll
@@ -572,9 +578,10 @@ __global__ __launch_bounds__(kThreads, sizeof(E) == 2 ? 7 : 6) void k_logprobs(L
     if (kTop && u != u0) top.step();
     float m4[4];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) m4[g] = fmaxf(fmaxf(fmaxf(x[4 * g], x[4 * g + 1]), x[4 * g + 2]), x[4 * g + 3]);
-    const float mt = fmaxf(fmaxf(fmaxf(m4[0], m4[1]), m4[2]), m4[3]);
-    if (mt > b.m) b.to(mt);
+    for (int g = 0; g < 4; ++g)
+      m4[g] = max_or_nan(max_or_nan(max_or_nan(x[4 * g], x[4 * g + 1]), x[4 * g + 2]), x[4 * g + 3]);
+    const float mt = max_or_nan(max_or_nan(max_or_nan(m4[0], m4[1]), m4[2]), m4[3]);
+    if (!(mt <= b.m)) b.to(max_or_nan(mt, b.m));
     if (b.m != -INFINITY) {
       float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
       auto add = [&](int j, float y) {
@@ -661,7 +668,7 @@ __global__ __launch_bounds__(kThreads) void k_logprobs_join(LogprobArgs a) {
     RowSums p = {a.part_m[o + j], 0.0, a.part_st[2 * (o + j)], a.part_st[2 * (o + j) + 1]};
     if (p.m == -INFINITY) continue;
     p.k = ceil((double)p.m * (double)kLog2e);
-    const float m = fmaxf(b.m, p.m);
+    const float m = max_or_nan(b.m, p.m);
     p.to(m);
     b.to(m);
     b.s += p.s;

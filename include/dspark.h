@@ -279,7 +279,7 @@ int dspark_emitted_tokens(int32_t R, int32_t gamma, const int32_t* tokens, const
  * entry may be -inf (masked): its token has log probability -inf and is no
  * alternative; places without one hold id -1 and -inf.  A row whose id lies
  * outside [0, V) is skipped without being read: NaN, ids -1.  A row without a
- * finite entry has no distribution: NaN, ids -1.
+ * finite entry, or with one that is +inf or NaN, has no distribution: NaN, ids -1.
  * logits: dtype; ids [N] int32; logprob, entropy [N] float32; top_ids int32 and
  * top_logprobs float32 [N, n_top] (NULL if n_top is 0).  Sums in binary64 over
  * binary32 exponentials (16 at a time in binary32).

@@ -109,3 +109,23 @@ def test_zero(dev, dtype, kind, N, V, n_top):  # noqa: F811
         z = torch.randint(-3, 4, (N, V), generator=g).float() * 2.0 ** -130
     z = z.to(dtype_of(dtype))
     check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), expect(z, ids, n_top))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("what", [math.nan, -math.nan, math.inf])
+@pytest.mark.parametrize("N,V", [(6, 20011), (6, 40009), (2051, 300), (6, 5)])
+@pytest.mark.parametrize("n_top", [0, 3])
+def test_rows_without_a_distribution(dev, dtype, what, N, V, n_top):  # noqa: F811
+    """A NaN or +inf among the entries: NaN and no alternatives, the other rows as ever."""
+    import torch
+    z, ids, g = rand(N, V, 13)
+    z[0, V - 1] = what
+    z[1, 0] = what
+    z[2, V // 2] = what
+    z[3, ids[3].item()] = what
+    z[3, :V // 3] = -math.inf
+    z = z.to(dtype_of(dtype))
+    none = ~(z < math.inf).all(1, keepdim=True)
+    assert none[:3].all()
+    want = expect(z.double().masked_fill(none, -math.inf), ids, n_top)
+    check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), want)
