@@ -99,8 +99,8 @@ class PagedCache:
         self._call(dspark.lib().dspark_cache_init, self._t)
 
     def fork(self, src, dst):
-        """Slots dst [n] get the tokens of slots src [n] by sharing pages
-        (dspark_cache_fork).  Returns status [n] (1: the pair was refused)."""
+        """Slots dst [n] get the tokens of slots src [n] by sharing the pages that hold
+        them, not those reserved behind (dspark_cache_fork).  Returns status [n] (1: the pair was refused)."""
         n = src.numel()
         self._need(src, "src", torch.int32, (n,))
         self._need(dst, "dst", torch.int32, (n,))

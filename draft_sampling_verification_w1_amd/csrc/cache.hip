@@ -65,7 +65,9 @@ __device__ __forceinline__ void wave_add(int v, int32_t* dst) {
   if ((threadIdx.x & 63) == 0 && v) atomicAdd(dst, v);
 }
 
-// One workgroup per pair.  A pair is refused (status 1) if an index is out of
+// One workgroup per pair.  Shared are the pages that hold tokens: what src has reserved
+// behind them it will write, and reserve looks for sharers in a slot's last page alone.
+// A pair is refused (status 1) if an index is out of
 // range, dst holds pages, an earlier pair names the same dst, or its src is any
 // pair's dst: every accepted pair then reads only slots that no pair writes.
 __global__ __launch_bounds__(256) void k_cache_fork(CacheArgs a, int n, const int32_t* src,
@@ -81,7 +83,9 @@ __global__ __launch_bounds__(256) void k_cache_fork(CacheArgs a, int n, const in
   bad = __syncthreads_or(bad);
   if (threadIdx.x == 0) status[i] = bad ? 1 : 0;
   if (bad) return;
-  const int held = min(max(a.t.held[s], 0), a.max_pages);
+  const int len = a.t.lens[s];
+  const int used = (int)(((int64_t)max(len, 0) + (1 << a.page_shift) - 1) >> a.page_shift);
+  const int held = min(min(max(a.t.held[s], 0), a.max_pages), used);
   const int32_t* from = a.t.table + (int64_t)s * a.max_pages;
   int32_t* to = a.t.table + (int64_t)d * a.max_pages;
   for (int j = threadIdx.x; j < held; j += 256) {
@@ -91,7 +95,7 @@ __global__ __launch_bounds__(256) void k_cache_fork(CacheArgs a, int n, const in
   }
   __syncthreads();  // every thread has read held[d] before it changes
   if (threadIdx.x == 0) {
-    a.t.lens[d] = a.t.lens[s];
+    a.t.lens[d] = len;
     a.t.held[d] = held;
   }
 }

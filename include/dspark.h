@@ -339,9 +339,10 @@ typedef struct {
 /* Empty tables: every slot without tokens, every page free. */
 int dspark_cache_init(const dspark_cache* c, const dspark_cache_tables* t, void* stream);
 
-/* Forks: slot dst[i] gets the tokens of slot src[i] by sharing its pages (one
- * more reference each; nothing is copied).  status[i] = 0, or 1 for a pair that is
- * refused and changes nothing: an index outside [0, slots), a dst that holds
+/* Forks: slot dst[i] gets the tokens of slot src[i] by sharing the pages that
+ * hold them (one more reference each; nothing is copied).  Pages that src has
+ * reserved behind its tokens stay its own.  status[i] = 0, or 1 for a pair that
+ * is refused and changes nothing: an index outside [0, slots), a dst that holds
  * pages, a dst that an earlier pair names, or a src that is any pair's dst.
  * src, dst, status [n] int32, 1 <= n <= 4096. */
 int dspark_cache_fork(const dspark_cache* c, const dspark_cache_tables* t, int32_t n,

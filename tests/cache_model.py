@@ -21,7 +21,8 @@ class CacheModel:
                    or len(before[0][d]) > 0)
             status.append(int(bad))
             if not bad:
-                self.rows[d], self.lens[d] = list(before[0][s]), before[1][s]
+                # the pages that hold tokens; what s has reserved behind them stays its own
+                self.rows[d], self.lens[d] = before[0][s][:-(-before[1][s] // self.page)], before[1][s]
                 for p in self.rows[d]:
                     self.refs[p] += 1
         return status
