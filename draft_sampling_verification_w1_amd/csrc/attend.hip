@@ -56,6 +56,9 @@ __device__ __forceinline__ void wait_loads() { __builtin_amdgcn_s_waitcnt(0x0F70
 constexpr float kRise = 8.f;      // how far scores may pass the running maximum (in log2) ...
 constexpr float kRiseSum = 1024.f;  // ... and the sum of a lane's eight weights
 constexpr float kNone = -1e30f;  // maximum of a row that has seen no key
+// From here on a maximum, a rounded product of score and scale, is off by a whole or more
+// (binary logarithm), and an exact product against it could be anything.
+constexpr float kFar = 0x1p24f;
 
 __device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -416,7 +419,9 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     return __ballot(risen) != 0;
   };
   // The maxima brought up to a step's scores, and the sums so far scaled down.
+  bool far = false;  // some row's maximum lies far from zero
   auto follow = [&]() {
+    far = false;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       float mn = fmaxf(m[i], mx[i]);
@@ -424,21 +429,22 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
       mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
       const float f = __builtin_amdgcn_exp2f(m[i] - mn);
       m[i] = mn;
+      far |= mn > kNone && fabsf(mn) > kFar;
       l[i] *= f;
 #pragma unroll
       for (int d = 0; d < kDT; ++d) o[i][d] *= f;
     }
+    far = __ballot(far) != 0;
   };
   // A step's weights p and their sums, against the maxima as they are; true if a sum
   // shows that some score lies far above its row's maximum.
-  auto weights = [&]() {
+  auto weights_of = [&](auto exponent) {
     bool risen = false;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       float e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        e[j] = __builtin_amdgcn_exp2f(fmaf(s[i][j >> 2][j & 3], a.scale_log2, -m[i]));
+      for (int j = 0; j < 8; ++j) e[j] = __builtin_amdgcn_exp2f(exponent(s[i][j >> 2][j & 3], m[i]));
       sums[i] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       risen |= sums[i] > kRiseSum;
 #pragma unroll
@@ -449,21 +455,36 @@ __device__ __forceinline__ void attend_steps(const AttendArgs& a, const Group& i
     }
     return __ballot(risen) != 0;
   };
+  auto weights = [&]() {
+    return weights_of([&](float x, float m) { return fmaf(x, a.scale_log2, -m); });
+  };
+  // The product rounded as the maximum's was, so that the largest weight is 1.
+  auto far_weights = [&]() {
+    weights_of([&](float x, float m) {
+#pragma clang fp contract(off)
+      const float y = x * a.scale_log2;
+      return y - m;
+    });
+  };
   // The maxima move at the first step, and when a score is far above all before it;
   // otherwise they stay behind (the sums are far from binary32's end) and a step needs
   // neither a rescaling nor an exchange between lanes.  Large tiles are bound by
   // arithmetic and learn it from the weights' sums, without a maximum over the scores;
   // the others by memory, and go without keeping scores and weights side by side.
+  // Maxima far from zero are rare: such a step's weights are computed again (a choice
+  // before them costs 5% of a prompt's attention).
   auto step_weights = [&]() {
     if constexpr (KW == 1) {
-      if (weights()) {
+      if (__builtin_expect(weights() | far, 0)) {
         largest();
         follow();
-        weights();
+        if (far) far_weights();
+        else weights();
       }
     } else {
       if (largest()) follow();
       weights();
+      if (__builtin_expect(far, 0)) far_weights();
     }
   };
   auto add_sums = [&]() {

@@ -1,9 +1,8 @@
 """Chunk attention (dspark_attend) where its tiling and its numbers have their ends,
 against binary64 with the bounds of test_gpu_attend.py."""
-
 import pytest
 
-from test_gpu_attend import Batch, C, ints  # noqa: F401
+from test_gpu_attend import U, Batch, C, ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +35,52 @@ def test_table_shorter_than_the_chunk(C, dtype, heads, kv, dim, chunk):  # noqa:
     columns = range(width, -(-(20 + chunk) // 16))
     b.check(b.run(max_chunk=chunk), hidden={(0, j) for j in columns})
     assert torch.equal(c.lens, ints([20, 40]))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("exponent", [8, 20, 24, 25, 31, 33, 40, 60, 97])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("heads,kv,dim,chunk", [(4, 2, 64, 1), (2, 2, 128, 40), (8, 1, 128, 40), (2, 1, 256, 17)])
+def test_far_scores(C, dtype, exponent, sign, heads, kv, dim, chunk):  # noqa: F811
+    """Scaled scores of up to 2^98 = 3.2e29 in magnitude.
+
+    A score is exact: one dimension of query and key holds a power of two (times 65/64 or
+    66/64), the others nothing.  Its product with log2 e is not.  Every third key has the
+    largest score x, the others lie |x| / 65 and about |x| behind it.  From 2^20 on only the
+    largest have a weight, all the same; at 2^8 the next ones have e^-4: an exponent of 4
+    log2 e costs two roundings and that of log2 e, the exponential two more: (3 * 5.8 + 2) u.
+    Sums of n keys add n u; bf16 rounds the weights and the result (2^-8 each)."""
+    import torch
+    lens, chunks = [70, 333], [chunk, chunk]
+    b = Batch(C, dtype, 16, heads, kv, dim, lens, chunks, seed=exponent)
+    low, far = (1.0, 0.0) if sign > 0 else (66 / 64, 2.0)
+
+    def keys(n):
+        k = torch.zeros((n, kv, dim))
+        i = torch.arange(n)[:, None]
+        k[..., 3] = torch.where(i % 3 == 0, 65 / 64, torch.where(i % 3 == 1, low, far))
+        return (k * (sign * 2.0 ** (exponent - exponent // 2))).to(b.dt)
+
+    b.q = torch.zeros_like(b.q)
+    b.q[..., 3] = 2.0 ** (exponent // 2)
+    b.old_k, b.k = keys(len(b.old_k)), keys(len(b.k))
+    b.c.lens.zero_()
+    b.c.append(b.layer, b.old_k.cuda(), b.old_v.cuda(), ints(b.old))
+    b.c.lens.copy_(ints(lens))
+    b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets)
+    bf = dtype == "bf16"
+    for most in (chunk, 1):
+        got = b.run(max_chunk=most, scale=1.0).double().cpu()
+        for s, (ln, n) in enumerate(zip(lens, chunks)):
+            a, o = b.off[s], b.old[s]
+            kk = torch.cat([b.old_k[o:o + ln], b.k[a:a + n]]).double()
+            vv = torch.cat([b.old_v[o:o + ln], b.v[a:a + n]]).double()
+            mask = torch.arange(ln + n)[None] > ln + torch.arange(n)[:, None]
+            for h in range(heads):
+                sc = b.q[a:a + n, h].double() @ kk[:, h // (heads // kv)].T
+                w = torch.softmax(sc.masked_fill(mask, -torch.inf), 1)
+                v = vv[:, h // (heads // kv)]
+                want, A = w @ v, w @ v.abs()
+                tol = A * ((ln + n + 36) * U + (2.0 ** -8 if bf else 0)) + want.abs() * (2.0 ** -8 if bf else U)
+                off = (got[a:a + n, h] - want).abs()
+                assert (off <= tol).all(), (most, s, h, float((off / tol).max()))
