@@ -215,7 +215,8 @@ int check_ws_bytes(size_t need, void* ws, size_t ws_bytes) {
 
 // ---- log probabilities of given tokens ---------------------------------------
 int check_logprobs_shape(int N, int V, int n_top) {
-  if (N < 1 || N > (1 << 24)) return fail(DSPARK_ERR_SHAPE, "N=%d outside [1, 2^24]", N);
+  // a workgroup of 256 per row: 2^24 of them are more work-items than a launch holds
+  if (N < 1 || N >= (1 << 24)) return fail(DSPARK_ERR_SHAPE, "N=%d outside [1, 2^24)", N);
   if (V < 1 || V >= (1 << 26)) return fail(DSPARK_ERR_SHAPE, "V=%d outside [1, 2^26)", V);
   if (n_top < 0 || n_top > kMaxTopLogprobs)
     return fail(DSPARK_ERR_SHAPE, "n_top=%d outside [0, %d]", n_top, kMaxTopLogprobs);

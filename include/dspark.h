@@ -285,7 +285,7 @@ int dspark_emitted_tokens(int32_t R, int32_t gamma, const int32_t* tokens, const
  * binary32 exponentials (16 at a time in binary32).
  * ws: dspark_logprobs_workspace_bytes(N, V, n_top) bytes, 256-byte aligned; 0
  * bytes (ws may be NULL) where a workgroup takes a whole row.
- * Limits: 1 <= N <= 2^24, 1 <= V < 2^26, 0 <= n_top <= 64. */
+ * Limits: 1 <= N < 2^24, 1 <= V < 2^26, 0 <= n_top <= 64. */
 size_t dspark_logprobs_workspace_bytes(int32_t N, int32_t V, int32_t n_top);
 int dspark_token_logprobs(int32_t dtype, int32_t N, int32_t V, int64_t ld, const void* logits,
                           const int32_t* ids, int32_t n_top, float* logprob, float* entropy,

@@ -129,3 +129,22 @@ def test_rows_without_a_distribution(dev, dtype, what, N, V, n_top):  # noqa: F8
     assert none[:3].all()
     want = expect(z.double().masked_fill(none, -math.inf), ids, n_top)
     check(dev.token_logprobs(z.cuda(), ids.cuda(), n_top), want)
+
+
+def test_most_rows(dev):  # noqa: F811
+    """As many rows as a call takes, of two entries.  The bounds of test_gpu_logprobs.py with
+    |z - m| <= 6: (2 * 6 + 9) u, and (21 + (21 + 7) * 7) u for the entropy."""
+    import torch
+    N = 2 ** 24 - 1
+    a = torch.arange(N, device="cuda")
+    z = torch.stack([a % 5, (a + 3) % 7 - 2], 1).to(torch.bfloat16)
+    got = dev.token_logprobs(z, (a % 2).to(torch.int32), 1)
+    p = torch.log_softmax(z.double(), 1)
+    best = (z[:, 1] > z[:, 0]).to(torch.int32)
+    u = 2.0 ** -24
+    assert torch.equal(got["top_ids"].view(-1), best)
+    for name, want, tol in (("logprob", p.gather(1, (a % 2).view(-1, 1)), 21 * u),
+                            ("top_logprobs", p.gather(1, best.long().view(-1, 1)), 21 * u),
+                            ("entropy", -(p.exp() * p).sum(1, keepdim=True), 217 * u)):
+        off = (got[name].double().view(-1, 1) - want).abs()
+        assert (off <= tol + u * want.abs()).all(), name
