@@ -29,11 +29,11 @@
 // cut goes through are joined by k_attend_join.
 //
 // Measured (bf16, 32 heads on 8, 128 dimensions), append + attention + join:
-//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 65 us, 2.8 TB/s (attention alone
+//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 66 us, 2.7 TB/s (attention alone
 //     43 us, 4.2 TB/s; the rest are the two other launches);
-//   256 slots, up to 4,096 cached, 17 new tokens: 605 us, 4.6 TB/s (a large copy: 5.1);
-//   2 prompts, 2,048 tokens behind up to 8,192: 494 us, 917 TFLOP/s (a large library
-//     matrix product: 1,240).  The matrix units are busy 40% of the time: a step's
+//   256 slots, up to 4,096 cached, 17 new tokens: 609 us, 4.6 TB/s (a large copy: 5.1);
+//   2 prompts, 2,048 tokens behind up to 8,192: 500 us, 907 TFLOP/s (a large library
+//     matrix product: 1,240).  The matrix units are busy 39% of the time: a step's
 //     exponentials and its products do not overlap within a wave, and two waves per SIMD
 //     fill half of the gaps.  Tried without gain: values one step late with 4 waves, one
 //     wave per SIMD on 64 rows each, 192- and 256-row tiles (561, 577 us for 494),

@@ -8,7 +8,7 @@
 // in LDS, which is cut back to n by bisection over the values' bits when it fills.
 //
 // Many rows are bound by HBM: 4,352 rows of 151,936 bf16 logits with 20 alternatives take
-// 259 us, 5.1 TB/s like a large copy.  Few rows are bound by what a split costs before its
+// 263 us, 5.0 TB/s like a large copy.  Few rows are bound by what a split costs before its
 // first and behind its last step (245 rows: 47 us, 1.6 TB/s), and a single row by two
 // dependent launches (16 us).
 #include "device_common.h"
