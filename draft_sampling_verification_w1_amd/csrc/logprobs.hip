@@ -261,10 +261,10 @@ struct WaveTop {
   }
 };
 
-// Sums over entries z of one row: m the largest entry (NaN if one is), and with y = z L - k, L = log2 e
-// in binary32, k = ceil(m L): s = sum 2^y, t = sum 2^y y, in binary64.  m L is exact in
-// binary64 (24 x 24 bits), and so is k, however far from zero m lies.  Sums of two sets are
-// brought to one k by a power of two: exact, and no exponential.
+// Sums over entries z of one row: m the largest entry (NaN if one is), and with
+// y = z L - k, L = log2 e in binary32, k = ceil(m L): s = sum 2^y, t = sum 2^y y, in
+// binary64.  m L is exact in binary64 (24 x 24 bits), and so is k, however far from zero m
+// lies.  Sums of two sets are brought to one k by a power of two: exact, and no exponential.
 struct RowSums {
   float m;
   double k, s, t;

@@ -32,7 +32,7 @@ def test_fork_of_reserved_pages(C, lens, reserved, add):  # noqa: F811
     for rows in ([lens, 0, 0], [reserved, 0, 0]):
         assert c.reserve(ints(rows))["status"].tolist() == m.reserve(rows)[0] == [0, 0, 0]
         if rows[0] == lens:
-            old = torch.full((max(1, lens), 1, 64), 1.0, device="cuda") * torch.arange(max(1, lens), device="cuda").view(-1, 1, 1)
+            old = torch.arange(max(1, lens), device="cuda").view(-1, 1, 1).expand(-1, 1, 64).float().contiguous()
             c.append(0, old, old, ints([0, lens, lens, lens]))
             c.commit(ints(rows))
             m.commit(rows, 0)
