@@ -17,7 +17,7 @@ OBJDIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdspark.so")
 SOURCES = ["bias_pass.hip", "select.hip", "verify_aux.hip", "schedule.hip", "misc.hip", "acceptance.hip",
            "sts.hip", "check.hip", "logprobs.hip", "cache.hip",
-           "attend.hip", "api.hip"]
+           "cache_store.hip", "attend.hip", "attend4.hip", "api.hip"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
@@ -33,7 +33,8 @@ HIPCC_FLAGS = [
 # before any difference of infinities is formed); without NaNs to honour, the
 # compiler drops the NaN-quieting v_max it otherwise puts in front of every
 # maximum of matrix-core results.
-EXTRA_FLAGS = {"bias_pass.hip": ["-fno-honor-nans"], "attend.hip": ["-fno-honor-nans"]}
+EXTRA_FLAGS = {"bias_pass.hip": ["-fno-honor-nans"], "attend.hip": ["-fno-honor-nans"],
+               "attend4.hip": ["-fno-honor-nans"]}
 
 
 def _hipcc() -> str:

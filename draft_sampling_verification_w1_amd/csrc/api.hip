@@ -247,8 +247,8 @@ LogprobLayout logprob_layout(int N, int V, int n_top, int skew) {
 // ---- paged cache ---------------------------------------------------------------
 int check_cache(const dspark_cache* c) {
   if (!c) return fail(DSPARK_ERR_ARG, "cache is NULL");
-  if (c->dtype != DSPARK_F32 && c->dtype != DSPARK_BF16)
-    return fail(DSPARK_ERR_DTYPE, "dtype %d is not DSPARK_F32 or DSPARK_BF16", c->dtype);
+  if (c->dtype != DSPARK_F32 && c->dtype != DSPARK_BF16 && c->dtype != DSPARK_MXFP4)
+    return fail(DSPARK_ERR_DTYPE, "dtype %d is not DSPARK_F32, DSPARK_BF16 or DSPARK_MXFP4", c->dtype);
   if (c->slots < 1 || c->slots > kMaxCacheSlots)
     return fail(DSPARK_ERR_SHAPE, "slots=%d outside [1, %d]", c->slots, kMaxCacheSlots);
   if (c->pages < 1 || c->pages > (1 << 24))
@@ -291,7 +291,9 @@ CacheArgs cache_args(const dspark_cache* c, const dspark_cache_tables* t) {
   a.layers = c->layers;
   a.kv_heads = c->kv_heads;
   a.head_dim = c->head_dim;
-  a.page_bytes = c->kv_heads * c->page_size * c->head_dim * (c->dtype == DSPARK_BF16 ? 2 : 4);
+  const int elems = c->kv_heads * c->page_size * c->head_dim;
+  // 4 bits an element and a scale byte per 32, or whole elements
+  a.page_bytes = c->dtype == DSPARK_MXFP4 ? elems / 32 * 17 : elems * (c->dtype == DSPARK_BF16 ? 2 : 4);
   if (t) a.t = tables_of(t);
   return a;
 }
@@ -312,6 +314,26 @@ int check_tokens(const dspark_cache* c, int layer, int N, int heads, const char*
   return DSPARK_OK;
 }
 
+// The type of token rows next to a cache: the pool's, or any beside a 4-bit pool.
+int check_rows(const dspark_cache* c, int dtype, const char* what) {
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16)
+    return fail(DSPARK_ERR_DTYPE, "%s: dtype %d is not DSPARK_F32 or DSPARK_BF16", what, dtype);
+  if (c->dtype != DSPARK_MXFP4 && c->dtype != dtype)
+    return fail(DSPARK_ERR_DTYPE, "%s: dtype %d is not the cache's (%d)", what, dtype, c->dtype);
+  return DSPARK_OK;
+}
+
+// Calls whose rows have the pool's own type.
+int check_own_type(const dspark_cache* c, const char* what, const char* other) {
+  if (c->dtype == DSPARK_MXFP4)
+    return fail(DSPARK_ERR_DTYPE, "%s: a 4-bit cache is used with %s", what, other);
+  return DSPARK_OK;
+}
+
+bool overlap(const void* a, const void* b, size_t bytes) {
+  return (uintptr_t)a < (uintptr_t)b + bytes && (uintptr_t)b < (uintptr_t)a + bytes;
+}
+
 // One layer's pages of K or V.
 void* layer_of(const dspark_cache* c, void* pool, int layer) {
   return static_cast<char*>(pool) + (int64_t)layer * c->pages * cache_args(c, nullptr).page_bytes;
@@ -322,19 +344,20 @@ struct AttendLayout {
   size_t o, ml, cuts, bytes;
 };
 
-// Records of the groups that spans cut: two per span at most.
-AttendLayout attend_layout(const dspark_cache* c, int N, int heads, int max_chunk) {
+// Records of the groups that spans cut: two per span at most.  bf16: the queries' type.
+AttendLayout attend_layout(const dspark_cache* c, bool bf16, int N, int heads, int max_chunk) {
   AttendLayout L = {};
-  const bool bf16 = c->dtype == DSPARK_BF16;
+  const bool packed = c->dtype == DSPARK_MXFP4;
+  const auto grid_of = packed ? attend4_grid : attend_grid;
   const int longest = max_chunk < N ? max_chunk : N;
-  L.rows = attend_rows(bf16, c->head_dim, heads / c->kv_heads, longest);
-  L.grid = attend_grid(bf16, c->head_dim, L.rows);
+  L.rows = (packed ? attend4_rows : attend_rows)(bf16, c->head_dim, heads / c->kv_heads, longest);
+  L.grid = grid_of(bf16, c->head_dim, L.rows);
   // sized for any tile, whatever chunk a call names
   size_t records = 0, most = 0;
-  for (int rows = 16; rows <= attend_max_rows(bf16, c->head_dim); rows += 16) {
-    const size_t n = (size_t)2 * attend_grid(bf16, c->head_dim, rows) * rows;
+  for (int rows = 16; rows <= (packed ? attend4_max_rows : attend_max_rows)(bf16, c->head_dim); rows += 16) {
+    const size_t g = grid_of(bf16, c->head_dim, rows);
+    const size_t n = 2 * g * rows;
     records = records > n ? records : n;
-    const size_t g = attend_grid(bf16, c->head_dim, rows);
     most = most > g ? most : g;
   }
   Carver v;
@@ -343,6 +366,44 @@ AttendLayout attend_layout(const dspark_cache* c, int N, int heads, int max_chun
   L.cuts = v.take((1 + most) * sizeof(AttendCut));
   L.bytes = v.off;
   return L;
+}
+
+// dspark_attend and dspark_attend4 from the token rows on.
+int attend(const dspark_cache* c, const dspark_cache_tables* t, int layer, const void* K,
+           const void* V, int N, int heads, int dtype, const void* q, const int32_t* offsets,
+           float scale, int max_chunk, void* out, void* ws, size_t ws_bytes, void* stream,
+           const char* what) {
+  if (int e = check_tokens(c, layer, N, heads, what)) return e;
+  if (!(scale > 0.f) || scale > 1e30f)
+    return fail(DSPARK_ERR_RANGE, "%s: scale %g is not positive and finite", what, (double)scale);
+  if (max_chunk < 1) return fail(DSPARK_ERR_SHAPE, "%s: max_chunk=%d is below 1", what, max_chunk);
+  if (!K || !V || !q || !offsets || !out)
+    return fail(DSPARK_ERR_ARG, "%s: tensor pointers must be non-NULL", what);
+  if (!aligned16(K) || !aligned16(V) || !aligned16(q) || !aligned16(out))
+    return fail(DSPARK_ERR_ARG, "%s: K, V, q and out must be 16-byte aligned", what);
+  const bool bf16 = dtype == DSPARK_BF16, packed = c->dtype == DSPARK_MXFP4;
+  const AttendLayout L = attend_layout(c, bf16, N, heads, max_chunk);
+  if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
+  if (overlap(q, out, (size_t)N * heads * c->head_dim * (bf16 ? 2 : 4)))
+    return fail(DSPARK_ERR_ARG, "%s: q and out must not overlap", what);
+  AttendArgs a = {};
+  a.c = cache_args(c, t);
+  a.N = N;
+  a.heads = heads;
+  a.group = heads / c->kv_heads;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.q = q;
+  a.K = layer_of(c, const_cast<void*>(K), layer);
+  a.V = layer_of(c, const_cast<void*>(V), layer);
+  a.offsets = offsets;
+  a.out = out;
+  a.grid = L.grid;
+  a.part_o = at<float>(ws, L.o);
+  a.part_ml = at<float>(ws, L.ml);
+  a.cuts = at<AttendCut>(ws, L.cuts);
+  hipError_t e = (packed ? launch_attend4 : launch_attend)(bf16, L.rows, a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, what);
+  return ok();
 }
 
 // Packed tiles, then one float per tile (max |W2| over the tile).
@@ -1069,6 +1130,7 @@ __attribute__((visibility("default"))) int dspark_cache_append(
     const void* k, const void* v, const int32_t* offsets, void* stream) {
   if (int e = check_cache(c)) return e;
   if (int e = check_tables(t)) return e;
+  if (int e = check_own_type(c, "cache_append", "dspark_cache_store")) return e;
   if (int e = check_tokens(c, layer, N, c->kv_heads, "cache_append")) return e;
   if (!K || !V || !k || !v || !offsets)
     return fail(DSPARK_ERR_ARG, "cache_append: tensor pointers must be non-NULL");
@@ -1080,11 +1142,92 @@ __attribute__((visibility("default"))) int dspark_cache_append(
   return ok();
 }
 
+__attribute__((visibility("default"))) int dspark_cache_store(
+    const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, void* K, void* V, int32_t N,
+    int32_t dtype, const void* k, const void* v, const int32_t* offsets, const dspark_rotation* rot,
+    int32_t heads, const void* q, void* q_out, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_rows(c, dtype, "cache_store")) return e;
+  if (heads < 0) return fail(DSPARK_ERR_SHAPE, "cache_store: heads=%d is negative", heads);
+  if (int e = check_tokens(c, layer, N, heads ? heads : c->kv_heads, "cache_store")) return e;
+  if (!K || !V || !k || !v || !offsets)
+    return fail(DSPARK_ERR_ARG, "cache_store: tensor pointers must be non-NULL");
+  if (!aligned16(K) || !aligned16(V) || !aligned16(k) || !aligned16(v))
+    return fail(DSPARK_ERR_ARG, "cache_store: K, V, k and v must be 16-byte aligned");
+  if (rot) {
+    if (rot->dim < 16 || rot->dim > c->head_dim || rot->dim % 16)
+      return fail(DSPARK_ERR_SHAPE, "cache_store: rotation of %d dimensions is no multiple of 16 up to %d",
+                  rot->dim, c->head_dim);
+    if (!rot->freqs || (uintptr_t)rot->freqs % 8)
+      return fail(DSPARK_ERR_ARG, "cache_store: frequencies must be non-NULL and 8-byte aligned");
+    if (rot->interleaved != 0 && rot->interleaved != 1)
+      return fail(DSPARK_ERR_RANGE, "cache_store: interleaved=%d is not 0 or 1", rot->interleaved);
+  }
+  if (heads) {
+    if (!rot) return fail(DSPARK_ERR_ARG, "cache_store: queries without a rotation");
+    if (!q || !q_out) return fail(DSPARK_ERR_ARG, "cache_store: q and q_out must be non-NULL");
+    if (!aligned16(q) || !aligned16(q_out))
+      return fail(DSPARK_ERR_ARG, "cache_store: q and q_out must be 16-byte aligned");
+    const size_t bytes = (size_t)N * heads * c->head_dim * (dtype == DSPARK_BF16 ? 2 : 4);
+    if (q != q_out && overlap(q, q_out, bytes))
+      return fail(DSPARK_ERR_ARG, "cache_store: q_out must be q or not overlap it");
+  }
+  StoreArgs a = {};
+  a.c = cache_args(c, t);
+  a.N = N;
+  a.heads = heads;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.q_out = q_out;
+  a.K = layer_of(c, K, layer);
+  a.V = layer_of(c, V, layer);
+  a.offsets = offsets;
+  a.freqs = rot ? rot->freqs : nullptr;
+  a.rot = rot ? rot->dim : 0;
+  a.interleaved = rot ? rot->interleaved : 0;
+  hipError_t e = launch_cache_store(dtype == DSPARK_BF16, c->dtype == DSPARK_MXFP4, a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_store");
+  return ok();
+}
+
+__attribute__((visibility("default"))) int dspark_cache_read(
+    const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, const void* K, const void* V,
+    int32_t N, int32_t dtype, const int32_t* offsets, const int32_t* first, void* k, void* v,
+    void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (int e = check_rows(c, dtype, "cache_read")) return e;
+  if (int e = check_tokens(c, layer, N, c->kv_heads, "cache_read")) return e;
+  if (!K || !V || !k || !v || !offsets)
+    return fail(DSPARK_ERR_ARG, "cache_read: tensor pointers must be non-NULL");
+  if (!aligned16(K) || !aligned16(V) || !aligned16(k) || !aligned16(v))
+    return fail(DSPARK_ERR_ARG, "cache_read: K, V, k and v must be 16-byte aligned");
+  const size_t bytes = (size_t)N * c->kv_heads * c->head_dim * (dtype == DSPARK_BF16 ? 2 : 4);
+  if (overlap(k, v, bytes)) return fail(DSPARK_ERR_ARG, "cache_read: k and v must not overlap");
+  ReadArgs a = {};
+  a.c = cache_args(c, t);
+  a.N = N;
+  a.K = layer_of(c, const_cast<void*>(K), layer);
+  a.V = layer_of(c, const_cast<void*>(V), layer);
+  a.offsets = offsets;
+  a.first = first ? first : t->lens;
+  a.k = k;
+  a.v = v;
+  hipError_t e = launch_cache_read(dtype == DSPARK_BF16, c->dtype == DSPARK_MXFP4, a, (hipStream_t)stream);
+  if (e != hipSuccess) return hip_fail(e, "cache_read");
+  return ok();
+}
+
 __attribute__((visibility("default"))) size_t dspark_attend_workspace_bytes(const dspark_cache* c,
                                                                            int32_t N, int32_t heads) {
   if (check_cache(c) != DSPARK_OK) return 0;
   if (check_tokens(c, 0, N, heads, "attend") != DSPARK_OK) return 0;
-  return attend_layout(c, N, heads, N).bytes;
+  if (c->dtype != DSPARK_MXFP4)
+    return attend_layout(c, c->dtype == DSPARK_BF16, N, heads, N).bytes;
+  const size_t b = attend_layout(c, true, N, heads, N).bytes, f = attend_layout(c, false, N, heads, N).bytes;
+  return b > f ? b : f;
 }
 
 __attribute__((visibility("default"))) int dspark_attend(
@@ -1093,37 +1236,22 @@ __attribute__((visibility("default"))) int dspark_attend(
     int32_t max_chunk, void* out, void* ws, size_t ws_bytes, void* stream) {
   if (int e = check_cache(c)) return e;
   if (int e = check_tables(t)) return e;
-  if (int e = check_tokens(c, layer, N, heads, "attend")) return e;
-  if (!(scale > 0.f) || scale > 1e30f)
-    return fail(DSPARK_ERR_RANGE, "attend: scale %g is not positive and finite", (double)scale);
-  if (max_chunk < 1) return fail(DSPARK_ERR_SHAPE, "attend: max_chunk=%d is below 1", max_chunk);
-  if (!K || !V || !q || !offsets || !out)
-    return fail(DSPARK_ERR_ARG, "attend: tensor pointers must be non-NULL");
-  if (!aligned16(K) || !aligned16(V) || !aligned16(q) || !aligned16(out))
-    return fail(DSPARK_ERR_ARG, "attend: K, V, q and out must be 16-byte aligned");
-  const AttendLayout L = attend_layout(c, N, heads, max_chunk);
-  if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
-  const size_t q_bytes = (size_t)N * heads * c->head_dim * (c->dtype == DSPARK_BF16 ? 2 : 4);
-  if ((uintptr_t)q < (uintptr_t)out + q_bytes && (uintptr_t)out < (uintptr_t)q + q_bytes)
-    return fail(DSPARK_ERR_ARG, "attend: q and out must not overlap");
-  AttendArgs a = {};
-  a.c = cache_args(c, t);
-  a.N = N;
-  a.heads = heads;
-  a.group = heads / c->kv_heads;
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.q = q;
-  a.K = layer_of(c, const_cast<void*>(K), layer);
-  a.V = layer_of(c, const_cast<void*>(V), layer);
-  a.offsets = offsets;
-  a.out = out;
-  a.grid = L.grid;
-  a.part_o = at<float>(ws, L.o);
-  a.part_ml = at<float>(ws, L.ml);
-  a.cuts = at<AttendCut>(ws, L.cuts);
-  hipError_t e = launch_attend(c->dtype == DSPARK_BF16, L.rows, a, (hipStream_t)stream);
-  if (e != hipSuccess) return hip_fail(e, "attend");
-  return ok();
+  if (int e = check_own_type(c, "attend", "dspark_attend4")) return e;
+  return attend(c, t, layer, K, V, N, heads, c->dtype, q, offsets, scale, max_chunk, out, ws,
+                ws_bytes, stream, "attend");
+}
+
+__attribute__((visibility("default"))) int dspark_attend4(
+    const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, const void* K,
+    const void* V, int32_t N, int32_t heads, int32_t dtype, const void* q, const int32_t* offsets,
+    float scale, int32_t max_chunk, void* out, void* ws, size_t ws_bytes, void* stream) {
+  if (int e = check_cache(c)) return e;
+  if (int e = check_tables(t)) return e;
+  if (c->dtype != DSPARK_MXFP4)
+    return fail(DSPARK_ERR_DTYPE, "attend4: the cache's dtype %d is not DSPARK_MXFP4", c->dtype);
+  if (int e = check_rows(c, dtype, "attend4")) return e;
+  return attend(c, t, layer, K, V, N, heads, dtype, q, offsets, scale, max_chunk, out, ws, ws_bytes,
+                stream, "attend4");
 }
 
 }  // extern "C"

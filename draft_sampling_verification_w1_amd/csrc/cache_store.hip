@@ -1,0 +1,573 @@
+// cache_store.hip -- a chunk's keys and values into the pages with the position rotation
+// and the conversion to 4 bits on the way, and tokens out of the pages again.
+//
+// Rotation.  A token at position p turns the pair (a, b) of its key (and of its queries) by
+// the angle p f_j, f_j in radians per position:
+//   a' = a c - b s,  b' = b c + a s,   c = cos(p f_j), s = sin(p f_j).
+// The angle is a binary64 product (p f_j loses everything in binary32 from some 10^5
+// positions on); it is reduced by the nearest multiple of pi / 2 (two parts of pi / 2, one
+// fma each, exact to 2^-53 or so) and the sine and cosine are their Taylor series on
+// [-pi/4, pi/4] (to r^15: below 2^-52), rounded to binary32 once.  A workgroup works them out
+// for its 8 tokens and all heads use them from LDS: there is no table that ends at some
+// longest position and none to read.  The pair's products and sums are rounded one by one
+// in binary32 (no fma), so that the 4-bit codes follow from the plain definition bit for bit.
+//
+// 4 bits.  32 elements of a token share a power of two 2^e, an element is one of +-{0, 0.5, 1,
+// 1.5, 2, 3, 4, 6} 2^e (E2M1 with E8M0 scales, the types of gfx950's conversions and matrix
+// instructions).  e is the smallest with max |x| <= 7 * 2^e: what saturates at 6 is then off by
+// at most 1, as what is rounded between 4 and 6 is.  The maximum is taken over the bits of
+// |x|, whose order as whole numbers puts infinities and NaN above all numbers.
+//
+// Layout of a 4-bit page (one layer's K or V): the codes of all heads, then their scales.
+//   K codes [head][D / 32][token][16 bytes]: a lane's 16 bytes are 32 elements of one key;
+//   V codes [head][token / 8][D / 64][16][2][8 tokens]: a byte holds two neighbouring elements of one
+//     token, its neighbours the same elements of the other seven; a lane's 16 bytes are 8
+//     keys x 4 elements, from where the conversion builds the matrix operand of 8 keys;
+//   scales [head][D / 32][token], so that 8 keys' scales are one 8-byte load.
+//
+// Work.  A workgroup takes an aligned group of 8 positions of a slot (what V stores side by
+// side) and shares its heads out over its waves and over blockIdx.y; a wave takes one head of K, V
+// or the queries at a time (two of 64 dimensions), 16 bytes per lane and load.  K and
+// queries: a lane holds two 8-element pieces of one token that rotate with each other.  V: a
+// lane holds two neighbouring elements of all 8 tokens, which is a transposition in registers.
+#include "device_common.h"
+#include "kernels.h"
+
+namespace dspark {
+
+namespace {
+
+constexpr int kGroup = 8;  // positions of a group
+
+__device__ __forceinline__ bool page_ok(const CacheArgs& a, int p) { return p >= 0 && p < a.pages; }
+
+// A group of positions of a slot that some of the call's token rows have.
+struct Place {
+  int row;       // first token row of the group, -1: there is none
+  int n;         // its rows
+  int e0;        // place of the first among the group's 8 positions
+  int page;      // page id, -1: none
+  int at;        // the group's first position in the page
+  int64_t pos;   // position of the first row
+};
+
+// The workgroup's group (blockIdx.x).  Slot s's groups are numbered from offsets[s] / 8 + 3 s on,
+// which leaves room for a group that is cut at either end.  Each thread looks at its slots'
+// offsets and start position at once, so that finding the group is one round trip, its page
+// another.
+__device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int32_t* offsets,
+                                            const int32_t* starts) {
+  __shared__ int found[6];
+  const int w = blockIdx.x;
+  if (threadIdx.x == 0) found[0] = -1;
+  __syncthreads();
+  for (int s = threadIdx.x; s < c.slots; s += 256) {
+    const int o0 = min(max(offsets[s], 0), N), o1 = min(max(offsets[s + 1], o0), N);
+    const int start = starts[s], held = c.t.held[s];
+    const int first = o0 / kGroup + 3 * s;
+    if (o0 < o1 && first <= w && w < o1 / kGroup + 3 * (s + 1)) {
+      found[0] = s;
+      found[1] = o0;
+      found[2] = o1;
+      found[3] = w - first;
+      found[4] = start;
+      found[5] = held;
+    }
+  }
+  __syncthreads();
+  Place g = {-1, 0, 0, -1, 0, 0};
+  const int s = found[0], o0 = found[1], o1 = found[2], start = found[4];
+  if (s < 0) return g;
+  const int64_t base = max(start, 0);
+  const int64_t first = (base / kGroup + found[3]) * kGroup;  // of the group
+  g.e0 = first < base ? (int)(base - first) : 0;
+  g.pos = first + g.e0;
+  const int64_t row = o0 + (g.pos - base);
+  if (row >= o1) return g;
+  g.row = (int)row;
+  g.n = (int)min((int64_t)(kGroup - g.e0), o1 - row);
+  const int64_t j = g.pos >> c.page_shift;
+  if (start >= 0 && j < min(found[5], c.max_pages)) {
+    const int p = c.t.table[(int64_t)s * c.max_pages + j];
+    if (page_ok(c, p)) g.page = p;
+  }
+  g.at = (int)(first & ((1 << c.page_shift) - 1));
+  return g;
+}
+
+// 8 elements in binary32.
+__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
+  const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const f32x4 w = reinterpret_cast<const f32x4*>(p)[h];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[4 * h + i] = w[i];
+  }
+}
+// 8 elements rounded to nearest even.
+__device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
+  bf16x8 b;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) b[i] = (__bf16)x[i];
+  *reinterpret_cast<bf16x8*>(p) = b;
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    reinterpret_cast<f32x4*>(p)[h] = f32x4{x[4 * h], x[4 * h + 1], x[4 * h + 2], x[4 * h + 3]};
+}
+
+// sin and cos of a binary64 angle (below 2^40 in magnitude), rounded to binary32.
+__device__ __forceinline__ float2 cos_sin(double angle) {
+  const double k = rint(angle * 0.63661977236758134);
+  double r = fma(-k, 1.5707963267948966, angle);
+  r = fma(-k, 6.123233995736766e-17, r);
+  const double z = r * r;
+  double s = -7.6471637318198164e-13;  // -1 / 15!
+  s = fma(s, z, 1.6059043836821613e-10);
+  s = fma(s, z, -2.5052108385441720e-08);
+  s = fma(s, z, 2.7557319223985893e-06);
+  s = fma(s, z, -1.9841269841269841e-04);
+  s = fma(s, z, 8.3333333333333332e-03);
+  s = fma(s, z, -1.6666666666666666e-01);
+  s = fma(s, z * r, r);
+  double c = -1.1470745597729725e-11;  // -1 / 14!
+  c = fma(c, z, 2.0876756987868100e-09);
+  c = fma(c, z, -2.7557319223985888e-07);
+  c = fma(c, z, 2.4801587301587302e-05);
+  c = fma(c, z, -1.3888888888888889e-03);
+  c = fma(c, z, 4.1666666666666664e-02);
+  c = fma(c, z, -0.5);
+  c = fma(c, z, 1.0);
+  const int q = (int)((int64_t)k & 3);
+  const float fs = (float)s, fc = (float)c;
+  const float a = (q & 1) ? fs : fc, b = (q & 1) ? fc : fs;
+  return make_float2((q == 1 || q == 2) ? -a : a, (q & 2) ? -b : b);
+}
+
+// (a, b) turned; every operation rounded.
+__device__ __forceinline__ void turn(float& a, float& b, float2 cs) {
+#pragma clang fp contract(off)
+  const float x = a * cs.x - b * cs.y;
+  const float y = b * cs.x + a * cs.y;
+  a = x;
+  b = y;
+}
+
+// The scale byte of a block whose largest |x| has these bits: e + 127 within [7, 252], or
+// 255 (every value is NaN) if one is infinite or NaN.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
+  const int e = (int)(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x600000u);
+  return top >= 0x7F800000u ? 255u : (uint32_t)min(max(e, 7), 252);
+}
+// The power of two of a scale byte; blocks without values take zero codes.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+template <int kSel>
+__device__ __forceinline__ uint32_t code2(uint32_t old, float lo, float hi, float scale) {
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, lo, hi, scale, kSel);
+}
+__device__ __forceinline__ uint32_t code8(const float (&x)[8], float scale) {
+  uint32_t w = code2<0>(0u, x[0], x[1], scale);
+  w = code2<1>(w, x[2], x[3], scale);
+  w = code2<2>(w, x[4], x[5], scale);
+  return code2<3>(w, x[6], x[7], scale);
+}
+
+// Largest of 16 neighbouring lanes, in all of them (rotations within a row of 16 lanes).
+__device__ __forceinline__ uint32_t max16(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xF, 0xF, true));
+  return x;
+}
+
+// Two neighbouring elements in binary32.
+__device__ __forceinline__ float2 load2(const uint16_t* p) {
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+  return make_float2(bf16_lo(w), bf16_hi(w));
+}
+__device__ __forceinline__ float2 load2(const float* p) { return *reinterpret_cast<const float2*>(p); }
+
+// Byte of token 0 of the group's 8 in V's codes: elements 2 i and 2 i + 1.
+template <int D>
+__device__ __forceinline__ int v_code_at(int group, int i) {
+  const int n = i / (D / 32), rest = i % (D / 32);
+  return ((group * (D / 64) + rest / 2) * 16 + n) * 16 + (rest & 1) * 8;
+}
+
+// Head h of K: two 8-element pieces (c0, c1) of token t, turned.
+template <typename E, int D, bool kPacked>
+__device__ __forceinline__ void store_k(const StoreArgs& a, const Place& g, int h, int t, int c0,
+                                        int c1, const float (&x)[8], const float (&y)[8], bool live,
+                                        uint32_t* top) {
+  const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
+  const int row = g.at + g.e0 + t;
+  if constexpr (kPacked) {
+    // the pieces' maxima meet in LDS: a block of 32 elements may be held by any lanes of the wave
+    uint32_t mx = 0u, my = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      mx = max(mx, magnitude(x[i]));
+      my = max(my, magnitude(y[i]));
+    }
+    if (live) {
+      top[c0] = mx;
+      top[c1] = my;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+    if (live && g.page >= 0) {
+      uint8_t* blob = static_cast<uint8_t*>(a.K) + (int64_t)g.page * a.c.page_bytes;
+      uint8_t* codes = blob + h * (page * (D / 2));
+      uint8_t* scales = blob + H * page * (D / 2) + h * (page * (D / 32));
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int c = p ? c1 : c0, b = c >> 2;
+        const u32x4 m = *reinterpret_cast<const u32x4*>(top + 4 * b);
+        const uint32_t byte = scale_byte(max(max(m.x, m.y), max(m.z, m.w)));
+        const uint32_t code = byte == 255u ? 0u : code8(p ? y : x, scale_of(byte));
+        *reinterpret_cast<uint32_t*>(codes + (b * page + row) * 16 + (c & 3) * 4) = code;
+        if ((c & 3) == 0) scales[b * page + row] = (uint8_t)byte;
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  } else if (live && g.page >= 0) {
+    constexpr int kE = 16 / (int)sizeof(E);
+    E* to = static_cast<E*>(a.K) + ((int64_t)g.page * H + h) * page * D;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const int c = p ? c1 : c0;
+      alignas(16) E piece[8];
+      store8(piece, p ? y : x);
+#pragma unroll
+      for (int i = 0; i < 8 / kE; ++i)
+        *reinterpret_cast<u32x4*>(to + ((int64_t)(c * (8 / kE) + i) * page + row) * kE) =
+            *reinterpret_cast<const u32x4*>(piece + i * kE);
+    }
+  }
+}
+
+// Elements 2 i and 2 i + 1 of head h of V, all tokens of the group.
+template <typename E, int D, bool kPacked>
+__device__ __forceinline__ void store_v(const StoreArgs& a, const Place& g, int h, int i, bool live) {
+  const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
+  const E* from = static_cast<const E*>(a.v) + ((int64_t)g.row * H + h) * D + 2 * i;
+  if constexpr (kPacked) {
+    float2 x[kGroup];
+#pragma unroll
+    for (int t = 0; t < kGroup; ++t)
+      x[t] = live ? load2(from + (int64_t)min(t, g.n - 1) * H * D) : make_float2(0.f, 0.f);
+    uint32_t word[2] = {0u, 0u}, bytes[2] = {0u, 0u};
+#pragma unroll
+    for (int t = 0; t < kGroup; ++t) {
+      const uint32_t byte = scale_byte(max16(max(magnitude(x[t].x), magnitude(x[t].y))));
+      const float s = scale_of(byte);
+      uint32_t& w = word[t >> 2];
+      uint32_t old = w;
+      if ((t & 3) == 0) w = code2<0>(w, x[t].x, x[t].y, s);
+      if ((t & 3) == 1) w = code2<1>(w, x[t].x, x[t].y, s);
+      if ((t & 3) == 2) w = code2<2>(w, x[t].x, x[t].y, s);
+      if ((t & 3) == 3) w = code2<3>(w, x[t].x, x[t].y, s);
+      if (byte == 255u) w = old;
+      bytes[t >> 2] |= byte << (8 * (t & 3));
+    }
+    if (!live || g.page < 0) return;
+    uint8_t* blob = static_cast<uint8_t*>(a.V) + (int64_t)g.page * a.c.page_bytes;
+    uint8_t* code = blob + h * (page * (D / 2)) + v_code_at<D>(g.at >> 3, i);
+    uint8_t* scale = blob + H * page * (D / 2) + h * (page * (D / 32)) + (i >> 4) * page + g.at;
+    if (g.n == kGroup) {
+      *reinterpret_cast<u32x2*>(code) = u32x2{word[0], word[1]};
+      if ((i & 15) == 0) *reinterpret_cast<u32x2*>(scale) = u32x2{bytes[0], bytes[1]};
+    } else {
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) {
+        if (t >= g.n) break;
+        code[g.e0 + t] = (uint8_t)(word[t >> 2] >> (8 * (t & 3)));
+        if ((i & 15) == 0) scale[g.e0 + t] = (uint8_t)(bytes[t >> 2] >> (8 * (t & 3)));
+      }
+    }
+  } else {
+    if (!live || g.page < 0) return;
+    constexpr int kE = 16 / (int)sizeof(E);
+    typedef E Pair __attribute__((ext_vector_type(2)));
+    alignas(16) E x[2][kGroup];
+#pragma unroll
+    for (int t = 0; t < kGroup; ++t) {
+      const Pair p = *reinterpret_cast<const Pair*>(from + (int64_t)min(t, g.n - 1) * H * D);
+      x[0][t] = p[0];
+      x[1][t] = p[1];
+    }
+    E* to = static_cast<E*>(a.V) + ((int64_t)g.page * H + h) * page * D;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (g.n == kGroup) {
+#pragma unroll
+        for (int p = 0; p < kGroup / kE; ++p)
+          *reinterpret_cast<u32x4*>(to + ((int64_t)(g.at / kE + p) * D + 2 * i + e) * kE) =
+              *reinterpret_cast<const u32x4*>(&x[e][p * kE]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < kGroup; ++t) {
+          if (t >= g.n) break;
+          const int row = g.at + g.e0 + t;
+          to[((int64_t)(row / kE) * D + 2 * i + e) * kE + row % kE] = x[e][t];
+        }
+      }
+    }
+  }
+}
+
+template <typename E, int D, bool kPacked>
+__global__ __launch_bounds__(256) void k_cache_store(StoreArgs a) {
+  constexpr int kUnits = D / 16;                           // lanes of a token of one head
+  constexpr int kHeads = kUnits < 8 ? 8 / kUnits : 1;      // heads that a wave takes at once
+  constexpr int kTurns = kUnits > 8 ? kUnits / 8 : 1;      // or rounds of the wave for a head
+  __shared__ float2 cs[kGroup * (D / 2)];
+  __shared__ __align__(16) uint32_t tops[4][64 / kUnits * (D / 8)];
+  const Place g = find_place(a.c, a.N, a.offsets, a.c.t.lens);
+  if (g.row < 0) return;
+  const int half = a.rot / 2;
+  for (int x = threadIdx.x; x < g.n * half; x += 256) {
+    const int t = x / half, j = x - t * half;
+    cs[t * half + j] = cos_sin((double)(g.pos + t) * a.freqs[j]);
+  }
+  __syncthreads();
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int kv = (a.c.kv_heads + kHeads - 1) / kHeads, qs = (a.heads + kHeads - 1) / kHeads;
+  const int tasks = 2 * kv + qs;
+  for (int task = (int)blockIdx.y * 4 + wave; task < tasks; task += 4 * (int)gridDim.y) {
+    const bool values = task >= kv && task < 2 * kv;
+    const bool query = task >= 2 * kv;
+    const int first = (query ? task - 2 * kv : (values ? task - kv : task)) * kHeads;
+#pragma unroll
+    for (int r = 0; r < kTurns; ++r) {
+      const int x = r * 64 + lane;
+      const int h = first + (kHeads > 1 ? x / (8 * kUnits) : 0);
+      if (values) {
+        const int i = kHeads > 1 ? x % (D / 2) : x;
+        store_v<E, D, kPacked>(a, g, min(h, a.c.kv_heads - 1), i, h < a.c.kv_heads);
+        continue;
+      }
+      const int H = query ? a.heads : a.c.kv_heads;
+      const int t = x / kUnits % kGroup, u = x % kUnits;
+      const bool live = h < H && t < g.n;
+      const bool apart = !a.interleaved && u < a.rot / 16;
+      const int c0 = apart ? u : 2 * u, c1 = apart ? u + a.rot / 16 : 2 * u + 1;
+      float p[8], q[8];
+      const int64_t at = ((int64_t)(g.row + t) * H + h) * D;
+      if (live) {
+        const E* from = static_cast<const E*>(query ? a.q : a.k) + at;
+        load8(from + 8 * c0, p);
+        load8(from + 8 * c1, q);
+        if (u < a.rot / 16) {
+          const float2* w = cs + t * half + 8 * u;
+          if (apart) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) turn(p[i], q[i], w[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              turn(p[2 * i], p[2 * i + 1], w[i]);
+              turn(q[2 * i], q[2 * i + 1], w[4 + i]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = q[i] = 0.f;
+      }
+      if (query) {
+        if (live) {
+          E* to = static_cast<E*>(a.q_out) + at;
+          store8(to + 8 * c0, p);
+          store8(to + 8 * c1, q);
+        }
+      } else {
+        // lanes of one token of one head share D / 8 maxima
+        store_k<E, D, kPacked>(a, g, h, t, c0, c1, p, q, live, tops[wave] + lane / kUnits * (D / 8));
+      }
+    }
+  }
+}
+
+// ---- tokens out of the pages -----------------------------------------------------------
+__device__ __forceinline__ void put8(uint16_t* to, uint32_t code, float s) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  union { bf16x2 b[4]; u32x4 w; } x;
+  x.b[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 0);
+  x.b[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 1);
+  x.b[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 2);
+  x.b[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 3);
+  *reinterpret_cast<u32x4*>(to) = x.w;
+}
+__device__ __forceinline__ void put8(float* to, uint32_t code, float s) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 0);
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 1);
+  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 2);
+  const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 3);
+  reinterpret_cast<f32x4*>(to)[0] = f32x4{a[0], a[1], b[0], b[1]};
+  reinterpret_cast<f32x4*>(to)[1] = f32x4{c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ void put2(uint16_t* to, uint32_t code, float s) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<bf16x2*>(to) = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 0);
+}
+__device__ __forceinline__ void put2(float* to, uint32_t code, float s) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  *reinterpret_cast<f32x2*>(to) = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 0);
+}
+// A block of values that are all NaN.
+constexpr uint32_t kNoScale = 255u;
+
+template <typename E, int D, bool kPacked>
+__global__ __launch_bounds__(256) void k_cache_read(ReadArgs a) {
+  constexpr int kE = 16 / (int)sizeof(E);
+  const Place g = find_place(a.c, a.N, a.offsets, a.first);
+  if (g.row < 0) return;
+  const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int64_t p = max(g.page, 0);
+  const bool there = g.page >= 0;
+  for (int task = (int)blockIdx.y * 4 + wave; task < 2 * H; task += 4 * (int)gridDim.y) {
+    const bool values = task >= H;
+    const int h = values ? task - H : task;
+    E* const out = static_cast<E*>(values ? a.v : a.k) + ((int64_t)g.row * H + h) * D;
+    const int64_t step = (int64_t)H * D;  // from a token's row to the next
+    if (!values) {
+      // a lane takes 8 elements of a token
+      for (int x = lane; x < kGroup * (D / 8); x += 64) {
+        const int t = x / (D / 8), c = x % (D / 8);
+        if (t >= g.n) break;
+        const int row = g.at + g.e0 + t;
+        E* const to = out + t * step + 8 * c;
+        if constexpr (kPacked) {
+          const uint8_t* blob = static_cast<const uint8_t*>(a.K) + p * a.c.page_bytes;
+          const uint32_t code =
+              *reinterpret_cast<const uint32_t*>(blob + h * (page * (D / 2)) + ((c >> 2) * page + row) * 16 + (c & 3) * 4);
+          const uint32_t byte = blob[H * page * (D / 2) + h * (page * (D / 32)) + (c >> 2) * page + row];
+          put8(to, there ? code : 0u, there ? (byte == kNoScale ? NAN : scale_of(byte)) : 1.f);
+        } else {
+          const E* from = static_cast<const E*>(a.K) + (p * H + h) * page * D;
+#pragma unroll
+          for (int i = 0; i < 8 / kE; ++i) {
+            const u32x4 w = *reinterpret_cast<const u32x4*>(from + ((int64_t)(c * (8 / kE) + i) * page + row) * kE);
+            *reinterpret_cast<u32x4*>(to + i * kE) = there ? w : u32x4{0u, 0u, 0u, 0u};
+          }
+        }
+      }
+    } else {
+      // a lane takes two neighbouring elements of the group's tokens
+      for (int i = lane; i < D / 2; i += 64) {
+        if constexpr (kPacked) {
+          const uint8_t* blob = static_cast<const uint8_t*>(a.V) + p * a.c.page_bytes;
+          const u32x2 code = *reinterpret_cast<const u32x2*>(blob + h * (page * (D / 2)) + v_code_at<D>(g.at >> 3, i));
+          const u32x2 byte = *reinterpret_cast<const u32x2*>(
+              blob + H * page * (D / 2) + h * (page * (D / 32)) + (i >> 4) * page + g.at);
+#pragma unroll
+          for (int t = 0; t < kGroup; ++t) {
+            const int r = t - g.e0;
+            const uint32_t s = byte[t >> 2] >> (8 * (t & 3)) & 255u;
+            if (r >= 0 && r < g.n)
+              put2(out + r * step + 2 * i, there ? code[t >> 2] >> (8 * (t & 3)) : 0u,
+                   there ? (s == kNoScale ? NAN : scale_of(s)) : 1.f);
+          }
+        } else {
+          typedef E Pair __attribute__((ext_vector_type(2)));
+          const E* from = static_cast<const E*>(a.V) + (p * H + h) * page * D;
+          alignas(16) E x[2][kGroup];
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int q = 0; q < kGroup / kE; ++q)
+              *reinterpret_cast<u32x4*>(&x[e][q * kE]) = *reinterpret_cast<const u32x4*>(
+                  from + ((int64_t)(g.at / kE + q) * D + 2 * i + e) * kE);
+#pragma unroll
+          for (int t = 0; t < kGroup; ++t) {
+            const int r = t - g.e0;
+            if (r >= 0 && r < g.n)
+              *reinterpret_cast<Pair*>(out + r * step + 2 * i) =
+                  there ? Pair{x[0][t], x[1][t]} : Pair{(E)0, (E)0};
+          }
+        }
+      }
+    }
+  }
+}
+
+// Workgroups that share a group's heads: as few as fill the card.
+unsigned split_of(int groups, int tasks) {
+  const int most = (tasks + 3) / 4;
+  const int want = (2048 + groups - 1) / groups;
+  return (unsigned)(want < most ? want : most);
+}
+
+}  // namespace
+
+hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStream_t stream) {
+  TimingScope t("cache_store", stream);
+  const int per = a.c.head_dim == 64 ? 2 : 1;
+  const int tasks = 2 * ((a.c.kv_heads + per - 1) / per) + (a.heads + per - 1) / per;
+  const int active = a.N / kGroup + a.c.slots;
+  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(active, tasks));
+#define STORE(E, D, P) hipLaunchKernelGGL((k_cache_store<E, D, P>), grid, dim3(256), 0, stream, a)
+#define STORE_DIMS(E, P)                       \
+  switch (a.c.head_dim) {                      \
+    case 64: STORE(E, 64, P); break;           \
+    case 128: STORE(E, 128, P); break;         \
+    default: STORE(E, 256, P); break;          \
+  }
+  if (bf16 && packed) {
+    STORE_DIMS(uint16_t, true)
+  } else if (bf16) {
+    STORE_DIMS(uint16_t, false)
+  } else if (packed) {
+    STORE_DIMS(float, true)
+  } else {
+    STORE_DIMS(float, false)
+  }
+#undef STORE_DIMS
+#undef STORE
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStream_t stream) {
+  TimingScope t("cache_read", stream);
+  const int active = a.N / kGroup + a.c.slots;
+  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(active, 2 * a.c.kv_heads));
+#define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a)
+#define READ_DIMS(E, P)                       \
+  switch (a.c.head_dim) {                     \
+    case 64: READ(E, 64, P); break;           \
+    case 128: READ(E, 128, P); break;         \
+    default: READ(E, 256, P); break;          \
+  }
+  if (bf16 && packed) {
+    READ_DIMS(uint16_t, true)
+  } else if (bf16) {
+    READ_DIMS(uint16_t, false)
+  } else if (packed) {
+    READ_DIMS(float, true)
+  } else {
+    READ_DIMS(float, false)
+  }
+#undef READ_DIMS
+#undef READ
+  return hipGetLastError();
+}
+
+}  // namespace dspark

@@ -325,6 +325,35 @@ hipError_t launch_cache_append(const CacheArgs& a, bool bf16, void* K, void* V, 
                                const void* k, const void* v, const int32_t* offsets,
                                hipStream_t stream);
 
+// A chunk's keys and values into the pages, rotated and in the pool's type (cache_store.hip).
+struct StoreArgs {
+  CacheArgs c;
+  int N, heads;            // token rows; query heads (0: no queries)
+  const void* k;           // [N, kv_heads, head_dim]
+  const void* v;
+  const void* q;           // [N, heads, head_dim]
+  void* q_out;
+  void* K;                 // one layer's pages
+  void* V;
+  const int32_t* offsets;  // [slots + 1]
+  const double* freqs;     // [rot / 2] radians per position
+  int rot;                 // dimensions that rotate (0: none)
+  int interleaved;         // pairs (2 j, 2 j + 1), else (j, j + rot / 2)
+};
+hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStream_t stream);
+// Tokens out of the pages: slot s's rows from position first[s] on.
+struct ReadArgs {
+  CacheArgs c;
+  int N;
+  const void* K;
+  const void* V;
+  const int32_t* offsets;
+  const int32_t* first;    // [slots]
+  void* k;                 // [N, kv_heads, head_dim]
+  void* v;
+};
+hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStream_t stream);
+
 // A group of rows whose key steps lie in several spans (attend.hip); rows 0: none.
 struct AttendCut {
   int32_t row0, rows, token0, head;
@@ -350,5 +379,10 @@ int attend_grid(bool bf16, int head_dim, int rows);
 int attend_max_rows(bool bf16, int head_dim);
 int attend_rows(bool bf16, int head_dim, int group, int max_chunk);
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
+// The same over a 4-bit cache (attend4.hip); bf16: the queries' type.
+int attend4_grid(bool bf16, int head_dim, int rows);
+int attend4_max_rows(bool bf16, int head_dim);
+int attend4_rows(bool bf16, int head_dim, int group, int max_chunk);
+hipError_t launch_attend4(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
 
 }  // namespace dspark

@@ -15,7 +15,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdspark.so")
 
-F32, BF16 = 0, 1
+F32, BF16, MXFP4 = 0, 1, 2
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16}
 
 SYMBOLS = ("dspark_w2_packed_bytes", "dspark_pack_w2", "dspark_workspace_bytes",
@@ -25,8 +25,8 @@ SYMBOLS = ("dspark_w2_packed_bytes", "dspark_pack_w2", "dspark_workspace_bytes",
            "dspark_emitted_tokens", "dspark_logprobs_workspace_bytes", "dspark_token_logprobs",
            "dspark_cache_init", "dspark_cache_fork", "dspark_cache_reserve", "dspark_cache_commit",
            "dspark_cache_free", "dspark_cache_compact_workspace_bytes", "dspark_cache_compact",
-           "dspark_cache_copy_pages", "dspark_cache_append", "dspark_attend_workspace_bytes",
-           "dspark_attend", "dspark_check_inputs", "dspark_last_error", "dspark_timing_enable",
+           "dspark_cache_copy_pages", "dspark_cache_append", "dspark_cache_store", "dspark_cache_read",
+           "dspark_attend_workspace_bytes", "dspark_attend", "dspark_attend4", "dspark_check_inputs", "dspark_last_error", "dspark_timing_enable",
            "dspark_timing_report")
 
 
@@ -43,6 +43,10 @@ class Cache(ctypes.Structure):
 
 class CacheTables(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("table", "lens", "held", "refs", "free_bits", "n_free")]
+
+
+class CacheRotation(ctypes.Structure):
+    _fields_ = [("freqs", ctypes.c_void_p), ("dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 class DsparkError(RuntimeError):
@@ -106,10 +110,15 @@ def lib() -> ctypes.CDLL:
         L.dspark_cache_compact.argtypes = [C, CT, CT, _vp, _vp, _vp, _vp, size, _vp]
         L.dspark_cache_copy_pages.argtypes = [C, _vp, _vp, i32, _vp, _vp, _vp, _vp]
         L.dspark_cache_append.argtypes = [C, CT, i32, _vp, _vp, i32, _vp, _vp, _vp, _vp]
+        L.dspark_cache_store.argtypes = [C, CT, i32, _vp, _vp, i32, i32, _vp, _vp, _vp,
+                                         ctypes.POINTER(CacheRotation), i32, _vp, _vp, _vp]
+        L.dspark_cache_read.argtypes = [C, CT, i32, _vp, _vp, i32, i32, _vp, _vp, _vp, _vp, _vp]
         L.dspark_attend_workspace_bytes.argtypes = [C, i32, i32]
         L.dspark_attend_workspace_bytes.restype = size
         L.dspark_attend.argtypes = [C, CT, i32, _vp, _vp, i32, i32, _vp, _vp, ctypes.c_float, i32,
                                     _vp, _vp, size, _vp]
+        L.dspark_attend4.argtypes = [C, CT, i32, _vp, _vp, i32, i32, i32, _vp, _vp, ctypes.c_float,
+                                     i32, _vp, _vp, size, _vp]
         L.dspark_last_error.restype = ctypes.c_char_p
         L.dspark_timing_enable.argtypes = [ctypes.c_int]
         L.dspark_timing_report.argtypes = [ctypes.c_char_p, ctypes.c_size_t]
@@ -120,7 +129,8 @@ def lib() -> ctypes.CDLL:
                      "dspark_check_inputs", "dspark_emitted_tokens", "dspark_token_logprobs",
                      "dspark_cache_init", "dspark_cache_fork", "dspark_cache_reserve",
                      "dspark_cache_commit", "dspark_cache_free", "dspark_cache_compact",
-                     "dspark_cache_copy_pages", "dspark_cache_append", "dspark_attend",
+                     "dspark_cache_copy_pages", "dspark_cache_append", "dspark_cache_store",
+                     "dspark_cache_read", "dspark_attend", "dspark_attend4",
                      "dspark_timing_enable", "dspark_timing_report"):
             getattr(L, name).restype = ctypes.c_int
         _lib = L

@@ -67,7 +67,8 @@ typedef enum {
   DSPARK_ERR_HIP = -6         /* HIP runtime error while enqueuing */
 } dspark_status;
 
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+/* DSPARK_MXFP4: a cache's pages in 4 bits (below), no tensor's type. */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_MXFP4 = 2 } dspark_dtype;
 
 /* One decoding round's problem: R requests, gamma block positions, vocabulary
  * V, Markov-head rank, storage dtype and the round's random seed.
@@ -301,7 +302,16 @@ int dspark_token_logprobs(int32_t dtype, int32_t N, int32_t V, int64_t ld, const
  * Storage, owned by the caller (E = 16 bytes of elements: 8 bf16, 4 f32):
  *   K [layers, pages, kv_heads, head_dim / E, page_size, E]
  *   V [layers, pages, kv_heads, page_size / E, head_dim, E]   (dtype, 16-byte aligned)
- * (the operand orders of the matrix cores).  Tables (dspark_cache_tables):
+ * (the operand orders of the matrix cores).  A cache of type DSPARK_MXFP4 holds 4 bits
+ * an element: 32 elements of a token (one head's elements 32 b .. 32 b + 31) share a scale
+ * 2^(byte - 127), an element is a sign bit and the place of its magnitude among 0, 0.5, 1, 1.5,
+ * 2, 3, 4, 6 times the scale (OCP MX: E2M1 with E8M0 scales).  K and V are bytes
+ * [layers, pages, kv_heads * page_size * head_dim * 17 / 32], a page (D = head_dim):
+ *   K  codes [kv_heads, D / 32, page_size, 16]: byte i holds elements 2 i (low bits), 2 i + 1
+ *   V  codes [kv_heads, page_size / 8, D / 64, 16, 2, 8]: byte (o, g, n, h, t) holds elements
+ *      n D / 16 + 4 g + 2 h (low bits) and the next one of token 8 o + t
+ *   both: then scale bytes [kv_heads, D / 32, page_size].
+ * Tables (dspark_cache_tables):
  *   table     [slots, max_pages] int32, a slot's pages in order, -1 behind them
  *   lens      [slots] int32, tokens cached
  *   held      [slots] int32, pages held (at least ceil(lens / page_size))
@@ -399,10 +409,48 @@ int dspark_cache_copy_pages(const dspark_cache* c, void* K, void* V, int32_t n, 
  * k and v [N, kv_heads, head_dim], row i at position lens[s] + i - offsets[s];
  * rows behind offsets[slots] belong to nobody.  The pages have to be reserved;
  * a token without one is dropped.  offsets [slots + 1] int32, from 0, not
- * falling.  Limits: 1 <= N <= 2^22. */
+ * falling.  Limits: 1 <= N <= 2^22.  Not for a 4-bit cache (dspark_cache_store). */
 int dspark_cache_append(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, void* K,
                         void* V, int32_t N, const void* k, const void* v, const int32_t* offsets,
                         void* stream);
+
+/* Rotation by position: at position p the pair of elements (a, b) becomes
+ * (a c - b s, b c + a s) with c, s = cos, sin(p freqs[j]), the angle a binary64 product, c
+ * and s rounded to binary32, then every product and sum.  The pairs are elements (j, j + dim / 2), or
+ * (2 j, 2 j + 1) if interleaved is 1, j < dim / 2; elements from dim on stay as they are.  freqs
+ * [dim / 2] float64 in device memory, radians per position, angles below 2^40 in magnitude.
+ * dim: a multiple of 16, 16 <= dim <= head_dim. */
+typedef struct {
+  const double* freqs;
+  int32_t dim;
+  int32_t interleaved;
+} dspark_rotation;
+
+/* dspark_cache_append with what a layer does around it, in one pass: keys and
+ * queries rotated by their positions lens[s] + i - offsets[s] (rot; NULL: no rotation),
+ * keys and values converted to the cache's type.  dtype: of k, v, q and q_out; the cache's own, or
+ * DSPARK_F32 or DSPARK_BF16 for a 4-bit cache.  heads: query heads, a multiple of kv_heads,
+ * q [N, heads, head_dim] to q_out (which may be q, and must not overlap it otherwise); 0: no
+ * queries (q and q_out are not read).  Queries need rot.  Rows behind offsets[slots] of q_out are left
+ * as they were; queries of tokens without a page are rotated like the others.
+ * 4 bits: rotated keys (binary32) and values are divided by the block's scale, the smallest power of two
+ * within 2^-120 .. 2^125 of which the block's largest magnitude is at most 7, and rounded to the
+ * nearest (ties to the even code), 6 at most.  A block with an infinity or NaN gets the scale
+ * byte 255: all of it is NaN. */
+int dspark_cache_store(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, void* K,
+                       void* V, int32_t N, int32_t dtype, const void* k, const void* v,
+                       const int32_t* offsets, const dspark_rotation* rot, int32_t heads,
+                       const void* q, void* q_out, void* stream);
+
+/* Tokens out of the pages again, as dense rows: row offsets[s] + i of k and v
+ * [N, kv_heads, head_dim] is slot s's token at position first[s] + i (first NULL: lens[s], the chunk
+ * behind the committed tokens).  dtype: as in dspark_cache_store (what 4 bits stand for is a bf16
+ * value: no rounding).  Positions that no page of the slot holds are 0, and all of a slot whose
+ * first is negative; rows behind offsets[slots] are left as they were.  Positions that a page holds and no
+ * token was written to have any value.  first [slots] int32.  k and v must not overlap. */
+int dspark_cache_read(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
+                      const void* K, const void* V, int32_t N, int32_t dtype, const int32_t* offsets,
+                      const int32_t* first, void* k, void* v, void* stream);
 
 /* Attention of a chunk of new tokens per slot over the cache (after
  * dspark_cache_append wrote the chunk): row i of slot s, head h, sees the
@@ -417,12 +465,21 @@ int dspark_cache_append(const dspark_cache* c, const dspark_cache_tables* t, int
  * out must not overlap q (a row's keys are shared out over workgroups).
  * max_chunk: the longest chunk expected, >= 1; it chooses the tiling only, any
  * chunk is computed.  scale > 0.  heads a multiple of kv_heads, N * heads <= 2^30.
- * ws: dspark_attend_workspace_bytes(c, N, heads) bytes, 256-byte aligned. */
+ * ws: dspark_attend_workspace_bytes(c, N, heads) bytes, 256-byte aligned.  Not for a
+ * 4-bit cache (dspark_attend4). */
 size_t dspark_attend_workspace_bytes(const dspark_cache* c, int32_t N, int32_t heads);
 int dspark_attend(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer, const void* K,
                   const void* V, int32_t N, int32_t heads, const void* q, const int32_t* offsets,
                   float scale, int32_t max_chunk, void* out, void* ws, size_t ws_bytes,
                   void* stream);
+
+/* dspark_attend over a 4-bit cache: keys and values are what the codes stand for, exactly;
+ * dtype of q and out: DSPARK_BF16 (products of bf16 operands, weights rounded to bf16) or
+ * DSPARK_F32.  A block whose scale byte is 255 must not be seen.  Everything else as in dspark_attend. */
+int dspark_attend4(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
+                   const void* K, const void* V, int32_t N, int32_t heads, int32_t dtype,
+                   const void* q, const int32_t* offsets, float scale, int32_t max_chunk, void* out,
+                   void* ws, size_t ws_bytes, void* stream);
 
 /* Device-side check of the values the host cannot see, the preconditions
  * above (a debugging aid, off the hot path: one pass over every tensor given).

@@ -1,0 +1,376 @@
+"""dspark_cache_store and dspark_cache_read (PagedCache.append with a rotation, into 4 bits; read)
+against the plain model.
+
+Tolerances, u = 2^-24.  A rotated element a c - b s: c and s off by u/2 each relative (rounding) and
+2^-52 |angle| absolutely (the binary64 product), each product rounded (u/2), their sum too (u/2):
+|error| <= (|a| + |b|) (u + 2^-52 |angle|) + u/2 |result|, bounded below by 2 u (|a| + |b|) and the angle's
+term; stored as bf16 it is rounded once more (2^-8).  Copied elements, codes of elements that do not
+rotate and what read returns are exact."""
+import math
+
+import numpy as np
+import pytest
+
+import mx_model as M
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def C():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from draft_sampling_verification_w1_amd import cache, dspark
+    dspark.lib()
+    return cache
+
+
+def ints(x):
+    import torch
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def host(t):
+    return t.double().cpu().numpy()
+
+
+class Chunk:
+    """A cache whose slots hold pages for lens + chunks tokens, and a chunk of rows."""
+
+    def __init__(self, C, pool, rows, page, heads, kv, dim, lens, chunks, seed=0, layers=2, extra=3, pages=None):
+        import torch
+        self.C, self.pool, self.lens, self.chunks = C, pool, lens, chunks
+        self.page, self.heads, self.kv, self.dim = page, heads, kv, dim
+        self.dt = {"f32": torch.float32, "bf16": torch.bfloat16}[rows]
+        g = torch.Generator().manual_seed(seed)
+        S = len(lens)
+        need = [-(-(ln + c) // page) for ln, c in zip(lens, chunks)]
+        total = sum(need) + 5 if pages is None else pages
+        c = C.PagedCache(S, max(max(need), 1) + 1, total, page, layers, kv, dim,
+                         C.FOUR_BITS if pool == "4bit" else self.dt)
+        table = torch.full((S, c.max_pages), -1, dtype=torch.int32)
+        order = torch.randperm(total, generator=g)[:sum(need)] if pages is None else total - 1 - torch.arange(sum(need))
+        at = 0
+        for s in range(S):
+            table[s, :need[s]] = order[at:at + need[s]].to(torch.int32)
+            at += need[s]
+        c.table.copy_(table)
+        c.lens.copy_(ints(lens))
+        c.held.copy_(ints(need))
+        self.c, self.table, self.layer = c, table, layers - 1
+        self.off = [0] + np.cumsum(chunks).tolist()
+        self.offsets = ints(self.off)
+        self.N = max(1, self.off[-1] + extra)
+        rand = lambda h: (torch.randn((self.N, h, dim), generator=g) * 2 ** torch.randint(-3, 4, (self.N, 1, 1), generator=g)).to(self.dt)  # noqa: E731
+        self.q, self.k, self.v = rand(heads), rand(kv), rand(kv)
+        self.pos = np.concatenate([np.arange(ln, ln + n) for ln, n in zip(lens, chunks)]) if sum(chunks) else np.zeros(0)
+
+    def fill(self, byte=0xA5):
+        import torch
+        for t in (self.c.K, self.c.V):
+            t.view(torch.uint8).fill_(byte)
+
+    def stored(self, name):
+        """Rows of the chunk as the pages hold them: values [n, kv, dim], and scale bytes for 4 bits."""
+        import torch
+        pool = (self.c.K if name == "K" else self.c.V)[self.layer].cpu()
+        rows, scales, seen = [], [], {}
+        for s, (ln, n) in enumerate(zip(self.lens, self.chunks)):
+            for p in range(ln, ln + n):
+                page = int(self.table[s, p // self.page])
+                r = p % self.page
+                if self.pool == "4bit":
+                    if page not in seen:
+                        seen[page] = M.unpack(pool[page].numpy(), name, self.kv, self.page, self.dim)
+                    x, sc = seen[page]
+                    rows.append(x[r] * np.repeat(np.exp2(sc[r].astype(float) - 127), 32, -1))
+                    scales.append(sc[r])
+                else:
+                    e = pool.shape[-1]
+                    x = pool[page][:, :, r, :].reshape(self.kv, self.dim) if name == "K" else \
+                        pool[page][:, r // e, :, r % e]
+                    rows.append(x.double().numpy())
+        if not rows:
+            return np.zeros((0, self.kv, self.dim)), np.zeros((0, self.kv, self.dim // 32), np.uint8)
+        return np.stack(rows), np.stack(scales) if scales else None
+
+    def check_rotated(self, got, x, freqs, interleaved, out_eps):
+        """got [n, heads, d] against the rotation of x in binary64."""
+        n = self.off[-1]
+        x = host(x)[:n]
+        want = M.rotate(x, self.pos, freqs, interleaved, exact=True)
+        tol = self.slack(x, freqs, interleaved) + np.abs(want) * out_eps
+        assert got[:n].shape == want.shape and (np.abs(got[:n] - want) <= tol).all()
+
+    def slack(self, x, freqs, interleaved):
+        """Error bound of a rotated element before the last rounding."""
+        dim = 2 * len(freqs)
+        size = np.zeros_like(x)
+        a, b = (slice(0, dim, 2), slice(1, dim, 2)) if interleaved else (slice(0, dim // 2), slice(dim // 2, dim))
+        both = np.abs(x[..., a]) + np.abs(x[..., b])
+        angle = np.abs(self.pos[:, None] * np.asarray(freqs)[None])[:, None]
+        size[..., a] = size[..., b] = both * (2 * U + 2.0 ** -52 * angle)
+        return size
+
+    def check_codes(self, name, x, slack):
+        """Stored 4-bit values against x [n, kv, d] known to within slack."""
+        got, sc = self.stored(name)
+        low, high = np.abs(x) - slack, np.abs(x) + slack
+        b0, b1 = M.scale_bytes(np.maximum(low, 0)), M.scale_bytes(high)
+        assert ((sc == b0) | (sc == b1)).all()
+        signs = np.where(np.abs(x) > slack, np.sign(x), 0)
+        lo, hi = M.values(np.maximum(low, 0), sc), M.values(high, sc)
+        size = np.abs(got)
+        assert ((size >= lo) & (size <= hi)).all()
+        assert ((np.sign(got) == signs) | (got == 0) | (signs == 0)).all()
+
+
+LENS = [0, 1, 5, 7, 8, 15, 16, 30, 33, 100, 0, 250]
+CHUNKS = [1, 8, 9, 1, 17, 0, 3, 2, 40, 7, 0, 9]
+SHAPES = [(4, 4, 64), (6, 3, 64), (8, 2, 128), (5, 5, 128), (2, 1, 256)]
+
+
+@pytest.mark.parametrize("pool", ["own", "4bit"])
+@pytest.mark.parametrize("rows", ["f32", "bf16"])
+@pytest.mark.parametrize("page", [16, 32, 256])
+@pytest.mark.parametrize("heads,kv,dim", SHAPES)
+@pytest.mark.parametrize("rot,interleaved", [(1.0, False), (0.5, True), (16, False)])
+def test_store(C, pool, rows, page, heads, kv, dim, rot, interleaved):
+    import torch
+    dim_r = rot if rot == 16 else int(dim * rot)
+    b = Chunk(C, pool, rows, page, heads, kv, dim, LENS, CHUNKS, seed=page + dim)
+    b.fill()
+    freqs = C.rope_frequencies(dim_r, 1e4)
+    out = torch.full_like(b.q, 7.5, device="cuda")
+    got = b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets, rotation=C.Rotation(freqs, interleaved),
+                     q=b.q.cuda(), q_out=out)
+    assert got is out
+    n, f = b.off[-1], freqs.cpu().numpy()
+    eps = 2.0 ** -8 if rows == "bf16" else U
+    b.check_rotated(host(out), b.q, f, interleaved, eps)
+    assert (host(out)[n:] == 7.5).all()
+    if pool == "own":
+        b.check_rotated(b.stored("K")[0], b.k, f, interleaved, eps)
+        assert np.array_equal(b.stored("V")[0], host(b.v)[:n])
+    else:
+        x = host(b.k)[:n]
+        b.check_codes("K", M.rotate(x, b.pos, f, interleaved, exact=True), b.slack(x, f, interleaved))
+        b.check_codes("V", host(b.v)[:n], 0.0)
+    # bytes of other tokens, heads' padding and layers are left alone: what a second store over
+    # another filling leaves different is nobody's, and holds the filling
+    K, V = b.c.K.view(torch.uint8).clone(), b.c.V.view(torch.uint8).clone()
+    b.fill(0x5A)
+    b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets, rotation=C.Rotation(freqs, interleaved))
+    size = (2 * b.dt.itemsize * 8 if pool == "own" else 17) * n * kv * dim // (16 if pool == "own" else 32)
+    for old, new in ((K, b.c.K.view(torch.uint8)), (V, b.c.V.view(torch.uint8))):
+        other = old != new
+        assert (old[other] == 0xA5).all() and (new[other] == 0x5A).all()
+        assert int((~other).sum()) == size
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", ["f32", "bf16"])
+def test_store_without_rotation(C, rows, dim):
+    """4 bits without a rotation: codes exactly the model's; a cache of whole elements as append writes it."""
+    import torch
+    b = Chunk(C, "4bit", rows, 32, 2, 2, dim, LENS, CHUNKS)
+    b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets)
+    n = b.off[-1]
+    for name, x in (("K", b.k), ("V", b.v)):
+        got, sc = b.stored(name)
+        assert np.array_equal(sc, M.scale_bytes(host(x)[:n])) and np.array_equal(got, M.values(host(x)[:n]))
+    w = Chunk(C, "own", rows, 32, 2, 2, dim, LENS, CHUNKS)
+    w.fill()
+    lib = __import__("draft_sampling_verification_w1_amd.dspark", fromlist=["lib"])
+    k, v = w.k.cuda(), w.v.cuda()
+    w.c._call(lib.lib().dspark_cache_store, w.c._t, w.layer, w.c.K.data_ptr(), w.c.V.data_ptr(), w.N,
+              lib._DTYPES[w.dt], k.data_ptr(), v.data_ptr(), w.offsets.data_ptr(), None, 0, None, None)
+    K, V = w.c.K.clone(), w.c.V.clone()
+    w.fill()
+    w.c.append(w.layer, k, v, w.offsets)
+    assert torch.equal(K.view(torch.uint8), w.c.K.view(torch.uint8))
+    assert torch.equal(V.view(torch.uint8), w.c.V.view(torch.uint8))
+
+
+def test_far_positions(C):
+    """Angles of positions past 2^24, where binary32 holds no odd number."""
+    import torch
+    lens = [(1 << 24) + 1, (1 << 29) + 12345]
+    b = Chunk(C, "own", "f32", 256, 2, 1, 64, [0, 0], [0, 0], layers=1)
+    c = C.PagedCache(2, 10, 4, 256, 1, 1, 64, torch.float32)
+    c.lens.copy_(ints(lens))
+    q = torch.randn((6, 2, 64), device="cuda")
+    k = torch.randn((6, 1, 64), device="cuda")
+    freqs = C.rope_frequencies(64, 1e4)
+    # no page of these slots: keys and values go nowhere, queries are rotated
+    K = c.K.clone()
+    got = c.append(0, k, k.clone(), ints([0, 3, 6]), rotation=C.Rotation(freqs), q=q)
+    b.pos = np.concatenate([np.arange(ln, ln + 3) for ln in lens])
+    b.off = [0, 3, 6]
+    b.check_rotated(host(got), q, freqs.cpu().numpy(), False, U)
+    assert torch.equal(K, c.K)
+
+
+def test_q_in_place_and_extremes(C):
+    """Queries rotated in place; blocks of zeros, subnormal, huge and non-finite elements."""
+    import torch
+    b = Chunk(C, "4bit", "f32", 16, 4, 2, 128, [3, 20], [9, 2])
+    for i, x in enumerate([0.0, 1e-40, 1e-37, 3e38, 7.0, 7.0000005, 3.5, 5.0]):
+        b.v[i] = x
+        b.v[i, :, ::3] = -x / 2
+    b.v[8, 0, 40] = math.inf
+    b.v[8, 1, 100] = math.nan
+    q = b.q.cuda()
+    freqs = C.rope_frequencies(128)
+    apart = b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets, rotation=C.Rotation(freqs), q=q)
+    same = b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets, rotation=C.Rotation(freqs), q=q, q_out=q)
+    assert same is q and torch.equal(apart[:11], q[:11])
+    got, sc = b.stored("V")
+    want = host(b.v)[:11]
+    bad = np.zeros(sc.shape, bool)
+    bad[8, 0, 1] = bad[8, 1, 3] = True
+    assert (sc[bad] == 255).all()
+    fine = ~np.repeat(bad, 32, -1)
+    with np.errstate(invalid="ignore"):
+        want_sc = M.scale_bytes(want)
+        assert np.array_equal(sc, want_sc)
+        assert np.array_equal(got[fine], M.values(np.where(fine, want, 0), np.where(bad, 120, sc))[fine])
+    k, v = b.c.read(b.layer, b.offsets, N=b.N)
+    assert v.dtype == torch.bfloat16
+    back = host(v)[:11]
+    assert np.isnan(back[~fine]).all() and np.array_equal(back[fine], got[fine])
+
+
+@pytest.mark.parametrize("pool,rows", [("own", "f32"), ("own", "bf16"), ("4bit", "f32"), ("4bit", "bf16")])
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("heads,kv,dim", SHAPES)
+def test_read(C, pool, rows, page, heads, kv, dim):
+    import torch
+    b = Chunk(C, pool, rows, page, heads, kv, dim, LENS, CHUNKS, seed=3)
+    b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets)
+    n = b.off[-1]
+    k, v = (torch.full((b.N, kv, dim), 7.5, dtype=b.dt, device="cuda") for _ in range(2))
+    assert b.c.read(b.layer, b.offsets, out=(k, v))[0] is k
+    assert np.array_equal(host(k)[:n], b.stored("K")[0]) and np.array_equal(host(v)[:n], b.stored("V")[0])
+    assert (host(k)[n:] == 7.5).all() and (host(v)[n:] == 7.5).all()
+    # from positions of their own: inside a slot's chunk, across its end, before 0
+    first = [ln + 1 for ln in LENS]
+    first[2] = -1
+    n1 = [max(0, c - 1) for c in CHUNKS]
+    n1[4] += page * 20   # to behind the slot's pages
+    o1 = [0] + np.cumsum(n1).tolist()
+    k1, v1 = b.c.read(b.layer, ints(o1), first=ints(first), N=o1[-1], dtype=b.dt)
+    K, V = host(k), host(v)
+    for s in range(len(LENS)):
+        got_k, got_v = host(k1)[o1[s]:o1[s + 1]], host(v1)[o1[s]:o1[s + 1]]
+        if s == 2:
+            assert not got_k.any() and not got_v.any()
+            continue
+        a, m = b.off[s] + 1, max(0, CHUNKS[s] - 1)
+        assert np.array_equal(got_k[:m], K[a:a + m]) and np.array_equal(got_v[:m], V[a:a + m])
+        behind = -(-(LENS[s] + CHUNKS[s]) // page) * page - first[s]
+        assert not got_k[behind:].any() and not got_v[behind:].any()
+
+
+def test_absent_pages(C):
+    """Ids outside the pool and negative lengths: nothing is written, queries still turn, read gives 0."""
+    import torch
+    b = Chunk(C, "4bit", "bf16", 16, 2, 2, 64, [0, 14, 3], [20, 5, 2])
+    t = b.c.table.clone()
+    t[0, 1], t[1, 0], t[1, 1] = b.c.pages, -1, 2 ** 31 - 1
+    b.c.table.copy_(t)
+    b.c.lens.copy_(ints([0, 14, -5]))
+    b.fill(0x11)
+    q = b.q.cuda()
+    got = b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets, rotation=C.Rotation(C.rope_frequencies(64)), q=q)
+    b.pos = np.concatenate([np.arange(20), np.arange(14, 19), np.arange(2)])
+    b.check_rotated(host(got), b.q, C.rope_frequencies(64).cpu().numpy(), False, 2.0 ** -8)
+    touched = (b.c.K[b.layer] != 0x11).view(b.c.pages, -1).any(1)
+    assert touched.nonzero().flatten().tolist() == [int(b.table[0, 0])]
+    k, _ = b.c.read(b.layer, b.offsets, first=ints([0, 14, -5]), N=b.N)
+    assert host(k)[:16].any() and not host(k)[16:].any()
+
+
+def test_many_slots(C):
+    rng = np.random.default_rng(4096)
+    lens, chunks = rng.integers(0, 30, 4096).tolist(), rng.integers(0, 3, 4096).tolist()
+    b = Chunk(C, "4bit", "bf16", 16, 1, 1, 64, lens, chunks)
+    b.c.append(b.layer, b.k.cuda(), b.v.cuda(), b.offsets)
+    k, v = b.c.read(b.layer, b.offsets, N=b.N)
+    n = b.off[-1]
+    assert np.array_equal(host(k)[:n], M.values(host(b.k)[:n])) and np.array_equal(host(v)[:n], M.values(host(b.v)[:n]))
+
+
+def test_far_pages(C):
+    """Byte offsets past 2^32 in a 4-bit pool."""
+    import torch
+    free, _ = torch.cuda.mem_get_info()
+    pages = 2 ** 32 // (8 * 16 * 128 * 17 // 32) + 200
+    if free < 3 * pages * 8 * 16 * 128:
+        pytest.skip("not enough memory")
+    b = Chunk(C, "4bit", "bf16", 16, 8, 8, 128, [300, 41], [5, 1], layers=1, pages=pages)
+    b.c.append(0, b.k.cuda(), b.v.cuda(), b.offsets)
+    k, v = b.c.read(0, b.offsets, N=b.N)
+    assert np.array_equal(host(k)[:6], M.values(host(b.k)[:6])) and np.array_equal(host(v)[:6], M.values(host(b.v)[:6]))
+    assert np.array_equal(b.stored("K")[0], M.values(host(b.k)[:6]))
+
+
+@pytest.mark.parametrize("pool", ["own", "4bit"])
+def test_replayed_graph_and_streams(C, pool):
+    """append with a rotation and read inside a graph, replayed with other rows and lengths; another stream."""
+    import torch
+    b = Chunk(C, pool, "bf16", 16, 4, 2, 128, [30, 200, 4], [5, 1, 9])
+    c, q, k, v = b.c, b.q.cuda(), b.k.cuda(), b.v.cuda()
+    rot = C.Rotation(C.rope_frequencies(128))
+    q_out, out = torch.zeros_like(q), (torch.zeros_like(k), torch.zeros_like(v))
+    c.append(b.layer, k, v, b.offsets, rotation=rot, q=q, q_out=q_out)
+    c.read(b.layer, b.offsets, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.append(b.layer, k, v, b.offsets, rotation=rot, q=q, q_out=q_out)
+        c.read(b.layer, b.offsets, out=out)
+    side = torch.cuda.Stream()
+    for i in range(4):
+        for x in (q, k, v):
+            x.normal_()
+        c.lens.copy_(ints([30 - i, 200 - 3 * i, 4]))
+        g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (q_out, *out)]
+        with torch.cuda.stream(side):
+            e = c.append(b.layer, k, v, b.offsets, rotation=rot, q=q, q_out=torch.zeros_like(q))
+            r = c.read(b.layer, b.offsets, out=(torch.zeros_like(k), torch.zeros_like(v)))
+        side.synchronize()
+        for x, y in zip(got, (e, *r)):
+            assert torch.equal(x, y)
+
+
+def test_pages_move_with_their_scales(C):
+    """fork, copy on write and compaction of a 4-bit cache: the copies hold what the sources held."""
+    import torch
+    c = C.PagedCache(4, 6, 20, 16, 2, 2, 64, C.FOUR_BITS)
+    c.reserve(ints([20, 0, 40, 0]))
+    k, v = (torch.randn((60, 2, 64), device="cuda").bfloat16() for _ in range(2))
+    off = ints([0, 20, 20, 60, 60])
+    for layer in range(2):
+        c.append(layer, k * (layer + 1), v, off)
+    c.commit(ints([20, 0, 40, 0]))
+    assert c.fork(ints([0]), ints([1])).tolist() == [0]
+    out = c.reserve(ints([0, 2, 0, 0]))
+    assert int(out["cow_dst"][1]) >= 0
+    zero = ints([0, 0, 0, 0])
+    for layer in range(2):
+        a = c.read(layer, ints([0, 20, 40, 40, 40]), first=zero, N=40)
+        assert torch.equal(a[0][:20], a[0][20:]) and torch.equal(a[1][:20], a[1][20:])
+        want = M.values(host(k[:20] * (layer + 1)))
+        assert np.array_equal(host(a[0][:20]), want)
+    c.free(ints([0]))
+    before = [c.read(layer, ints([0, 0, 20, 60, 60]), first=zero, N=60) for layer in range(2)]
+    assert int(c.compact()["n_moves"]) > 0
+    for layer in range(2):
+        after = c.read(layer, ints([0, 0, 20, 60, 60]), first=zero, N=60)
+        assert torch.equal(after[0], before[layer][0]) and torch.equal(after[1], before[layer][1])
