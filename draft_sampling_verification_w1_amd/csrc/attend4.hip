@@ -3,8 +3,9 @@
 // The mathematics, the tiles' rows, the division of the work over spans and the join of cut
 // groups are those of attend.hip (attend_common.h); the pages' layout is that of
 // cache_store.hip.  What differs is how the operands come about:
-//   K: a lane's share of a key is D / 4 neighbouring elements, D / 8 bytes in memory; the queries are
-//     loaded in the same order, so that the product over the dimensions needs no exchange.
+//   K, bf16 queries: the codes and scales go into the scaled matrix product as they lie in memory,
+//     16 bytes (a block of 32 elements) per lane; the queries are two 8-bit operands (Queries).
+//   K, f32 queries: a lane's D / 4 neighbouring elements of a key, converted to binary32.
 //   V: a lane's 16 bytes are 8 keys x 4 elements.  A conversion takes two neighbouring
 //     elements of one key with that key's scale to two bf16 (exact: two significant bits);
 //     a byte permutation pairs the keys up as the matrix operand wants them.
@@ -30,10 +31,12 @@ __device__ __forceinline__ f32x2 pair_f32(uint32_t w, float s) {
   return __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, s, kSel);
 }
 
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
 // A lane's codes of one step as they lie in memory.
 template <int D>
-struct RawK {  // one 16-key block: D / 4 elements of a key
-  uint32_t w[D / 32];
+struct RawK {  // one 16-key block: blocks of 32 elements of a key (f32: D / 4 elements)
+  uint32_t w[D == 256 ? 8 : 4];
   uint32_t scale[D == 256 ? 2 : 1];
 };
 template <int D>
@@ -42,10 +45,88 @@ struct RawV {  // bf16: 8 keys, f32: 2 x 4 keys, of D / 16 elements
   uint32_t scale[2];
 };
 
+// A lane's share of a row of queries as matrix operands.
+template <typename E, int D>
+struct Queries;
+
+// f32: operand s: elements quad D / 4 + 4 s ..
+template <int D>
+struct Queries<float, D> {
+  f32x4 x[D / 16];
+  __device__ __forceinline__ void load(const float* p, bool live, int quad) {
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s)
+      x[s] = live ? *reinterpret_cast<const f32x4*>(p + quad * (D / 4) + 4 * s) : f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+};
+
+// bf16: the keys' codes are operands as they are, beside two 8-bit numbers per query element whose
+// sum it is: hi, its E4M3 rounding (4 significant bits) relative to a power of two that takes the
+// row's largest element to [128, 256), and lo, what is left, 16 times finer.  bf16 has 8
+// significant bits: the sum is exact for elements above 2^-13 of the row's largest, and off by at most
+// 2^-21 of that below.  The product with 4-bit codes and their scales is exact, sums are binary32.
+//   operand of 128 dimensions: lane group quad holds elements 16 quad .. + 15 and 64 + 16 quad .. + 15
+//   D = 64: hi and lo are the two halves of one operand, the keys' blocks are loaded twice.
+template <int D>
+constexpr int kQueryOps = D / 64;
+
+template <int D>
+struct Queries<uint16_t, D> {
+  i32x8 x[kQueryOps<D>];
+  uint32_t scale[D == 64 ? 1 : 2];  // bytes of hi and lo (of the lane group's half for 64 dimensions)
+  __device__ __forceinline__ void load(const uint16_t* p, bool live, int quad) {
+    u32x4 raw[D / 64][2];
+    uint32_t top = 0u;
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        raw[g][h] = live ? *reinterpret_cast<const u32x4*>(p + 64 * g + 16 * quad + 8 * h) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          top = max(top, max(raw[g][h][i] & 0x7FFFu, raw[g][h][i] >> 16 & 0x7FFFu));
+      }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
+    const uint32_t byte = max((int)(top >> 7) - 7, 5);
+    const float f = __uint_as_float((254u - byte) << 23);
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t w0 = raw[g][h][2 * i], w1 = raw[g][h][2 * i + 1];
+          const float a = bf16_lo(w0) * f, b = bf16_hi(w0) * f, c = bf16_lo(w1) * f, d = bf16_hi(w1) * f;
+          int hi = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+          hi = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, hi, true);
+          int lo = __builtin_amdgcn_cvt_pk_fp8_f32((a - __builtin_amdgcn_cvt_f32_fp8(hi, 0)) * 16.f,
+                                                   (b - __builtin_amdgcn_cvt_f32_fp8(hi, 1)) * 16.f, 0, false);
+          lo = __builtin_amdgcn_cvt_pk_fp8_f32((c - __builtin_amdgcn_cvt_f32_fp8(hi, 2)) * 16.f,
+                                               (d - __builtin_amdgcn_cvt_f32_fp8(hi, 3)) * 16.f, lo, true);
+          const int at = 2 * h + i;
+          if constexpr (D == 64) {
+            x[0][at] = hi;
+            x[0][4 + at] = lo;
+          } else {
+            x[g / 2 * 2][g % 2 * 4 + at] = hi;
+            x[g / 2 * 2 + 1][g % 2 * 4 + at] = lo;
+          }
+        }
+    if constexpr (D == 64) {
+      scale[0] = quad < 2 ? byte : byte - 4;
+    } else {
+      scale[0] = byte;
+      scale[1] = byte - 4;
+    }
+  }
+};
+
 // Key steps [first, end) of a group; `rec`: the record that takes the sums of a group
 // that is cut, or -1.  RW x KW waves: RW row groups of NQ 16-row blocks each, KW parts of the
-// key range.  kHalf: pages of 16 tokens, two of which a step spans.
-template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
+// key range.  kBuf: steps whose codes are on their way or in registers.  kHalf: pages of 16 tokens, two
+// of which a step spans.
+template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
 __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& it, int first,
                                               int end, int64_t rec, float* sh_ml, int* sh_limit,
                                               f32x4* sh_o) {
@@ -89,13 +170,13 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
   // halves' ids from them.  Ids outside the pool count as no page.
   const int shift = a.c.page_shift;
   const int32_t* table = a.c.t.table + (int64_t)it.slot * a.c.max_pages;
-  int col0 = (t0 * kKeys) >> shift;
+  int col0 = ((t0 * kKeys) >> shift) & ~1;
   auto columns = [&](int c0) {
     const int c = c0 + lane;
     const int p = c < a.c.max_pages ? table[c] : -1;
     return p >= 0 && p < a.c.pages ? p : -1;
   };
-  int ids = columns(col0);
+  int ids = columns(col0), ids_next = columns(col0 + 64);
   // without key parts nothing else ends a group for all waves, and one may still read its limits
   if constexpr (KW == 1) __syncthreads();
   for (int r = threadIdx.x; r < kRows; r += kThreads)
@@ -103,10 +184,10 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
   const int page = 1 << shift;
   auto pages_of = [&](int t, int& pa, int& pb) {
     const int ca = (t * kKeys) >> shift, cb = (t * kKeys + 16) >> shift;
-    if (cb >= col0 + 64) {
-      col0 = ca;
-      ids = columns(col0);
-      wait_loads();
+    if (ca >= col0 + 64) {  // a step's two columns lie in one window: both are even, or the same
+      col0 += 64;
+      ids = ids_next;
+      ids_next = columns(col0 + 64);
     }
     pa = __builtin_amdgcn_readlane(ids, ca - col0);
     pb = __builtin_amdgcn_readlane(ids, cb - col0);
@@ -125,15 +206,15 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       const uint8_t* blob = Kb + page_of(key, pa, pb);
       const uint8_t* codes = blob + code_head;
       const uint8_t* scales = blob + scale_head;
-      if constexpr (D == 64) {
+      if constexpr (kF32 && D == 64) {
         const u32x2 w = *reinterpret_cast<const u32x2*>(codes + ((quad >> 1) * page + row) * 16 + (quad & 1) * 8);
         k[u].w[0] = w.x;
         k[u].w[1] = w.y;
         k[u].scale[0] = scales[(quad >> 1) * page + row];
       } else {
 #pragma unroll
-        for (int b = 0; b < D / 128; ++b) {
-          const int block = quad * (D / 128) + b;
+        for (int b = 0; b < (D + 127) / 128; ++b) {
+          const int block = kF32 ? quad * (D / 128) + b : (D == 64 ? quad & 1 : 4 * b + quad);
           const u32x4 w = *reinterpret_cast<const u32x4*>(codes + (block * page + row) * 16);
 #pragma unroll
           for (int i = 0; i < 4; ++i) k[u].w[4 * b + i] = w[i];
@@ -187,112 +268,112 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       v.scale[u] = (v.scale[u] & mask) | (0x7F7F7F7Fu & ~mask);
     }
   };
-  // operands of a 16-key block: lane (n, quad), operand s: elements quad D / 4 + kE s ..
+  // f32: operands of a 16-key block: lane (n, quad), operand s: elements quad D / 4 + 4 s ..
   auto k_operands = [&](const RawK<D>& r, Chunk (&k)[kSteps]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      if constexpr (!kF32) {
-        const float f = scale_of(r.scale[D == 256 ? s / 4 : 0]);
-        const u32x4 w = {pair_bf16<0>(r.w[s], f), pair_bf16<1>(r.w[s], f), pair_bf16<2>(r.w[s], f), pair_bf16<3>(r.w[s], f)};
-        k[s] = __builtin_bit_cast(bf16x8, w);
-      } else {
-        const float f = scale_of(r.scale[D == 256 ? s / 8 : 0]);
-        const uint32_t w = r.w[s / 2];
-        const f32x2 x = s & 1 ? pair_f32<2>(w, f) : pair_f32<0>(w, f);
-        const f32x2 y = s & 1 ? pair_f32<3>(w, f) : pair_f32<1>(w, f);
-        k[s] = f32x4{x[0], x[1], y[0], y[1]};
+      const float f = scale_of(r.scale[D == 256 ? s / 8 : 0]);
+      const uint32_t w = r.w[s / 2];
+      const f32x2 x = s & 1 ? pair_f32<2>(w, f) : pair_f32<0>(w, f);
+      const f32x2 y = s & 1 ? pair_f32<3>(w, f) : pair_f32<1>(w, f);
+      if constexpr (kF32) k[s] = f32x4{x[0], x[1], y[0], y[1]};
+    }
+  };
+  // operands d and d + 1 (d = 4 g + 2 h): elements n D / 16 + d, .. + 1 of the lane's keys
+  auto v_operands = [&](const RawV<D>& r, const float (&s)[8], int g, int h, Chunk (&lo)[kVC], Chunk (&hi)[kVC]) {
+    const uint32_t x = r.w[g][2 * h], y = r.w[g][2 * h + 1];
+    if constexpr (!kF32) {
+      const uint32_t p[8] = {pair_bf16<0>(x, s[0]), pair_bf16<1>(x, s[1]), pair_bf16<2>(x, s[2]), pair_bf16<3>(x, s[3]),
+                             pair_bf16<0>(y, s[4]), pair_bf16<1>(y, s[5]), pair_bf16<2>(y, s[6]), pair_bf16<3>(y, s[7])};
+      u32x4 a, b;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x05040100u);
+        b[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x07060302u);
+      }
+      lo[0] = __builtin_bit_cast(Chunk, a);
+      hi[0] = __builtin_bit_cast(Chunk, b);
+    } else {
+      const f32x2 p[8] = {pair_f32<0>(x, s[0]), pair_f32<1>(x, s[1]), pair_f32<2>(x, s[2]), pair_f32<3>(x, s[3]),
+                          pair_f32<0>(y, s[4]), pair_f32<1>(y, s[5]), pair_f32<2>(y, s[6]), pair_f32<3>(y, s[7])};
+#pragma unroll
+      for (int u = 0; u < kVC; ++u) {
+        lo[u] = __builtin_bit_cast(Chunk, f32x4{p[4 * u][0], p[4 * u + 1][0], p[4 * u + 2][0], p[4 * u + 3][0]});
+        hi[u] = __builtin_bit_cast(Chunk, f32x4{p[4 * u][1], p[4 * u + 1][1], p[4 * u + 2][1], p[4 * u + 3][1]});
       }
     }
   };
-  // operand d: element n D / 16 + d of the lane's keys
-  auto v_operands = [&](const RawV<D>& r, Chunk (&v)[kVC][kDT]) {
-    float s[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t) s[t] = scale_of(r.scale[t >> 2] >> (8 * (t & 3)) & 255u);
-#pragma unroll
-    for (int g = 0; g < D / 64; ++g)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t x = r.w[g][2 * h], y = r.w[g][2 * h + 1];
-        const int d = 4 * g + 2 * h;
-        if constexpr (!kF32) {
-          const uint32_t p[8] = {pair_bf16<0>(x, s[0]), pair_bf16<1>(x, s[1]), pair_bf16<2>(x, s[2]), pair_bf16<3>(x, s[3]),
-                                 pair_bf16<0>(y, s[4]), pair_bf16<1>(y, s[5]), pair_bf16<2>(y, s[6]), pair_bf16<3>(y, s[7])};
-          u32x4 lo, hi;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            lo[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x05040100u);
-            hi[i] = __builtin_amdgcn_perm(p[2 * i + 1], p[2 * i], 0x07060302u);
-          }
-          v[0][d] = __builtin_bit_cast(bf16x8, lo);
-          v[0][d + 1] = __builtin_bit_cast(bf16x8, hi);
-        } else {
-          const f32x2 p[8] = {pair_f32<0>(x, s[0]), pair_f32<1>(x, s[1]), pair_f32<2>(x, s[2]), pair_f32<3>(x, s[3]),
-                              pair_f32<0>(y, s[4]), pair_f32<1>(y, s[5]), pair_f32<2>(y, s[6]), pair_f32<3>(y, s[7])};
-#pragma unroll
-          for (int u = 0; u < kVC; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-              v[u][d + e] = __builtin_bit_cast(Chunk, f32x4{p[4 * u][e], p[4 * u + 1][e], p[4 * u + 2][e], p[4 * u + 3][e]});
-        }
-      }
-  };
 
-  RawK<D> k[2];
-  RawV<D> v;
-  int pa = -1, pb = -1;
+  // Loads are started without a condition (behind the end the last step's again), so that
+  // the number on their way is known where one is waited for.
+  RawK<D> k[kBuf][2];
+  RawV<D> v[kBuf];
+  int pa[kBuf], pb[kBuf];
   if (t0 < t1) {
-    pages_of(t0, pa, pb);
-    load_k(t0, pa, pb, k);
-    load_v(t0, pa, pb, v);
+#pragma unroll
+    for (int j = 0; j < kBuf; ++j) {
+      const int t = min(t0 + j, t1 - 1);
+      pages_of(t, pa[j], pb[j]);
+      load_k(t, pa[j], pb[j], k[j]);
+      load_v(t, pa[j], pb[j], v[j]);
+    }
   }
   // queries as operands
-  Chunk qo[NQ][kSteps];
+  Queries<E, D> qo[NQ];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
     const int row = row0 + wrow + 16 * i + n;
     const bool live = row < rows;
     const int token = live ? row / G : 0;
-    const E* p = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D;
-#pragma unroll
-    for (int s = 0; s < kSteps; ++s)
-      qo[i][s] = live ? *reinterpret_cast<const Chunk*>(p + quad * (D / 4) + kE * s) : Op::zero();
+    qo[i].load(q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D, live, quad);
   }
   __syncthreads();  // the limits are there, and the last group's sums are out of LDS
   wait_loads();
-  for (int t = t0; t < t1; ++t) {
-    const int ma = pa, mb = pb;
+  for (int tb = t0; tb < t1; tb += kBuf) {
+#pragma unroll
+   for (int j = 0; j < kBuf; ++j) {
+    const int t = tb + j, ahead = min(t + kBuf, t1 - 1);
+    if (kBuf > 1 && t >= t1) break;
+    const int ma = pa[j], mb = pb[j];
     const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0;
     f32x4 s[NQ][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      Chunk ko[kSteps];
-      k_operands(k[u], ko);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if constexpr (kF32) {
+        Chunk ko[kSteps];
+        k_operands(k[j][u], ko);
 #pragma unroll
-      for (int c = 0; c < kSteps; ++c)
+        for (int c = 0; c < kSteps; ++c)
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) s[i][u] = Op::score(ko[c], qo[i][c], s[i][u]);
+          for (int i = 0; i < NQ; ++i) s[i][u] = Op::score(ko[c], qo[i].x[c], s[i][u]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < kQueryOps<D>; ++c) {
+          const int b = D == 256 ? c / 2 : 0;
+          const i32x8 ko = {(int)k[j][u].w[4 * b], (int)k[j][u].w[4 * b + 1], (int)k[j][u].w[4 * b + 2], (int)k[j][u].w[4 * b + 3], 0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < NQ; ++i)
+            s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                ko, qo[i].x[c], s[i][u], 4, 0, 0, (int)k[j][u].scale[b], 0, (int)qo[i].scale[D == 64 ? 0 : c & 1]);
+        }
+      }
     }
-    RawV<D> w = v;
-    if (t + 1 < t1) {
-      pages_of(t + 1, pa, pb);
-      load_k(t + 1, pa, pb, k);
-      load_v(t + 1, pa, pb, v);
-    }
+    pages_of(ahead, pa[j], pb[j]);
+    load_k(ahead, pa[j], pb[j], k[j]);
     if (partial) {
-      clear_v(t, ma, mb, w);
+      clear_v(t, ma, mb, v[j]);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         const int left = sh_limit[wrow + 16 * i + n] - t * kKeys;  // of this step's keys
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = Op::skey_of(u, j, quad);
+          for (int r = 0; r < 4; ++r) {
+            const int key = Op::skey_of(u, r, quad);
             const bool there = key < left && (key < 16 ? ma : mb) >= 0;
-            s[i][u][j] = there ? s[i][u][j] : -INFINITY;
+            s[i][u][r] = there ? s[i][u][r] : -INFINITY;
           }
       }
     }
@@ -327,31 +408,42 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       const bool far = m[i] > kNone && fabsf(m[i]) > kFar;
       float e[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = s[i][j >> 2][j & 3];
+      for (int r = 0; r < 8; ++r) {
+        const float x = s[i][r >> 2][r & 3];
         float y;
         {
 #pragma clang fp contract(off)
           y = x * a.scale_log2;
           y = y - m[i];
         }
-        e[j] = __builtin_amdgcn_exp2f(far ? y : fmaf(x, a.scale_log2, -m[i]));
+        e[r] = __builtin_amdgcn_exp2f(far ? y : fmaf(x, a.scale_log2, -m[i]));
       }
       l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (!kF32) p[i][0][j] = (__bf16)e[j];
-        else p[i][j >> 2][j & 3] = e[j];
+      for (int r = 0; r < 8; ++r) {
+        if constexpr (!kF32) p[i][0][r] = (__bf16)e[r];
+        else p[i][r >> 2][r & 3] = e[r];
       }
     }
-    Chunk vo[kVC][kDT];
-    v_operands(w, vo);
+    float vs[8];
 #pragma unroll
-    for (int u = 0; u < kVC; ++u)
+    for (int r = 0; r < 8; ++r) vs[r] = scale_of(v[j].scale[r >> 2] >> (8 * (r & 3)) & 255u);
 #pragma unroll
-      for (int d = 0; d < kDT; ++d)
+    for (int g = 0; g < D / 64; ++g)
 #pragma unroll
-        for (int i = 0; i < NQ; ++i) o[i][d] = Op::score(vo[u][d], p[i][u], o[i][d]);
+      for (int h = 0; h < 2; ++h) {
+        Chunk lo[kVC], hi[kVC];
+        v_operands(v[j], vs, g, h, lo, hi);
+#pragma unroll
+        for (int u = 0; u < kVC; ++u)
+#pragma unroll
+          for (int i = 0; i < NQ; ++i) {
+            o[i][4 * g + 2 * h] = Op::score(lo[u], p[i][u], o[i][4 * g + 2 * h]);
+            o[i][4 * g + 2 * h + 1] = Op::score(hi[u], p[i][u], o[i][4 * g + 2 * h + 1]);
+          }
+      }
+    load_v(ahead, pa[j], pb[j], v[j]);
+   }
   }
 
   // ---- the sums of the key parts joined: the other parts leave theirs in LDS in the
@@ -428,7 +520,7 @@ struct Shape4 {
   static constexpr int waves = (sizeof(E) == 2 && D <= 128) || RW * KW == 8 ? 2 : 1;
 };
 
-template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
+template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
 __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) void k_attend4(AttendArgs a) {
   constexpr int kRows = 16 * NQ * RW;
   __shared__ Plan plan;
@@ -465,29 +557,29 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
       cut.first = (int)rec;
       cut.last = (int)((g.start + g.units - 1) / plan.span);
     }
-    attend4_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_o);
+    attend4_steps<E, D, NQ, RW, KW, kBuf, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_o);
     x += end - first;
   }
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }
 
-template <typename E, int D, int NQ, int RW, int KW>
+template <typename E, int D, int NQ, int RW, int KW, int kBuf>
 void start4(const AttendArgs& a, hipStream_t stream) {
   const dim3 grid(a.grid), block(64 * RW * KW);
-  if (a.c.page_shift == 4) hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, false>), grid, block, 0, stream, a);
+  if (a.c.page_shift == 4) hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, kBuf, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, kBuf, false>), grid, block, 0, stream, a);
 }
 
-// Tiles in use: rows (16 NQ RW), NQ, RW, KW.
-#define ATTEND4_TILES(X) X(16, 1, 1, 4) X(32, 2, 1, 4) X(64, 2, 2, 2) X(96, 3, 2, 2) X(128, 2, 4, 2) \
-  X(192, 3, 4, 2) X(256, 2, 8, 1) X(384, 3, 8, 1)
-#define ATTEND4_TILES_256(X) X(16, 1, 1, 4) X(32, 1, 2, 2) X(64, 1, 4, 2) X(128, 1, 8, 1)
-#define ATTEND4_TILES_F32(X) X(16, 1, 1, 4) X(32, 1, 2, 2)
+// Tiles in use: rows (16 NQ RW), NQ, RW, KW, steps on their way.
+#define ATTEND4_TILES(X) X(16, 1, 1, 4, 2) X(32, 2, 1, 4, 1) X(64, 2, 2, 2, 1) X(96, 3, 2, 2, 1) \
+  X(128, 2, 4, 2, 1) X(192, 3, 4, 2, 1) X(256, 2, 8, 1, 1) X(384, 3, 8, 1, 1)
+#define ATTEND4_TILES_256(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1) X(64, 1, 4, 2, 1) X(128, 1, 8, 1, 1)
+#define ATTEND4_TILES_F32(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1)
 
 template <typename E, int D>
 bool start4_rows(int rows, const AttendArgs& a, hipStream_t stream) {
-#define ATTEND4_CASE(ROWS, NQ, RW, KW) \
-  case ROWS: start4<E, D, NQ, RW, KW>(a, stream); return true;
+#define ATTEND4_CASE(ROWS, NQ, RW, KW, BUF) \
+  case ROWS: start4<E, D, NQ, RW, KW, BUF>(a, stream); return true;
   if constexpr (sizeof(E) == 4) {
     switch (rows) { ATTEND4_TILES_F32(ATTEND4_CASE) }
   } else if constexpr (D == 256) {
@@ -510,7 +602,7 @@ int attend4_rows(bool bf16, int head_dim, int group, int max_chunk) {
   const int64_t rows = (int64_t)max_chunk * group;
   const int64_t tiles = (rows + most - 1) / most;
   const int need = (int)((rows + tiles - 1) / tiles);
-#define ATTEND4_SIZE(ROWS, NQ, RW, KW) \
+#define ATTEND4_SIZE(ROWS, NQ, RW, KW, BUF) \
   if (ROWS >= need) return ROWS;
   if (!bf16) {
     ATTEND4_TILES_F32(ATTEND4_SIZE)
