@@ -329,6 +329,59 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
   }
   __syncthreads();  // the limits are there, and the last group's sums are out of LDS
   wait_loads();
+  f32x4 s[NQ][2];
+  Chunk p[NQ][kVC];
+  float sums[NQ];
+  bool far = false;  // some row's maximum lies far from zero
+  // A step's weights p and their sums against the maxima as they are; true if a sum shows
+  // that some score lies far above its row's maximum.
+  auto weights_of = [&](auto exponent) {
+    bool risen = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      float e[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) e[r] = __builtin_amdgcn_exp2f(exponent(s[i][r >> 2][r & 3], m[i]));
+      sums[i] = ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+      risen |= sums[i] > kRiseSum;
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if constexpr (!kF32) p[i][0][r] = (__bf16)e[r];
+        else p[i][r >> 2][r & 3] = e[r];
+      }
+    }
+    return __ballot(risen) != 0;
+  };
+  auto weights = [&]() {
+    return weights_of([&](float x, float m) { return fmaf(x, a.scale_log2, -m); });
+  };
+  // The product rounded as the maximum's was, so that the largest weight is 1.
+  auto far_weights = [&]() {
+    weights_of([&](float x, float m) {
+#pragma clang fp contract(off)
+      const float y = x * a.scale_log2;
+      return y - m;
+    });
+  };
+  // The maxima brought up to a step's scores, and the sums so far scaled down.
+  auto follow = [&]() {
+    far = false;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const float mx = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
+                             fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3]))) * a.scale_log2;
+      float mn = fmaxf(m[i], mx);
+      mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
+      mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
+      const float f = __builtin_amdgcn_exp2f(m[i] - mn);
+      m[i] = mn;
+      far |= mn > kNone && fabsf(mn) > kFar;
+      l[i] *= f;
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) o[i][d] *= f;
+    }
+    far = __ballot(far) != 0;
+  };
   for (int tb = t0; tb < t1; tb += kBuf) {
 #pragma unroll
    for (int j = 0; j < kBuf; ++j) {
@@ -336,7 +389,6 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     if (kBuf > 1 && t >= t1) break;
     const int ma = pa[j], mb = pb[j];
     const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0;
-    f32x4 s[NQ][2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
 #pragma unroll
@@ -362,7 +414,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
     pages_of(ahead, pa[j], pb[j]);
     load_k(ahead, pa[j], pb[j], k[j]);
-    if (partial) {
+    if (__builtin_expect(partial, 0)) {
+      asm volatile("");  // a branch, not selections in every step
       clear_v(t, ma, mb, v[j]);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -377,54 +430,16 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
           }
       }
     }
-    // The maxima move at the first step, and when a score is far above all before it;
-    // otherwise they stay behind, and a step needs no rescaling.
-    float mx[NQ];
-    bool risen = false;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      mx[i] = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                    fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3]))) * a.scale_log2;
-      risen |= mx[i] > m[i] + kRise;
+    // The maxima move at the first step, and when a lane's weights show that a score is far
+    // above all before it; otherwise they stay behind (the sums are far from binary32's end), and
+    // a step needs neither a maximum over its scores nor a rescaling.
+    if (__builtin_expect(weights() | far, 0)) {
+      follow();
+      if (far) far_weights();
+      else weights();
     }
-    if (__ballot(risen) != 0) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        float mn = fmaxf(m[i], mx[i]);
-        mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
-        mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
-        const float f = __builtin_amdgcn_exp2f(m[i] - mn);
-        m[i] = mn;
-        l[i] *= f;
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) o[i][d] *= f;
-      }
-    }
-    Chunk p[NQ][kVC];
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-      // Far from zero the maximum is a product rounded by a whole or more: the weights
-      // then come from the product rounded as it was, so that the largest is 1.
-      const bool far = m[i] > kNone && fabsf(m[i]) > kFar;
-      float e[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const float x = s[i][r >> 2][r & 3];
-        float y;
-        {
-#pragma clang fp contract(off)
-          y = x * a.scale_log2;
-          y = y - m[i];
-        }
-        e[r] = __builtin_amdgcn_exp2f(far ? y : fmaf(x, a.scale_log2, -m[i]));
-      }
-      l[i] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        if constexpr (!kF32) p[i][0][r] = (__bf16)e[r];
-        else p[i][r >> 2][r & 3] = e[r];
-      }
-    }
+    for (int i = 0; i < NQ; ++i) l[i] += sums[i];
     float vs[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) vs[r] = scale_of(v[j].scale[r >> 2] >> (8 * (r & 3)) & 255u);
