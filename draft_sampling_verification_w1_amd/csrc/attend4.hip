@@ -37,7 +37,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 template <int D>
 struct RawK {  // one 16-key block: blocks of 32 elements of a key (f32: D / 4 elements)
   uint32_t w[D == 256 ? 8 : 4];
-  uint32_t scale[D == 256 ? 2 : 1];
+  uint32_t scale[D == 256 ? 2 : 1];  // of the key and its neighbours in an aligned four
 };
 template <int D>
 struct RawV {  // bf16: 8 keys, f32: 2 x 4 keys, of D / 16 elements
@@ -45,18 +45,19 @@ struct RawV {  // bf16: 8 keys, f32: 2 x 4 keys, of D / 16 elements
   uint32_t scale[2];
 };
 
-// A lane's share of a row of queries as matrix operands.
+// A lane's share of a row of queries as matrix operands, left in LDS in 16-byte pieces 64 lanes apart: all key
+// parts use them, and a wave has its registers for codes on their way and for the sums.
 template <typename E, int D>
 struct Queries;
 
-// f32: operand s: elements quad D / 4 + 4 s ..
+// f32: piece s: elements quad D / 4 + 4 s ..
 template <int D>
 struct Queries<float, D> {
-  f32x4 x[D / 16];
-  __device__ __forceinline__ void load(const float* p, bool live, int quad) {
+  static constexpr int kPieces = D / 16;
+  static __device__ __forceinline__ void put(const float* p, bool live, int quad, u32x4* to, uint32_t*) {
 #pragma unroll
-    for (int s = 0; s < D / 16; ++s)
-      x[s] = live ? *reinterpret_cast<const f32x4*>(p + quad * (D / 4) + 4 * s) : f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < kPieces; ++s)
+      to[64 * s] = live ? *reinterpret_cast<const u32x4*>(p + quad * (D / 4) + 4 * s) : u32x4{0u, 0u, 0u, 0u};
   }
 };
 
@@ -67,14 +68,15 @@ struct Queries<float, D> {
 // 2^-21 of that below.  The product with 4-bit codes and their scales is exact, sums are binary32.
 //   operand of 128 dimensions: lane group quad holds elements 16 quad .. + 15 and 64 + 16 quad .. + 15
 //   D = 64: hi and lo are the two halves of one operand, the keys' blocks are loaded twice.
+// Operand c: pieces 2 c and 2 c + 1; c even hi, odd lo (D = 64: piece 0 hi, 1 lo).  The scale bytes of hi and lo
+// are bytes 0 and 1 of a word (D = 64: byte 0 that of the lane group's half).
 template <int D>
 constexpr int kQueryOps = D / 64;
 
 template <int D>
 struct Queries<uint16_t, D> {
-  i32x8 x[kQueryOps<D>];
-  uint32_t scale[D == 64 ? 1 : 2];  // bytes of hi and lo (of the lane group's half for 64 dimensions)
-  __device__ __forceinline__ void load(const uint16_t* p, bool live, int quad) {
+  static constexpr int kPieces = 2 * kQueryOps<D>;
+  static __device__ __forceinline__ void put(const uint16_t* p, bool live, int quad, u32x4* to, uint32_t* scale) {
     u32x4 raw[D / 64][2];
     uint32_t top = 0u;
 #pragma unroll
@@ -91,7 +93,8 @@ struct Queries<uint16_t, D> {
     const uint32_t byte = max((int)(top >> 7) - 7, 5);
     const float f = __uint_as_float((254u - byte) << 23);
 #pragma unroll
-    for (int g = 0; g < D / 64; ++g)
+    for (int g = 0; g < D / 64; ++g) {
+      u32x4 his, los;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -104,23 +107,23 @@ struct Queries<uint16_t, D> {
                                                    (b - __builtin_amdgcn_cvt_f32_fp8(hi, 1)) * 16.f, 0, false);
           lo = __builtin_amdgcn_cvt_pk_fp8_f32((c - __builtin_amdgcn_cvt_f32_fp8(hi, 2)) * 16.f,
                                                (d - __builtin_amdgcn_cvt_f32_fp8(hi, 3)) * 16.f, lo, true);
-          const int at = 2 * h + i;
-          if constexpr (D == 64) {
-            x[0][at] = hi;
-            x[0][4 + at] = lo;
-          } else {
-            x[g / 2 * 2][g % 2 * 4 + at] = hi;
-            x[g / 2 * 2 + 1][g % 2 * 4 + at] = lo;
-          }
+          his[2 * h + i] = (uint32_t)hi;
+          los[2 * h + i] = (uint32_t)lo;
         }
-    if constexpr (D == 64) {
-      scale[0] = quad < 2 ? byte : byte - 4;
-    } else {
-      scale[0] = byte;
-      scale[1] = byte - 4;
+      to[64 * (D == 64 ? 0 : g / 2 * 4 + g % 2)] = his;
+      to[64 * (D == 64 ? 1 : g / 2 * 4 + 2 + g % 2)] = los;
     }
+    *scale = D == 64 ? (quad < 2 ? byte : byte - 4) : byte | (byte - 4) << 8;
   }
 };
+
+// LDS of a workgroup: the queries, then (at the same place) the outputs of all key parts but the first.
+template <typename E, int D, int NQ, int RW, int KW>
+__host__ __device__ constexpr int lds_pieces() {
+  const int queries = NQ * RW * Queries<E, D>::kPieces * 64;
+  const int join = (KW - 1) * 16 * NQ * RW * D / 4;
+  return queries > join ? queries : join;
+}
 
 // Key steps [first, end) of a group; `rec`: the record that takes the sums of a group
 // that is cut, or -1.  RW x KW waves: RW row groups of NQ 16-row blocks each, KW parts of the
@@ -129,7 +132,7 @@ struct Queries<uint16_t, D> {
 template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
 __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& it, int first,
                                               int end, int64_t rec, float* sh_ml, int* sh_limit,
-                                              f32x4* sh_o) {
+                                              uint32_t* sh_scale, u32x4* sh) {
   typedef Ops<E> Op;
   typedef typename Op::Chunk Chunk;
   constexpr bool kF32 = sizeof(E) == 4;
@@ -177,8 +180,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     return p >= 0 && p < a.c.pages ? p : -1;
   };
   int ids = columns(col0), ids_next = columns(col0 + 64);
-  // without key parts nothing else ends a group for all waves, and one may still read its limits
-  if constexpr (KW == 1) __syncthreads();
+  __syncthreads();  // the last group's limits, queries and sums are out of LDS
   for (int r = threadIdx.x; r < kRows; r += kThreads)
     sh_limit[r] = min(it.w.len + min((row0 + r) / G, it.w.chunk) + 1, it.w.keys);
   const int page = 1 << shift;
@@ -210,7 +212,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
         const u32x2 w = *reinterpret_cast<const u32x2*>(codes + ((quad >> 1) * page + row) * 16 + (quad & 1) * 8);
         k[u].w[0] = w.x;
         k[u].w[1] = w.y;
-        k[u].scale[0] = scales[(quad >> 1) * page + row];
+        k[u].scale[0] = *reinterpret_cast<const uint32_t*>(scales + (quad >> 1) * page + (row & ~3));
       } else {
 #pragma unroll
         for (int b = 0; b < (D + 127) / 128; ++b) {
@@ -218,7 +220,13 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
           const u32x4 w = *reinterpret_cast<const u32x4*>(codes + (block * page + row) * 16);
 #pragma unroll
           for (int i = 0; i < 4; ++i) k[u].w[4 * b + i] = w[i];
-          k[u].scale[b] = scales[block * page + row];
+          if constexpr (kF32) {
+            k[u].scale[b] = *reinterpret_cast<const uint32_t*>(scales + block * page + (row & ~3));
+          } else if (u == 0) {  // the lane's two keys are 4 apart, in the same 8
+            const u32x2 x = *reinterpret_cast<const u32x2*>(scales + block * page + (row & ~7));
+            k[0].scale[b] = x.x;
+            k[1].scale[b] = x.y;
+          }
         }
       }
     }
@@ -272,7 +280,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
   auto k_operands = [&](const RawK<D>& r, Chunk (&k)[kSteps]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
-      const float f = scale_of(r.scale[D == 256 ? s / 8 : 0]);
+      const float f = scale_of(r.scale[D == 256 ? s / 8 : 0] >> (8 * (n & 3)) & 255u);
       const uint32_t w = r.w[s / 2];
       const f32x2 x = s & 1 ? pair_f32<2>(w, f) : pair_f32<0>(w, f);
       const f32x2 y = s & 1 ? pair_f32<3>(w, f) : pair_f32<1>(w, f);
@@ -318,16 +326,22 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       load_v(t, pa[j], pb[j], v[j]);
     }
   }
-  // queries as operands
-  Queries<E, D> qo[NQ];
+  // queries as operands, each row block by one key part
+  typedef Queries<E, D> Query;
+  u32x4* const mine = sh + (wave % RW) * NQ * Query::kPieces * 64 + lane;
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
+    if (i % KW != part) continue;
     const int row = row0 + wrow + 16 * i + n;
     const bool live = row < rows;
     const int token = live ? row / G : 0;
-    qo[i].load(q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D, live, quad);
+    Query::put(q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D, live, quad,
+               mine + i * Query::kPieces * 64, &sh_scale[((wave % RW) * NQ + i) * 64 + lane]);
   }
-  __syncthreads();  // the limits are there, and the last group's sums are out of LDS
+  __syncthreads();
+  uint32_t q_scale[NQ];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) q_scale[i] = kF32 ? 0u : sh_scale[((wave % RW) * NQ + i) * 64 + lane];
   wait_loads();
   f32x4 s[NQ][2];
   Chunk p[NQ][kVC];
@@ -363,6 +377,17 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       return y - m;
     });
   };
+  // Accumulators stay where the matrix instructions have them outside the rare rescaling: the
+  // compiler would otherwise copy them to the other register file before every step's branch.
+  auto settle = [&]() {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i)
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) {
+        if constexpr (NQ > 3) asm volatile("" : "+a"(o[i][d]));
+        else asm volatile("" : "+v"(o[i][d]));
+      }
+  };
   // The maxima brought up to a step's scores, and the sums so far scaled down.
   auto follow = [&]() {
     far = false;
@@ -386,40 +411,54 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
    for (int j = 0; j < kBuf; ++j) {
     const int t = tb + j, ahead = min(t + kBuf, t1 - 1);
-    if (kBuf > 1 && t >= t1) break;
     const int ma = pa[j], mb = pb[j];
-    const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0;
+    // (behind the part's last step: no key at all)
+    const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0 || (kBuf > 1 && t >= t1);
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int i = 0; i < NQ; ++i)
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if constexpr (kF32) {
-        Chunk ko[kSteps];
-        k_operands(k[j][u], ko);
+      for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (kF32) {
+      Chunk ko[2][kSteps];
+      k_operands(k[j][0], ko[0]);
+      k_operands(k[j][1], ko[1]);
 #pragma unroll
-        for (int c = 0; c < kSteps; ++c)
+      for (int i = 0; i < NQ; ++i)
 #pragma unroll
-          for (int i = 0; i < NQ; ++i) s[i][u] = Op::score(ko[c], qo[i].x[c], s[i][u]);
-      } else {
+        for (int c = 0; c < kSteps; ++c) {
+          const Chunk x = __builtin_bit_cast(Chunk, mine[(i * Query::kPieces + c) * 64]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) s[i][u] = Op::score(ko[u][c], x, s[i][u]);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i)
 #pragma unroll
         for (int c = 0; c < kQueryOps<D>; ++c) {
           const int b = D == 256 ? c / 2 : 0;
-          const i32x8 ko = {(int)k[j][u].w[4 * b], (int)k[j][u].w[4 * b + 1], (int)k[j][u].w[4 * b + 2], (int)k[j][u].w[4 * b + 3], 0, 0, 0, 0};
+          const u32x4 x = mine[(i * Query::kPieces + 2 * c) * 64], y = mine[(i * Query::kPieces + 2 * c + 1) * 64];
+          const i32x8 qo = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
 #pragma unroll
-          for (int i = 0; i < NQ; ++i)
-            s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                ko, qo[i].x[c], s[i][u], 4, 0, 0, (int)k[j][u].scale[b], 0, (int)qo[i].scale[D == 64 ? 0 : c & 1]);
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t* w = k[j][u].w + 4 * b;
+            const i32x8 ko = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+            const int ks = (int)(k[j][u].scale[b] >> (8 * (n & 3)));  // its low byte counts
+            if (D != 64 && (c & 1))
+              s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 1, (int)q_scale[i]);
+            else
+              s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 0, (int)q_scale[i]);
+          }
         }
-      }
     }
     pages_of(ahead, pa[j], pb[j]);
     load_k(ahead, pa[j], pb[j], k[j]);
     if (__builtin_expect(partial, 0)) {
       asm volatile("");  // a branch, not selections in every step
-      clear_v(t, ma, mb, v[j]);
+      clear_v(t, kBuf > 1 && t >= t1 ? -1 : ma, kBuf > 1 && t >= t1 ? -1 : mb, v[j]);
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
-        const int left = sh_limit[wrow + 16 * i + n] - t * kKeys;  // of this step's keys
+        // of this step's keys
+        const int left = kBuf > 1 && t >= t1 ? 0 : sh_limit[wrow + 16 * i + n] - t * kKeys;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -434,7 +473,9 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     // above all before it; otherwise they stay behind (the sums are far from binary32's end), and
     // a step needs neither a maximum over its scores nor a rescaling.
     if (__builtin_expect(weights() | far, 0)) {
+      settle();
       follow();
+      settle();
       if (far) far_weights();
       else weights();
     }
@@ -468,7 +509,9 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     l[i] += __shfl_xor(l[i], 16, 64);
     l[i] += __shfl_xor(l[i], 32, 64);
   }
+  f32x4* const sh_o = reinterpret_cast<f32x4*>(sh);
   if constexpr (KW > 1) {
+    __syncthreads();  // all parts are done with the queries
     if (part > 0) {
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
@@ -532,7 +575,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 
 template <typename E, int D, int NQ, int RW, int KW>
 struct Shape4 {
-  static constexpr int waves = (sizeof(E) == 2 && D <= 128) || RW * KW == 8 ? 2 : 1;
+  static constexpr int waves = NQ > 3 ? 1 : ((sizeof(E) == 2 && D <= 128) || RW * KW == 8 ? 2 : 1);
 };
 
 template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
@@ -541,7 +584,8 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
   __shared__ Plan plan;
   __shared__ float sh_ml[KW * kRows * 2];
   __shared__ int sh_limit[kRows];
-  __shared__ f32x4 sh_o[KW > 1 ? (KW - 1) * kRows * D / 4 : 1];
+  __shared__ uint32_t sh_scale[NQ * RW * 64];
+  __shared__ u32x4 sh[lds_pieces<E, D, NQ, RW, KW>()];
   make_plan(a, kRows, plan);
   const int64_t total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
@@ -572,7 +616,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
       cut.first = (int)rec;
       cut.last = (int)((g.start + g.units - 1) / plan.span);
     }
-    attend4_steps<E, D, NQ, RW, KW, kBuf, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_o);
+    attend4_steps<E, D, NQ, RW, KW, kBuf, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_scale, sh);
     x += end - first;
   }
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
@@ -586,7 +630,7 @@ void start4(const AttendArgs& a, hipStream_t stream) {
 }
 
 // Tiles in use: rows (16 NQ RW), NQ, RW, KW, steps on their way.
-#define ATTEND4_TILES(X) X(16, 1, 1, 4, 2) X(32, 2, 1, 4, 1) X(64, 2, 2, 2, 1) X(96, 3, 2, 2, 1) \
+#define ATTEND4_TILES(X) X(16, 1, 1, 4, 2) X(32, 2, 1, 4, 1) X(48, 3, 1, 4, 2) X(64, 2, 2, 2, 2) X(96, 3, 2, 2, 2) \
   X(128, 2, 4, 2, 1) X(192, 3, 4, 2, 1) X(256, 2, 8, 1, 1) X(384, 3, 8, 1, 1)
 #define ATTEND4_TILES_256(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1) X(64, 1, 4, 2, 1) X(128, 1, 8, 1, 1)
 #define ATTEND4_TILES_F32(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1)
