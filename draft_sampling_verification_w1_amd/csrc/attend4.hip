@@ -194,36 +194,47 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     pa = __builtin_amdgcn_readlane(ids, ca - col0);
     pb = __builtin_amdgcn_readlane(ids, cb - col0);
   };
+  // Operand addresses: a wave-uniform base (page, step within the page) and a lane's 32-bit
+  // offset that stays the same through the pass.  Pages of 16: the lane's page, no step within.
   const int64_t page_bytes = a.c.page_bytes;
-  const int code_head = it.head * page * (D / 2);
-  const int scale_head = H * page * (D / 2) + it.head * page * (D / 32);
-  const uint8_t* Kb = static_cast<const uint8_t*>(a.K);
-  const uint8_t* Vb = static_cast<const uint8_t*>(a.V);
-  // the page that holds a step's key, and the key's place in it
-  auto page_of = [&](int key, int pa, int pb) { return (int64_t)max(key < 16 ? pa : pb, 0) * page_bytes; };
+  const uint8_t* Kb = static_cast<const uint8_t*>(a.K) + it.head * page * (D / 2);
+  const uint8_t* Vb = static_cast<const uint8_t*>(a.V) + it.head * page * (D / 2);
+  // from a page's codes of this head to its scales
+  const uint32_t to_scales = (uint32_t)(H * page * (D / 2) - it.head * page * (D / 2) + it.head * page * (D / 32));
+  const int k_key = Op::key_of(0, n) & (page - 1);
+  const int k_block = kF32 ? quad * D / 128 : (D == 64 ? quad & 1 : quad);  // the first, others 4 on (f32: 1 on)
+  const uint32_t k_lane = (uint32_t)((k_block * page + k_key) * 16 + (kF32 && D == 64 ? (quad & 1) * 8 : 0));
+  const uint32_t ks_lane = to_scales + (uint32_t)(k_block * page + (k_key & (kF32 ? ~3 : ~7)));
+  const int v_key = (kF32 ? 4 * quad : 8 * quad) & (page - 1);
+  const uint32_t v_lane = (uint32_t)((v_key >> 3) * (D / 64 * 256) + n * 16 + (v_key & 4));
+  const uint32_t vs_lane = to_scales + (uint32_t)((n * D / 512) * page + v_key);
+  // the page of a lane's keys; f32 has 16 keys of a step on each of two pages for all lanes
+  auto page_at = [&](const uint8_t* pool, int pa, int pb, bool second) {
+    if constexpr (kHalf) return pool + (int64_t)max(second ? pb : pa, 0) * page_bytes;
+    else return pool + (int64_t)max(pa, 0) * page_bytes;
+  };
   auto load_k = [&](int t, int pa, int pb, RawK<D> (&k)[2]) {
+    const int at = kHalf ? 0 : (t * kKeys) & (page - 1);
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      const int key = Op::key_of(u, n), row = (t * kKeys + key) & (page - 1);
-      const uint8_t* blob = Kb + page_of(key, pa, pb);
-      const uint8_t* codes = blob + code_head;
-      const uint8_t* scales = blob + scale_head;
+      const uint8_t* base = page_at(Kb, pa, pb, kF32 ? u == 1 : n >= 8);
+      const int row = at + (kF32 ? (kHalf ? 0 : 16 * u) : 4 * u);
       if constexpr (kF32 && D == 64) {
-        const u32x2 w = *reinterpret_cast<const u32x2*>(codes + ((quad >> 1) * page + row) * 16 + (quad & 1) * 8);
+        const u32x2 w = *reinterpret_cast<const u32x2*>(base + row * 16 + k_lane);
         k[u].w[0] = w.x;
         k[u].w[1] = w.y;
-        k[u].scale[0] = *reinterpret_cast<const uint32_t*>(scales + (quad >> 1) * page + (row & ~3));
+        k[u].scale[0] = *reinterpret_cast<const uint32_t*>(base + row + ks_lane);
       } else {
 #pragma unroll
         for (int b = 0; b < (D + 127) / 128; ++b) {
-          const int block = kF32 ? quad * (D / 128) + b : (D == 64 ? quad & 1 : 4 * b + quad);
-          const u32x4 w = *reinterpret_cast<const u32x4*>(codes + (block * page + row) * 16);
+          const int block = kF32 ? b : 4 * b;
+          const u32x4 w = *reinterpret_cast<const u32x4*>(base + (row + block * page) * 16 + k_lane);
 #pragma unroll
           for (int i = 0; i < 4; ++i) k[u].w[4 * b + i] = w[i];
           if constexpr (kF32) {
-            k[u].scale[b] = *reinterpret_cast<const uint32_t*>(scales + block * page + (row & ~3));
+            k[u].scale[b] = *reinterpret_cast<const uint32_t*>(base + row + block * page + ks_lane);
           } else if (u == 0) {  // the lane's two keys are 4 apart, in the same 8
-            const u32x2 x = *reinterpret_cast<const u32x2*>(scales + block * page + (row & ~7));
+            const u32x2 x = *reinterpret_cast<const u32x2*>(base + row + block * page + ks_lane);
             k[0].scale[b] = x.x;
             k[1].scale[b] = x.y;
           }
@@ -232,32 +243,30 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
   };
   auto load_v = [&](int t, int pa, int pb, RawV<D>& v) {
-    const int block = n * D / 512;
+    const int at = kHalf ? 0 : (t * kKeys) & (page - 1);
     if constexpr (!kF32) {
-      const int key = 8 * quad, row = (t * kKeys + key) & (page - 1);
-      const uint8_t* blob = Vb + page_of(key, pa, pb);
-      const uint8_t* codes = blob + code_head + (row >> 3) * (D / 64 * 256) + n * 16;
+      const uint8_t* base = page_at(Vb, pa, pb, quad >= 2);
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
-        const u32x4 w = *reinterpret_cast<const u32x4*>(codes + g * 256);
+        const u32x4 w = *reinterpret_cast<const u32x4*>(base + (at >> 3) * (D / 64 * 256) + g * 256 + v_lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v.w[g][i] = w[i];
       }
-      const u32x2 s = *reinterpret_cast<const u32x2*>(blob + scale_head + block * page + row);
+      const u32x2 s = *reinterpret_cast<const u32x2*>(base + at + vs_lane);
       v.scale[0] = s.x;
       v.scale[1] = s.y;
     } else {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        const int key = 16 * u + 4 * quad, row = (t * kKeys + key) & (page - 1);
-        const uint8_t* blob = Vb + page_of(key, pa, pb);
-        const uint8_t* codes = blob + code_head + (row >> 3) * (D / 64 * 256) + n * 16 + (row & 4);
+        const uint8_t* base = page_at(Vb, pa, pb, u == 1);
+        const int row = at + (kHalf ? 0 : 16 * u);
 #pragma unroll
         for (int g = 0; g < D / 64; ++g)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            v.w[g][2 * h + u] = *reinterpret_cast<const uint32_t*>(codes + g * 256 + h * 8);
-        v.scale[u] = *reinterpret_cast<const uint32_t*>(blob + scale_head + block * page + row);
+            v.w[g][2 * h + u] =
+                *reinterpret_cast<const uint32_t*>(base + (row >> 3) * (D / 64 * 256) + g * 256 + h * 8 + v_lane);
+        v.scale[u] = *reinterpret_cast<const uint32_t*>(base + row + vs_lane);
       }
     }
   };
