@@ -549,7 +549,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape<E, D, NQ, RW, KW>::waves)) voi
   g.slot_end = 0;
   AttendCut cut = {};
   for (int64_t x = x0; x < x1;) {
-    find_group(a, kRows, plan, x, g);
+    find_group(a, kRows, plan, x, g, [&](int s) { return slot_work(a, s, kRows); });
     if (g.units == 0) {
       x = g.next;
       continue;

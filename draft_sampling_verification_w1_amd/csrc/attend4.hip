@@ -54,10 +54,15 @@ struct Queries;
 template <int D>
 struct Queries<float, D> {
   static constexpr int kPieces = D / 16;
-  static __device__ __forceinline__ void put(const float* p, bool live, int quad, u32x4* to, uint32_t*) {
+  u32x4 raw[kPieces];
+  __device__ __forceinline__ void load(const float* p, bool live, int quad) {
 #pragma unroll
     for (int s = 0; s < kPieces; ++s)
-      to[64 * s] = live ? *reinterpret_cast<const u32x4*>(p + quad * (D / 4) + 4 * s) : u32x4{0u, 0u, 0u, 0u};
+      raw[s] = live ? *reinterpret_cast<const u32x4*>(p + quad * (D / 4) + 4 * s) : u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void put(int, u32x4* to, uint32_t*) const {
+#pragma unroll
+    for (int s = 0; s < kPieces; ++s) to[64 * s] = raw[s];
   }
 };
 
@@ -76,18 +81,23 @@ constexpr int kQueryOps = D / 64;
 template <int D>
 struct Queries<uint16_t, D> {
   static constexpr int kPieces = 2 * kQueryOps<D>;
-  static __device__ __forceinline__ void put(const uint16_t* p, bool live, int quad, u32x4* to, uint32_t* scale) {
-    u32x4 raw[D / 64][2];
+  u32x4 raw[D / 64][2];
+  __device__ __forceinline__ void load(const uint16_t* p, bool live, int quad) {
+#pragma unroll
+    for (int g = 0; g < D / 64; ++g)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        raw[g][h] = live ? *reinterpret_cast<const u32x4*>(p + 64 * g + 16 * quad + 8 * h) : u32x4{0u, 0u, 0u, 0u};
+  }
+  __device__ __forceinline__ void put(int quad, u32x4* to, uint32_t* scale) const {
     uint32_t top = 0u;
 #pragma unroll
     for (int g = 0; g < D / 64; ++g)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        raw[g][h] = live ? *reinterpret_cast<const u32x4*>(p + 64 * g + 16 * quad + 8 * h) : u32x4{0u, 0u, 0u, 0u};
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           top = max(top, max(raw[g][h][i] & 0x7FFFu, raw[g][h][i] >> 16 & 0x7FFFu));
-      }
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     const uint32_t byte = max((int)(top >> 7) - 7, 5);
@@ -180,6 +190,18 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     return p >= 0 && p < a.c.pages ? p : -1;
   };
   int ids = columns(col0), ids_next = columns(col0 + 64);
+  // queries as operands, each row block by one key part; on their way beside the page ids
+  typedef Queries<E, D> Query;
+  constexpr int kMine = (NQ + KW - 1) / KW;
+  u32x4* const mine = sh + (wave % RW) * NQ * Query::kPieces * 64 + lane;
+  Query rows_of[kMine];
+#pragma unroll
+  for (int x = 0; x < kMine; ++x) {
+    const int i = x * KW + part, row = row0 + wrow + 16 * i + n;
+    const bool live = i < NQ && row < rows;
+    const int token = live ? row / G : 0;
+    rows_of[x].load(q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D, live, quad);
+  }
   __syncthreads();  // the last group's limits, queries and sums are out of LDS
   for (int r = threadIdx.x; r < kRows; r += kThreads)
     sh_limit[r] = min(it.w.len + min((row0 + r) / G, it.w.chunk) + 1, it.w.keys);
@@ -335,18 +357,10 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       load_v(t, pa[j], pb[j], v[j]);
     }
   }
-  // queries as operands, each row block by one key part
-  typedef Queries<E, D> Query;
-  u32x4* const mine = sh + (wave % RW) * NQ * Query::kPieces * 64 + lane;
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) {
-    if (i % KW != part) continue;
-    const int row = row0 + wrow + 16 * i + n;
-    const bool live = row < rows;
-    const int token = live ? row / G : 0;
-    Query::put(q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D, live, quad,
-               mine + i * Query::kPieces * 64, &sh_scale[((wave % RW) * NQ + i) * 64 + lane]);
-  }
+  for (int x = 0; x < kMine; ++x)
+    if (x * KW + part < NQ)
+      rows_of[x].put(quad, mine + (x * KW + part) * Query::kPieces * 64, &sh_scale[((wave % RW) * NQ + x * KW + part) * 64 + lane]);
   __syncthreads();
   uint32_t q_scale[NQ];
 #pragma unroll
@@ -518,37 +532,41 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     l[i] += __shfl_xor(l[i], 16, 64);
     l[i] += __shfl_xor(l[i], 32, 64);
   }
+  // Row block i belongs to part i % KW, which adds what the others have of it.
   f32x4* const sh_o = reinterpret_cast<f32x4*>(sh);
+  // place of part w's piece of block i, left out where it is the owner's own
+  auto piece = [&](int w, int i, int d) {
+    const int rank = w < i % KW ? w : w - 1;
+    return ((((wave % RW) * NQ + i) * (KW - 1) + rank) * kDT + d) * 64 + lane;
+  };
   if constexpr (KW > 1) {
     __syncthreads();  // all parts are done with the queries
-    if (part > 0) {
 #pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        if (quad == 0) {
-          sh_ml[(part * kRows + wrow + 16 * i + n) * 2] = m[i];
-          sh_ml[(part * kRows + wrow + 16 * i + n) * 2 + 1] = l[i];
-        }
-#pragma unroll
-        for (int d = 0; d < kDT; ++d) sh_o[(((wave - RW) * NQ + i) * kDT + d) * 64 + lane] = o[i][d];
+    for (int i = 0; i < NQ; ++i) {
+      if (quad == 0) {
+        sh_ml[(part * kRows + wrow + 16 * i + n) * 2] = m[i];
+        sh_ml[(part * kRows + wrow + 16 * i + n) * 2 + 1] = l[i];
       }
+      if (i % KW == part) continue;
+#pragma unroll
+      for (int d = 0; d < kDT; ++d) sh_o[piece(part, i, d)] = o[i][d];
     }
     __syncthreads();
-    if (part > 0) return;
   }
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
+    if (i % KW != part) continue;
     float f[KW], mn = m[i];
 #pragma unroll
-    for (int w = 1; w < KW; ++w) {
-      f[w] = sh_ml[(w * kRows + wrow + 16 * i + n) * 2];
+    for (int w = 0; w < KW; ++w) {
+      f[w] = KW > 1 ? sh_ml[(w * kRows + wrow + 16 * i + n) * 2] : m[i];
       mn = fmaxf(mn, f[w]);
     }
-    f[0] = __builtin_amdgcn_exp2f(m[i] - mn);
-    float ls = l[i] * f[0];
+    float ls = 0.f;
 #pragma unroll
-    for (int w = 1; w < KW; ++w) {
+    for (int w = 0; w < KW; ++w) {
       f[w] = __builtin_amdgcn_exp2f(f[w] - mn);
-      ls += sh_ml[(w * kRows + wrow + 16 * i + n) * 2 + 1] * f[w];
+      ls += (KW > 1 ? sh_ml[(w * kRows + wrow + 16 * i + n) * 2 + 1] : l[i]) * f[w];
     }
     const int r = wrow + 16 * i + n, row = row0 + r;
     if (row >= rows) continue;
@@ -561,10 +579,10 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     f32x4 sum[kDT];
 #pragma unroll
     for (int d = 0; d < kDT; ++d) {
-      sum[d] = o[i][d] * f[0];
+      sum[d] = o[i][d] * f[i % KW];
 #pragma unroll
-      for (int w = 1; w < KW; ++w)
-        sum[d] += sh_o[(((w - 1) * RW + wave) * NQ * kDT + i * kDT + d) * 64 + lane] * f[w];
+      for (int w = 0; w < KW; ++w)
+        if (w != i % KW) sum[d] += sh_o[piece(w, i, d)] * f[w];
       sum[d] *= norm;
     }
 #pragma unroll
@@ -595,6 +613,14 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
   __shared__ int sh_limit[kRows];
   __shared__ uint32_t sh_scale[NQ * RW * 64];
   __shared__ u32x4 sh[lds_pieces<E, D, NQ, RW, KW>()];
+  // what the plan's threads read of the slots, for the groups' places
+  __shared__ int near_slots[kPlanThreads][3];
+  const bool near = a.c.slots <= kPlanThreads;
+  for (int s = threadIdx.x; near && s < a.c.slots; s += 64 * RW * KW) {
+    near_slots[s][0] = min(max(a.offsets[s], 0), a.N);
+    near_slots[s][1] = min(max(a.offsets[s + 1], near_slots[s][0]), a.N);
+    near_slots[s][2] = a.c.t.lens[s];
+  }
   make_plan(a, kRows, plan);
   const int64_t total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
@@ -608,13 +634,20 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
   g.slot_end = 0;
   AttendCut cut = {};
   for (int64_t x = x0; x < x1;) {
-    find_group(a, kRows, plan, x, g);
+    find_group(a, kRows, plan, x, g, [&](int s) {
+      if (!near) return slot_work(a, s, kRows);
+      return plan_slot(__builtin_amdgcn_readfirstlane(near_slots[s][0]), __builtin_amdgcn_readfirstlane(near_slots[s][1]),
+                       __builtin_amdgcn_readfirstlane(near_slots[s][2]), (int64_t)a.c.max_pages << a.c.page_shift,
+                       a.group, kRows, a.c.kv_heads, a.extra);
+    });
     if (g.units == 0) {
       x = g.next;
       continue;
     }
-    const int first = (int)(x - g.start);
-    const int end = (int)min((int64_t)g.units, first + (x1 - x));
+    // a span may start, or end, in front of the group's first step
+    const int first = (int)max(x - g.start, (int64_t)0);
+    const int end = (int)min((int64_t)g.units, x1 - g.start);
+    if (end <= first) break;
     // a cut group's record: a span has two at most, of its first and of its last group
     const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
     if (first == 0 && end < g.units) {  // it goes on in the next span
@@ -626,7 +659,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
       cut.last = (int)((g.start + g.units - 1) / plan.span);
     }
     attend4_steps<E, D, NQ, RW, KW, kBuf, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_scale, sh);
-    x += end - first;
+    x = g.start + end;
   }
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }
@@ -681,6 +714,12 @@ int attend4_rows(bool bf16, int head_dim, int group, int max_chunk) {
   }
 #undef ATTEND4_SIZE
   return most;
+}
+
+// What a group costs beside its steps, in steps, where spans hold several groups (a span that
+// holds part of one group pays it whatever its steps are).
+int attend4_extra(int groups, int grid) {
+  return groups >= 2 * grid ? 20 : 0;
 }
 
 // Workgroups, and spans at most: what is resident at once.

@@ -91,7 +91,7 @@ __device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int ro
   const int o0 = min(max(a.offsets[s], 0), a.N);
   const int o1 = min(max(a.offsets[s + 1], o0), a.N);
   return plan_slot(o0, o1, a.c.t.lens[s], (int64_t)a.c.max_pages << a.c.page_shift, a.group, rows,
-                   a.c.kv_heads);
+                   a.c.kv_heads, a.extra);
 }
 
 // Units before each plan thread's run of slots (thread t: slots [t per, t per + per)).
@@ -103,27 +103,39 @@ struct Plan {
   int per;
 };
 
-// At least kPlanThreads threads.
+// kThreads: of the workgroup, a multiple of 64; each takes kRuns neighbouring runs of slots.
+template <int kThreads = kPlanThreads>
 __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& plan) {
+  constexpr int kRuns = kThreads < kPlanThreads ? kPlanThreads / kThreads : 1;
+  constexpr int kWaves = (kThreads < kPlanThreads ? kThreads : kPlanThreads) / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.c.slots + kPlanThreads - 1) / kPlanThreads;
-  const int s0 = tid < kPlanThreads ? tid * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
-  int64_t x = 0;
-  for (int s = s0; s < s1; ++s) x += slot_work(a, s, rows).units;
+  int64_t run[kRuns], x = 0;
+#pragma unroll
+  for (int r = 0; r < kRuns; ++r) {
+    const int t = tid * kRuns + r;
+    const int s0 = t < kPlanThreads ? t * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
+    for (int s = s0; s < s1; ++s) x += slot_work(a, s, rows).units;
+    run[r] = x;
+  }
+  const int64_t mine = x;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int64_t y = __shfl_up(x, off, 64);
     if (lane >= off) x += y;
   }
-  if (lane == 63 && wave < kPlanWaves) plan.sum[wave] = x;
+  if (lane == 63 && wave < kWaves) plan.sum[wave] = x;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kPlanWaves; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < wave) x += plan.sum[w];
     total += plan.sum[w];
   }
-  if (tid < kPlanThreads) plan.before[tid + 1] = x;
+  if (tid * kRuns < kPlanThreads) {
+#pragma unroll
+    for (int r = 0; r < kRuns; ++r) plan.before[tid * kRuns + r + 1] = x - mine + run[r];
+  }
   if (tid == 0) {
     const int64_t span = plan_span(total, a.grid);
     plan.before[0] = 0;
@@ -144,9 +156,11 @@ struct Group {
   int64_t slot_start, slot_end;
 };
 
-// `g` may hold the group before it: a slot is looked up when the line leaves it.
+// `g` may hold the group before it: a slot is looked up when the line leaves it.  work_of(s):
+// the slot's work.
+template <typename F>
 __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const Plan& plan,
-                                           int64_t x, Group& g) {
+                                           int64_t x, Group& g, F work_of) {
   if (x >= g.slot_end) {
     int lo = 0, hi = kPlanThreads - 1;
     while (lo < hi) {
@@ -158,7 +172,7 @@ __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const 
     int s = lo * plan.per;
     const int end = min(s + plan.per, a.c.slots);
     for (;; ++s) {
-      g.w = slot_work(a, s, rows);
+      g.w = work_of(s);
       if (x < start + g.w.units || s + 1 >= end) break;
       start += g.w.units;
     }
@@ -166,7 +180,7 @@ __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const 
     g.slot_start = start;
     g.slot_end = start + g.w.units;
   }
-  const PlanPlace at = plan_place(g.w, a.group, rows, x - g.slot_start);
+  const PlanPlace at = plan_place(g.w, a.group, rows, x - g.slot_start, a.extra);
   g.head = at.head;
   g.tile = at.tile;
   g.units = at.units;

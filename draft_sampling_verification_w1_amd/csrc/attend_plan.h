@@ -41,8 +41,9 @@ PLAN_FN int tile_units(const SlotWork& w, int group, int rows, int i) {
 
 // A slot's work.  o0, o1: its token rows, 0 <= o0 <= o1; cached: tokens before them;
 // width: positions of the table's row; group: query heads per kv head; rows of a tile.
+// extra: what a group takes on the line in front of its first step.
 PLAN_FN SlotWork plan_slot(int o0, int o1, int cached, int64_t width, int group, int rows,
-                           int kv_heads) {
+                           int kv_heads, int extra = 0) {
   SlotWork w;
   w.o0 = o0;
   w.chunk = o1 - o0;
@@ -68,7 +69,7 @@ PLAN_FN SlotWork plan_slot(int o0, int o1, int cached, int64_t width, int group,
       const int64_t most = 2 * (int64_t)w.keys;
       w.pair_units = (int)(((both < most ? both : most) + 2 * (kKeys - 1)) / kKeys);
     }
-    w.pair_units = plan_max(w.pair_units, kMinSpan);
+    w.pair_units = plan_max(w.pair_units, kMinSpan) + (w.tiles > 1 ? 2 : 1) * extra;
     w.units = (int64_t)w.pair_units * w.pairs * kv_heads;
   }
   return w;
@@ -78,13 +79,14 @@ PLAN_FN SlotWork plan_slot(int o0, int o1, int cached, int64_t width, int group,
 struct PlanPlace {
   int head, tile;
   int units;     // of the group, 0 behind its pair's end
-  int64_t start; // the group's first unit
+  int64_t start; // the group's first unit (of its first step, behind `extra`)
   int64_t next;  // the next pair's first unit
 };
 
-PLAN_FN PlanPlace plan_place(const SlotWork& w, int group, int rows, int64_t left) {
+PLAN_FN PlanPlace plan_place(const SlotWork& w, int group, int rows, int64_t left, int extra = 0) {
   PlanPlace g;
-  const int64_t pair = left / w.pair_units;
+  // a 64-bit division takes a hundred instructions more
+  const int64_t pair = left <= INT32_MAX ? (int64_t)((int32_t)left / w.pair_units) : left / w.pair_units;
   const int off = (int)(left - pair * w.pair_units);
   g.head = (int)(pair / w.pairs);
   const int i = (int)(pair - (int64_t)g.head * w.pairs), j = w.tiles - 1 - i;
@@ -92,12 +94,12 @@ PLAN_FN PlanPlace plan_place(const SlotWork& w, int group, int rows, int64_t lef
   g.next = left - off + w.pair_units;
   g.tile = i;
   g.units = ui;
-  g.start = left - off;
-  if (off >= ui) {
+  g.start = left - off + extra;
+  if (off >= ui + extra) {
     const int uj = j > i ? tile_units(w, group, rows, j) : 0;
     g.tile = j;
-    g.units = off < ui + uj ? uj : 0;
-    g.start = left - off + ui;
+    g.units = off < ui + uj + 2 * extra ? uj : 0;
+    g.start = left - off + ui + 2 * extra;
   }
   return g;
 }
