@@ -155,6 +155,18 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
   constexpr int kThreads = 64 * RW * KW;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int part = wave / RW;                 // the wave's part of the keys
+  // Two waves share a SIMD, of one workgroup or of two (ids 256 apart).  Matrix instructions go first, and of
+  // two waves at the same place always the same one, so that the waves do not stay side by side in
+  // the phases that need the same unit (two prompts: 468 us without, 449 with).
+  const int odd = RW * KW == 8 ? wave >> 2 : (int)(blockIdx.x >> 8 & 1);
+  auto matrix_first = [&]() {
+    if (odd) __builtin_amdgcn_s_setprio(3);
+    else __builtin_amdgcn_s_setprio(2);
+  };
+  auto matrix_done = [&]() {
+    if (odd) __builtin_amdgcn_s_setprio(1);
+    else __builtin_amdgcn_s_setprio(0);
+  };
   const int wrow = (wave % RW) * kWaveRows;   // its first row in the tile
   const int n = lane & 15, quad = lane >> 4;
   const int G = a.group, H = a.c.kv_heads;
@@ -441,6 +453,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+    matrix_first();
     if constexpr (kF32) {
       Chunk ko[2][kSteps];
       k_operands(k[j][0], ko[0]);
@@ -473,6 +486,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
           }
         }
     }
+    matrix_done();
     pages_of(ahead, pa[j], pb[j]);
     load_k(ahead, pa[j], pb[j], k[j]);
     if (__builtin_expect(partial, 0)) {
@@ -504,6 +518,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
 #pragma unroll
     for (int i = 0; i < NQ; ++i) l[i] += sums[i];
+    matrix_first();
     float vs[8];
 #pragma unroll
     for (int r = 0; r < 8; ++r) vs[r] = scale_of(v[j].scale[r >> 2] >> (8 * (r & 3)) & 255u);
@@ -521,6 +536,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
             o[i][4 * g + 2 * h + 1] = Op::score(hi[u], p[i][u], o[i][4 * g + 2 * h + 1]);
           }
       }
+    matrix_done();
     load_v(ahead, pa[j], pb[j], v[j]);
    }
   }
@@ -664,6 +680,75 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }
 
+// The join of cut groups (k_attend_join) for tiles of 16 rows, whose groups are few and may go through
+// hundreds of spans: a workgroup takes all rows of a group, 1024 / (8 D / 4) of them at once, and its pieces by
+// eights, so that their loads do not follow each other (8 groups of 64 pieces: 15 us by
+// k_attend_join, 5 so).
+template <typename E, int D>
+__global__ __launch_bounds__(1024) void k_attend4_join(AttendArgs a, int rows_per_tile) {
+  constexpr int kCols = D / 4, kLanes = 8, kAtOnce = 1024 / (kCols * kLanes);
+  __shared__ float sh_m[kAtOnce][kLanes], sh_l[kAtOnce][kLanes];
+  __shared__ f32x4 sh_o[kLanes][kAtOnce][kCols];
+  const int k = (int)blockIdx.x;
+  if (k >= a.cuts[0].first) return;
+  const AttendCut cut = a.cuts[1 + k];
+  if (cut.rows == 0) return;
+  const int c = (int)threadIdx.x % kCols, at = (int)threadIdx.x / kCols % kAtOnce, j = (int)threadIdx.x / (kCols * kAtOnce);
+  for (int r0 = 0; r0 < cut.rows; r0 += kAtOnce) {
+    const int r = r0 + at;
+    const bool live = r < cut.rows;
+    const auto record = [&](int p) {
+      return (p == k ? (int64_t)cut.first : 2 * (int64_t)p) * rows_per_tile + r;
+    };
+    float m = kNone;
+    if (live) {
+#pragma unroll 8
+      for (int p = k + j; p <= cut.last; p += kLanes) m = fmaxf(m, a.part_ml[record(p) * 2]);
+    }
+    __syncthreads();  // the last rows are out of LDS
+    if (c == 0) sh_m[at][j] = m;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kLanes; ++x) m = fmaxf(m, sh_m[at][x]);
+    float l = 0.f;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    if (live) {
+#pragma unroll 8
+      for (int p = k + j; p <= cut.last; p += kLanes) {
+        const int64_t o = record(p);
+        const float f = __builtin_amdgcn_exp2f(a.part_ml[o * 2] - m);
+        l += a.part_ml[o * 2 + 1] * f;
+        sum += *reinterpret_cast<const f32x4*>(a.part_o + o * D + 4 * c) * f;
+      }
+    }
+    if (c == 0) sh_l[at][j] = l;
+    sh_o[j][at][c] = sum;
+    __syncthreads();
+    if (j > 0 || !live) continue;
+    l = 0.f;
+    sum = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int x = 0; x < kLanes; ++x) {
+      l += sh_l[at][x];
+      sum += sh_o[x][at][c];
+    }
+    const int G = a.group, token = (cut.row0 + r) / G;
+    E* to = static_cast<E*>(a.out) +
+            ((int64_t)(cut.token0 + token) * a.heads + cut.head * G + (cut.row0 + r - token * G)) * D + 4 * c;
+    store4<E>(to, sum * (l > 0.f ? 1.f / l : 0.f));
+  }
+}
+
+template <typename E>
+void start4_join(int rows, const AttendArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)a.grid), block(1024);
+  switch (a.c.head_dim) {
+    case 64: hipLaunchKernelGGL((k_attend4_join<E, 64>), grid, block, 0, stream, a, rows); break;
+    case 128: hipLaunchKernelGGL((k_attend4_join<E, 128>), grid, block, 0, stream, a, rows); break;
+    default: hipLaunchKernelGGL((k_attend4_join<E, 256>), grid, block, 0, stream, a, rows); break;
+  }
+}
+
 template <typename E, int D, int NQ, int RW, int KW, int kBuf>
 void start4(const AttendArgs& a, hipStream_t stream) {
   const dim3 grid(a.grid), block(64 * RW * KW);
@@ -673,7 +758,7 @@ void start4(const AttendArgs& a, hipStream_t stream) {
 
 // Tiles in use: rows (16 NQ RW), NQ, RW, KW, steps on their way.
 #define ATTEND4_TILES(X) X(16, 1, 1, 4, 2) X(32, 2, 1, 4, 1) X(48, 3, 1, 4, 2) X(64, 2, 2, 2, 2) X(96, 3, 2, 2, 2) \
-  X(128, 2, 4, 2, 1) X(192, 3, 4, 2, 1) X(256, 2, 8, 1, 1) X(384, 3, 8, 1, 1)
+  X(128, 2, 4, 2, 1) X(192, 3, 4, 2, 1) X(256, 2, 8, 1, 2) X(384, 3, 8, 1, 2)
 #define ATTEND4_TILES_256(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1) X(64, 1, 4, 2, 1) X(128, 1, 8, 1, 1)
 #define ATTEND4_TILES_F32(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1)
 
@@ -744,7 +829,11 @@ hipError_t launch_attend4(bool bf16, int rows, const AttendArgs& a, hipStream_t 
     TimingScope t("attend_join", stream);
     const int per = join_rows(a.c.head_dim);
     const dim3 join((unsigned)a.grid, (unsigned)((rows + per - 1) / per));
-    if (bf16)
+    if (rows == 16 && bf16)
+      start4_join<uint16_t>(rows, a, stream);
+    else if (rows == 16)
+      start4_join<float>(rows, a, stream);
+    else if (bf16)
       hipLaunchKernelGGL(k_attend_join<uint16_t>, join, dim3(kPlanThreads), 0, stream, a, rows);
     else
       hipLaunchKernelGGL(k_attend_join<float>, join, dim3(kPlanThreads), 0, stream, a, rows);
