@@ -621,23 +621,122 @@ struct Shape4 {
   static constexpr int waves = NQ > 3 ? 1 : ((sizeof(E) == 2 && D <= 128) || RW * KW == 8 ? 2 : 1);
 };
 
+// The line of work (attend_common.h), or, where it has few groups, their pieces one after the other
+// (attend_plan.h, plan_target): before[] and spans then count pieces.
+struct Plan4 : Plan {
+  int64_t target;  // units of a piece, 0: the line is cut into spans
+  int64_t totals[kPlanWaves][2];
+  int near[kPlanThreads][3];  // a slot's token rows and length, if there are no more slots
+};
+
+__device__ __forceinline__ SlotWork near_work(const AttendArgs& a, const Plan4& plan, int s, int rows) {
+  return plan_slot(__builtin_amdgcn_readfirstlane(plan.near[s][0]), __builtin_amdgcn_readfirstlane(plan.near[s][1]),
+                   __builtin_amdgcn_readfirstlane(plan.near[s][2]), (int64_t)a.c.max_pages << a.c.page_shift, a.group,
+                   rows, a.c.kv_heads, a.extra);
+}
+
+template <int kThreads>
+__device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4& plan) {
+  static_assert(kThreads >= kPlanThreads, "a thread for each run of slots");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int per = (a.c.slots + kPlanThreads - 1) / kPlanThreads;
+  const int s0 = tid < kPlanThreads ? tid * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
+  const bool few = (int64_t)a.c.slots * a.c.kv_heads * 2 <= a.grid;  // at most, as far as slots tell
+  int64_t x = 0, groups = 0, steps = 0;
+  int long_chunk = 0, mine = 0;
+  for (int s = s0; s < s1; ++s) {
+    const SlotWork w = slot_work(a, s, rows);
+    x += w.units;
+    if (per == 1) {
+      plan.near[s][0] = w.o0;
+      plan.near[s][1] = w.o0 + w.chunk;
+      plan.near[s][2] = a.c.t.lens[s];
+    }
+    if (few && w.tiles > 0) {
+      mine = tile_units(w, a.group, rows, 0);
+      steps += (int64_t)mine * a.c.kv_heads;
+      groups += a.c.kv_heads;
+      long_chunk |= w.tiles > 1;
+    }
+  }
+  if (tid == 0) {
+    plan.before[0] = 0;
+    plan.per = per;
+    plan.target = 0;
+  }
+  if (few) {  // (then there are no more slots than threads)
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      steps += __shfl_xor(steps, off, 64);
+      groups += __shfl_xor(groups, off, 64);
+    }
+    if (lane == 0 && wave < kPlanWaves) {
+      plan.totals[wave][0] = steps;
+      plan.totals[wave][1] = groups;
+    }
+    const bool whole = !__syncthreads_or(long_chunk);
+    steps = groups = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWaves; ++w) {
+      steps += plan.totals[w][0];
+      groups += plan.totals[w][1];
+    }
+    if (whole && groups > 0) {
+      const int64_t target = plan_target(steps, groups, a.grid);
+      x = mine > 0 ? (int64_t)plan_pieces(mine, target) * a.c.kv_heads : 0;
+      if (tid == 0) plan.target = target;
+    }
+  }
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int64_t y = __shfl_up(x, off, 64);
+    if (lane >= off) x += y;
+  }
+  if (lane == 63 && wave < kPlanWaves) plan.sum[wave] = x;
+  __syncthreads();
+  int64_t total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    if (w < wave) x += plan.sum[w];
+    total += plan.sum[w];
+  }
+  if (tid < kPlanThreads) plan.before[tid + 1] = x;
+  if (tid == 0) {
+    const int64_t span = plan.target ? 1 : plan_span(total, a.grid);
+    plan.span = span;
+    plan.spans = (int)((total + span - 1) / span);
+  }
+  __syncthreads();
+}
+
+// The group of piece x of the batch: its slot is the run of slots that x lies in.  j, n: which piece of how many.
+__device__ __forceinline__ void find_piece(const AttendArgs& a, int rows, const Plan4& plan, int x,
+                                           Group& g, int& j, int& n) {
+  int lo = 0, hi = kPlanThreads - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (plan.before[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  const int left = x - (int)plan.before[lo];
+  g.w = near_work(a, plan, lo, rows);
+  g.slot = lo;
+  g.tile = 0;
+  g.units = tile_units(g.w, a.group, rows, 0);
+  n = plan_pieces(g.units, plan.target);
+  g.head = left / n;
+  j = left - g.head * n;
+}
+
 template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
 __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) void k_attend4(AttendArgs a) {
   constexpr int kRows = 16 * NQ * RW;
-  __shared__ Plan plan;
+  __shared__ Plan4 plan;
   __shared__ float sh_ml[KW * kRows * 2];
   __shared__ int sh_limit[kRows];
   __shared__ uint32_t sh_scale[NQ * RW * 64];
   __shared__ u32x4 sh[lds_pieces<E, D, NQ, RW, KW>()];
-  // what the plan's threads read of the slots, for the groups' places
-  __shared__ int near_slots[kPlanThreads][3];
-  const bool near = a.c.slots <= kPlanThreads;
-  for (int s = threadIdx.x; near && s < a.c.slots; s += 64 * RW * KW) {
-    near_slots[s][0] = min(max(a.offsets[s], 0), a.N);
-    near_slots[s][1] = min(max(a.offsets[s + 1], near_slots[s][0]), a.N);
-    near_slots[s][2] = a.c.t.lens[s];
-  }
-  make_plan(a, kRows, plan);
+  make_plan4<64 * RW * KW>(a, kRows, plan);
   const int64_t total = plan.before[kPlanThreads];
   // Workgroup ids go to the 8 XCDs in turn; each XCD takes a contiguous run of
   // spans, so that row tiles that read the same keys share its L2.
@@ -645,37 +744,49 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
   const int per_xcd = (plan.spans + 7) >> 3;
   const int idx = (int)(blockIdx.x >> 3), span = (int)(blockIdx.x & 7) * per_xcd + idx;
   if (idx >= per_xcd || span >= plan.spans) return;
+  const bool pieces = plan.target > 0;
   const int64_t x0 = span * plan.span, x1 = min(x0 + plan.span, total);
   Group g;
   g.slot_end = 0;
   AttendCut cut = {};
   for (int64_t x = x0; x < x1;) {
-    find_group(a, kRows, plan, x, g, [&](int s) {
-      if (!near) return slot_work(a, s, kRows);
-      return plan_slot(__builtin_amdgcn_readfirstlane(near_slots[s][0]), __builtin_amdgcn_readfirstlane(near_slots[s][1]),
-                       __builtin_amdgcn_readfirstlane(near_slots[s][2]), (int64_t)a.c.max_pages << a.c.page_shift,
-                       a.group, kRows, a.c.kv_heads, a.extra);
-    });
-    if (g.units == 0) {
-      x = g.next;
-      continue;
+    int first, end;
+    int64_t rec;  // a cut group's record: a span has two at most, of its first and of its last group
+    bool goes_on;
+    int last;
+    if (pieces) {
+      int j, n;
+      find_piece(a, kRows, plan, span, g, j, n);
+      first = piece_start(g.units, j, n);
+      end = piece_start(g.units, j + 1, n);
+      rec = n == 1 ? -1 : 2 * (int64_t)span;
+      goes_on = j == 0 && n > 1;
+      last = span + n - 1;
+      x = x1;
+    } else {
+      find_group(a, kRows, plan, x, g, [&](int s) { return plan.per == 1 ? near_work(a, plan, s, kRows) : slot_work(a, s, kRows); });
+      if (g.units == 0) {
+        x = g.next;
+        continue;
+      }
+      // a span may start, or end, in front of the group's first step
+      first = (int)max(x - g.start, (int64_t)0);
+      end = (int)min((int64_t)g.units, x1 - g.start);
+      if (end <= first) break;
+      rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
+      goes_on = first == 0 && end < g.units;
+      last = goes_on ? (int)((g.start + g.units - 1) / plan.span) : 0;
+      x = g.start + end;
     }
-    // a span may start, or end, in front of the group's first step
-    const int first = (int)max(x - g.start, (int64_t)0);
-    const int end = (int)min((int64_t)g.units, x1 - g.start);
-    if (end <= first) break;
-    // a cut group's record: a span has two at most, of its first and of its last group
-    const int64_t rec = first == 0 && end == g.units ? -1 : 2 * (int64_t)span + (x != x0);
-    if (first == 0 && end < g.units) {  // it goes on in the next span
+    if (goes_on) {
       cut.row0 = g.tile * kRows;
       cut.rows = min(kRows, g.w.chunk * a.group - cut.row0);
       cut.token0 = g.w.o0;
       cut.head = g.head;
       cut.first = (int)rec;
-      cut.last = (int)((g.start + g.units - 1) / plan.span);
+      cut.last = last;
     }
     attend4_steps<E, D, NQ, RW, KW, kBuf, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_scale, sh);
-    x = g.start + end;
   }
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }

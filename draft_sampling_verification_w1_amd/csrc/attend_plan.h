@@ -110,4 +110,16 @@ PLAN_FN int64_t plan_span(int64_t total, int grid) {
   return span > kMinSpan ? span : kMinSpan;
 }
 
+// Where a batch has few groups, of one row tile each, a group is cut by itself, into pieces of
+// about `target` units, so that no workgroup pays what a group costs beside its steps
+// twice.  total, groups: of the batch, groups > 0.  0: too many groups, the line is cut into spans.
+PLAN_FN int64_t plan_target(int64_t total, int64_t groups, int grid) {
+  if (2 * groups > grid) return 0;
+  const int64_t rest = grid - groups, target = (total + rest - 1) / rest;  // pieces: total / target + groups at most
+  return target > kMinSpan ? target : kMinSpan;
+}
+PLAN_FN int plan_pieces(int units, int64_t target) { return (int)((units + target - 1) / target); }
+// First unit of piece j of n.
+PLAN_FN int piece_start(int units, int j, int n) { return (int)((int64_t)units * j / n); }
+
 }  // namespace dspark
