@@ -51,12 +51,12 @@ struct Place {
   int64_t pos;   // position of the first row
 };
 
-// The workgroup's group (blockIdx.x).  Slot s's groups are numbered from offsets[s] / 8 + 3 s on,
-// which leaves room for a group that is cut at either end.  Each thread looks at its slots'
-// offsets and start position at once, so that finding the group is one round trip, its page
-// another.
+// The workgroup's group of `size` positions (blockIdx.x).  Slot s's groups are numbered from
+// offsets[s] / size + 3 s on, which leaves room for a group that is cut at either end.  Each thread
+// looks at its slots' offsets and start position at once, so that finding the group is one round
+// trip, its page another.
 __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int32_t* offsets,
-                                            const int32_t* starts) {
+                                            const int32_t* starts, int size) {
   __shared__ int found[6];
   const int w = blockIdx.x;
   if (threadIdx.x == 0) found[0] = -1;
@@ -64,8 +64,8 @@ __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int
   for (int s = threadIdx.x; s < c.slots; s += 256) {
     const int o0 = min(max(offsets[s], 0), N), o1 = min(max(offsets[s + 1], o0), N);
     const int start = starts[s], held = c.t.held[s];
-    const int first = o0 / kGroup + 3 * s;
-    if (o0 < o1 && first <= w && w < o1 / kGroup + 3 * (s + 1)) {
+    const int first = o0 / size + 3 * s;
+    if (o0 < o1 && first <= w && w < o1 / size + 3 * (s + 1)) {
       found[0] = s;
       found[1] = o0;
       found[2] = o1;
@@ -79,13 +79,13 @@ __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int
   const int s = found[0], o0 = found[1], o1 = found[2], start = found[4];
   if (s < 0) return g;
   const int64_t base = max(start, 0);
-  const int64_t first = (base / kGroup + found[3]) * kGroup;  // of the group
+  const int64_t first = (base / size + found[3]) * size;  // of the group
   g.e0 = first < base ? (int)(base - first) : 0;
   g.pos = first + g.e0;
   const int64_t row = o0 + (g.pos - base);
   if (row >= o1) return g;
   g.row = (int)row;
-  g.n = (int)min((int64_t)(kGroup - g.e0), o1 - row);
+  g.n = (int)min((int64_t)(size - g.e0), o1 - row);
   const int64_t j = g.pos >> c.page_shift;
   if (start >= 0 && j < min(found[5], c.max_pages)) {
     const int p = c.t.table[(int64_t)s * c.max_pages + j];
@@ -95,23 +95,27 @@ __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int
   return g;
 }
 
-// 8 elements in binary32.
-__device__ __forceinline__ void load8(const uint16_t* p, float (&x)[8]) {
-  const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+// 8 elements as they lie in memory, and in binary32.
+template <typename E>
+struct Eight {
+  u32x4 w[sizeof(E) / 2];
+  __device__ __forceinline__ void load(const E* p) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
+    for (int h = 0; h < (int)sizeof(E) / 2; ++h) w[h] = reinterpret_cast<const u32x4*>(p)[h];
   }
-}
-__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  __device__ __forceinline__ void values(float (&x)[8]) const {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const f32x4 w = reinterpret_cast<const f32x4*>(p)[h];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[4 * h + i] = w[i];
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (sizeof(E) == 2) {
+        x[2 * i] = bf16_lo(w[0][i]);
+        x[2 * i + 1] = bf16_hi(w[0][i]);
+      } else {
+        x[i] = __uint_as_float(w[0][i]);
+        x[4 + i] = __uint_as_float(w[1][i]);
+      }
+    }
   }
-}
+};
 // 8 elements rounded to nearest even.
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
   bf16x8 b;
@@ -338,173 +342,293 @@ __global__ __launch_bounds__(256) void k_cache_store(StoreArgs a) {
   constexpr int kTurns = kUnits > 8 ? kUnits / 8 : 1;      // or rounds of the wave for a head
   __shared__ float2 cs[kGroup * (D / 2)];
   __shared__ __align__(16) uint32_t tops[4][64 / kUnits * (D / 8)];
-  const Place g = find_place(a.c, a.N, a.offsets, a.c.t.lens);
+  const Place g = find_place(a.c, a.N, a.offsets, a.c.t.lens, kGroup);
   if (g.row < 0) return;
   const int half = a.rot / 2;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  // The waves' rounds: first V's, which need no angles, then K's and the queries'.
+  const int kv = (a.c.kv_heads + kHeads - 1) / kHeads * kTurns, qs = (a.heads + kHeads - 1) / kHeads * kTurns;
+  const int stride = 4 * (int)gridDim.y, rounds = 2 * kv + qs;
+  int round = (int)blockIdx.y * 4 + wave;
+  int turned = round < kv ? round + (kv - round + stride - 1) / stride * stride : round;
+
+  // A lane's two pieces (c0, c1) of token t of K's or a query's head.
+  const int u = lane % kUnits;
+  const bool turns = u < a.rot / 16, apart = !a.interleaved && turns;
+  const int c0 = apart ? u : 2 * u, c1 = apart ? u + a.rot / 16 : 2 * u + 1;
+  struct At {
+    bool query, live;
+    int h, t;
+    int64_t at;
+  };
+  const auto place = [&](int round) {
+    At p;
+    p.query = round >= 2 * kv;
+    const int x = (p.query ? round - 2 * kv : round - kv) % kTurns * 64 + lane;
+    p.h = (p.query ? round - 2 * kv : round - kv) / kTurns * kHeads + (kHeads > 1 ? x / (8 * kUnits) : 0);
+    p.t = x / kUnits % kGroup;
+    const int H = p.query ? a.heads : a.c.kv_heads;
+    p.live = p.h < H && p.t < g.n;
+    p.at = ((int64_t)(g.row + p.t) * H + p.h) * D;
+    return p;
+  };
+  Eight<E> next[2];
+  const auto fetch = [&](int round) {
+    const At p = place(round);
+    if (!p.live) return;
+    const E* from = static_cast<const E*>(p.query ? a.q : a.k) + p.at;
+    next[0].load(from + 8 * c0);
+    next[1].load(from + 8 * c1);
+  };
+  if (turned < rounds) fetch(turned);
   for (int x = threadIdx.x; x < g.n * half; x += 256) {
     const int t = x / half, j = x - t * half;
     cs[t * half + j] = cos_sin((double)(g.pos + t) * a.freqs[j]);
   }
+  for (; round < kv; round += stride) {
+    const int x = round % kTurns * 64 + lane;
+    const int h = round / kTurns * kHeads + (kHeads > 1 ? x / (8 * kUnits) : 0);
+    store_v<E, D, kPacked>(a, g, min(h, a.c.kv_heads - 1), kHeads > 1 ? x % (D / 2) : x, h < a.c.kv_heads);
+  }
   __syncthreads();
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int kv = (a.c.kv_heads + kHeads - 1) / kHeads, qs = (a.heads + kHeads - 1) / kHeads;
-  const int tasks = 2 * kv + qs;
-  for (int task = (int)blockIdx.y * 4 + wave; task < tasks; task += 4 * (int)gridDim.y) {
-    const bool values = task >= kv && task < 2 * kv;
-    const bool query = task >= 2 * kv;
-    const int first = (query ? task - 2 * kv : (values ? task - kv : task)) * kHeads;
+  // a round's loads are under way while the one before is turned and stored
+  for (; turned < rounds; turned += stride) {
+    const At at = place(turned);
+    float p[8], q[8];
+    next[0].values(p);
+    next[1].values(q);
+    if (turned + stride < rounds) fetch(turned + stride);
+    if (at.live && turns) {
+      const float2* w = cs + at.t * half + 8 * u;
+      if (apart) {
 #pragma unroll
-    for (int r = 0; r < kTurns; ++r) {
-      const int x = r * 64 + lane;
-      const int h = first + (kHeads > 1 ? x / (8 * kUnits) : 0);
-      if (values) {
-        const int i = kHeads > 1 ? x % (D / 2) : x;
-        store_v<E, D, kPacked>(a, g, min(h, a.c.kv_heads - 1), i, h < a.c.kv_heads);
-        continue;
-      }
-      const int H = query ? a.heads : a.c.kv_heads;
-      const int t = x / kUnits % kGroup, u = x % kUnits;
-      const bool live = h < H && t < g.n;
-      const bool apart = !a.interleaved && u < a.rot / 16;
-      const int c0 = apart ? u : 2 * u, c1 = apart ? u + a.rot / 16 : 2 * u + 1;
-      float p[8], q[8];
-      const int64_t at = ((int64_t)(g.row + t) * H + h) * D;
-      if (live) {
-        const E* from = static_cast<const E*>(query ? a.q : a.k) + at;
-        load8(from + 8 * c0, p);
-        load8(from + 8 * c1, q);
-        if (u < a.rot / 16) {
-          const float2* w = cs + t * half + 8 * u;
-          if (apart) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) turn(p[i], q[i], w[i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              turn(p[2 * i], p[2 * i + 1], w[i]);
-              turn(q[2 * i], q[2 * i + 1], w[4 + i]);
-            }
-          }
-        }
+        for (int i = 0; i < 8; ++i) turn(p[i], q[i], w[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = q[i] = 0.f;
-      }
-      if (query) {
-        if (live) {
-          E* to = static_cast<E*>(a.q_out) + at;
-          store8(to + 8 * c0, p);
-          store8(to + 8 * c1, q);
+        for (int i = 0; i < 4; ++i) {
+          turn(p[2 * i], p[2 * i + 1], w[i]);
+          turn(q[2 * i], q[2 * i + 1], w[4 + i]);
         }
-      } else {
-        // lanes of one token of one head share D / 8 maxima
-        store_k<E, D, kPacked>(a, g, h, t, c0, c1, p, q, live, tops[wave] + lane / kUnits * (D / 8));
       }
+    }
+    if (at.query) {
+      if (at.live) {
+        E* to = static_cast<E*>(a.q_out) + at.at;
+        store8(to + 8 * c0, p);
+        store8(to + 8 * c1, q);
+      }
+    } else {
+      // lanes of one token of one head share D / 8 maxima
+      store_k<E, D, kPacked>(a, g, at.h, at.t, c0, c1, p, q, at.live, tops[wave] + lane / kUnits * (D / 8));
     }
   }
 }
 
 // ---- tokens out of the pages -----------------------------------------------------------
-__device__ __forceinline__ void put8(uint16_t* to, uint32_t code, float s) {
+template <int kSel>
+__device__ __forceinline__ uint32_t two(uint16_t, uint32_t code, float s) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  union { bf16x2 b[4]; u32x4 w; } x;
-  x.b[0] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 0);
-  x.b[1] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 1);
-  x.b[2] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 2);
-  x.b[3] = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 3);
-  *reinterpret_cast<u32x4*>(to) = x.w;
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, kSel);
+  return __builtin_bit_cast(uint32_t, b);
 }
-__device__ __forceinline__ void put8(float* to, uint32_t code, float s) {
+template <int kSel>
+__device__ __forceinline__ u32x2 two(float, uint32_t code, float s) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));
-  const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 0);
-  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 1);
-  const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 2);
-  const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 3);
-  reinterpret_cast<f32x4*>(to)[0] = f32x4{a[0], a[1], b[0], b[1]};
-  reinterpret_cast<f32x4*>(to)[1] = f32x4{c[0], c[1], d[0], d[1]};
+  const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, kSel);
+  return __builtin_bit_cast(u32x2, b);
 }
-__device__ __forceinline__ void put2(uint16_t* to, uint32_t code, float s) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  *reinterpret_cast<bf16x2*>(to) = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(code, s, 0);
+// kPairs pairs of elements, 16 bytes at a time where there are as many.
+template <typename P, int kPairs>
+__device__ __forceinline__ void put(void* to, const P (&x)[kPairs]) {
+  constexpr int kBytes = kPairs * (int)sizeof(P);
+  typedef uint32_t Word __attribute__((ext_vector_type(kBytes >= 16 ? 4 : 2)));
+  union { P p[kPairs]; Word w[kBytes / (int)sizeof(Word)]; } all;
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) all.p[i] = x[i];
+#pragma unroll
+  for (int i = 0; i < kBytes / (int)sizeof(Word); ++i) static_cast<Word*>(to)[i] = all.w[i];
 }
-__device__ __forceinline__ void put2(float* to, uint32_t code, float s) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  *reinterpret_cast<f32x2*>(to) = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, 0);
-}
+
 // A block of values that are all NaN.
 constexpr uint32_t kNoScale = 255u;
+// Factors of 8 tokens' scale bytes.
+__device__ __forceinline__ float factor(u32x2 bytes, int t) {
+  const uint32_t b = bytes[t >> 2] >> (8 * (t & 3)) & 255u;
+  return b == kNoScale ? NAN : scale_of(b);
+}
 
-template <typename E, int D, bool kPacked>
-__global__ __launch_bounds__(256) void k_cache_read(ReadArgs a) {
-  constexpr int kE = 16 / (int)sizeof(E);
-  const Place g = find_place(a.c, a.N, a.offsets, a.first);
-  if (g.row < 0) return;
+// 4 x 4 words of four neighbouring lanes transposed: w[i] of lane j becomes w[j] of lane i.
+__device__ __forceinline__ void transpose4(u32x4& w, int lane) {
+  // first pairs of lanes, then pairs of pairs (quad_perm 1 0 3 2 and 2 3 0 1)
+  const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {
+    const uint32_t give = odd ? w[i] : w[i + 1];
+    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0xB1, 0xF, 0xF, true);
+    if (odd) w[i] = got;
+    else w[i + 1] = got;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t give = high ? w[i] : w[i + 2];
+    const uint32_t got = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)give, 0x4E, 0xF, 0xF, true);
+    if (high) w[i] = got;
+    else w[i + 2] = got;
+  }
+}
+
+// What a wave reads of 8 positions: tokens t0 <= t < t1 of them have rows, the first of which is `row`;
+// `at`: the first position's place in the page.
+struct Part {
+  int64_t row;
+  int t0, t1, at, page;
+};
+
+// Heads h0 .. of K in 4 bits.  A lane's 8 elements of each token; four lanes' codes of a block of 32
+// elements are loaded as 16 bytes of one token each and change places.
+template <typename E, int D>
+__device__ __forceinline__ void read_k4(const ReadArgs& a, const Part& g, int h0, int lane) {
+  constexpr int kLanes = D / 8;  // of a head
   const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t p = max(g.page, 0);
-  const bool there = g.page >= 0;
-  for (int task = (int)blockIdx.y * 4 + wave; task < 2 * H; task += 4 * (int)gridDim.y) {
-    const bool values = task >= H;
-    const int h = values ? task - H : task;
-    E* const out = static_cast<E*>(values ? a.v : a.k) + ((int64_t)g.row * H + h) * D;
-    const int64_t step = (int64_t)H * D;  // from a token's row to the next
-    if (!values) {
-      // a lane takes 8 elements of a token
-      for (int x = lane; x < kGroup * (D / 8); x += 64) {
-        const int t = x / (D / 8), c = x % (D / 8);
-        if (t >= g.n) break;
-        const int row = g.at + g.e0 + t;
-        E* const to = out + t * step + 8 * c;
-        if constexpr (kPacked) {
-          const uint8_t* blob = static_cast<const uint8_t*>(a.K) + p * a.c.page_bytes;
-          const uint32_t code =
-              *reinterpret_cast<const uint32_t*>(blob + h * (page * (D / 2)) + ((c >> 2) * page + row) * 16 + (c & 3) * 4);
-          const uint32_t byte = blob[H * page * (D / 2) + h * (page * (D / 32)) + (c >> 2) * page + row];
-          put8(to, there ? code : 0u, there ? (byte == kNoScale ? NAN : scale_of(byte)) : 1.f);
-        } else {
-          const E* from = static_cast<const E*>(a.K) + (p * H + h) * page * D;
+  const int c = lane % kLanes, h = h0 + lane / kLanes, hh = min(h, H - 1);
+  const uint8_t* blob = static_cast<const uint8_t*>(a.K) + (int64_t)max(g.page, 0) * a.c.page_bytes;
+  const uint8_t* codes = blob + hh * (page * (D / 2)) + ((c >> 2) * page + g.at + (c & 3)) * 16;
+  u32x4 w[2] = {reinterpret_cast<const u32x4*>(codes)[0], reinterpret_cast<const u32x4*>(codes)[4]};
+  u32x2 bytes = *reinterpret_cast<const u32x2*>(blob + H * page * (D / 2) + hh * (page * (D / 32)) +
+                                                (c >> 2) * page + g.at);
+  if (g.page < 0) {
+    w[0] = w[1] = u32x4{0u, 0u, 0u, 0u};
+    bytes = u32x2{0u, 0u};
+  }
+  transpose4(w[0], lane);
+  transpose4(w[1], lane);
+  if (h >= H) return;
+  E* const out = static_cast<E*>(a.k) + ((g.row - g.t0) * H + h) * D + 8 * c;
 #pragma unroll
-          for (int i = 0; i < 8 / kE; ++i) {
-            const u32x4 w = *reinterpret_cast<const u32x4*>(from + ((int64_t)(c * (8 / kE) + i) * page + row) * kE);
-            *reinterpret_cast<u32x4*>(to + i * kE) = there ? w : u32x4{0u, 0u, 0u, 0u};
-          }
-        }
+  for (int t = 0; t < kGroup; ++t) {
+    if (t < g.t0 || t >= g.t1) continue;
+    const uint32_t code = w[t >> 2][t & 3];
+    const float s = factor(bytes, t);
+    const decltype(two<0>(E(), 0u, 0.f)) x[4] = {two<0>(E(), code, s), two<1>(E(), code, s),
+                                                 two<2>(E(), code, s), two<3>(E(), code, s)};
+    put(out + (int64_t)t * H * D, x);
+  }
+}
+
+// Heads h0 .. h0 + 3 of V in 4 bits.  A lane's D / 16 neighbouring elements of all tokens.
+template <typename E, int D>
+__device__ __forceinline__ void read_v4(const ReadArgs& a, const Part& g, int h0, int lane) {
+  constexpr int kRun = D / 16;  // elements
+  const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
+  const int n = lane % 16, h = h0 + lane / 16, hh = min(h, H - 1);
+  const uint8_t* blob = static_cast<const uint8_t*>(a.V) + (int64_t)max(g.page, 0) * a.c.page_bytes;
+  const uint8_t* codes = blob + hh * (page * (D / 2)) + (g.at / kGroup * (D / 64) * 16 + n) * 16;
+  u32x4 w[D / 64];
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) w[i] = reinterpret_cast<const u32x4*>(codes)[16 * i];
+  u32x2 bytes = *reinterpret_cast<const u32x2*>(blob + H * page * (D / 2) + hh * (page * (D / 32)) +
+                                                n * kRun / 32 * page + g.at);
+  if (g.page < 0) {
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) w[i] = u32x4{0u, 0u, 0u, 0u};
+    bytes = u32x2{0u, 0u};
+  }
+  if (h >= H) return;
+  E* const out = static_cast<E*>(a.v) + ((g.row - g.t0) * H + h) * D + n * kRun;
+#pragma unroll
+  for (int t = 0; t < kGroup; ++t) {
+    if (t < g.t0 || t >= g.t1) continue;
+    const float s = factor(bytes, t);
+    decltype(two<0>(E(), 0u, 0.f)) x[kRun / 2];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t word = w[i][2 * e + (t >> 2)];
+        auto& to = x[2 * i + e];
+        if ((t & 3) == 0) to = two<0>(E(), word, s);
+        if ((t & 3) == 1) to = two<1>(E(), word, s);
+        if ((t & 3) == 2) to = two<2>(E(), word, s);
+        if ((t & 3) == 3) to = two<3>(E(), word, s);
       }
+    put(out + (int64_t)t * H * D, x);
+  }
+}
+
+// A head of K, 8 elements of a token per lane and load.
+template <typename E, int D>
+__device__ __forceinline__ void read_k(const ReadArgs& a, const Part& g, int h, int lane) {
+  constexpr int kE = 16 / (int)sizeof(E), kTurns = kGroup * (D / 8) / 64;
+  const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
+  const E* from = static_cast<const E*>(a.K) + ((int64_t)max(g.page, 0) * H + h) * page * D;
+  E* const out = static_cast<E*>(a.k) + ((g.row - g.t0) * H + h) * D;
+  u32x4 w[kTurns][8 / kE];
+#pragma unroll
+  for (int r = 0; r < kTurns; ++r)
+#pragma unroll
+    for (int i = 0; i < 8 / kE; ++i) {
+      const int x = 64 * r + lane, t = x / (D / 8), c = x % (D / 8);
+      w[r][i] = *reinterpret_cast<const u32x4*>(from + ((int64_t)(c * (8 / kE) + i) * page + g.at + t) * kE);
+    }
+#pragma unroll
+  for (int r = 0; r < kTurns; ++r) {
+    const int x = 64 * r + lane, t = x / (D / 8), c = x % (D / 8);
+    if (t < g.t0 || t >= g.t1) continue;
+#pragma unroll
+    for (int i = 0; i < 8 / kE; ++i)
+      *reinterpret_cast<u32x4*>(out + (int64_t)t * H * D + 8 * c + i * kE) =
+          g.page < 0 ? u32x4{0u, 0u, 0u, 0u} : w[r][i];
+  }
+}
+
+// A head of V: a lane takes two neighbouring elements of the tokens.
+template <typename E, int D>
+__device__ __forceinline__ void read_v(const ReadArgs& a, const Part& g, int h, int lane) {
+  constexpr int kE = 16 / (int)sizeof(E);
+  typedef E Pair __attribute__((ext_vector_type(2)));
+  const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
+  const E* from = static_cast<const E*>(a.V) + ((int64_t)max(g.page, 0) * H + h) * page * D;
+  E* const out = static_cast<E*>(a.v) + ((g.row - g.t0) * H + h) * D;
+  for (int i = lane; i < D / 2; i += 64) {
+    alignas(16) E x[2][kGroup];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int q = 0; q < kGroup / kE; ++q)
+        *reinterpret_cast<u32x4*>(&x[e][q * kE]) =
+            *reinterpret_cast<const u32x4*>(from + ((int64_t)(g.at / kE + q) * D + 2 * i + e) * kE);
+#pragma unroll
+    for (int t = 0; t < kGroup; ++t)
+      if (t >= g.t0 && t < g.t1)
+        *reinterpret_cast<Pair*>(out + (int64_t)t * H * D + 2 * i) =
+            g.page < 0 ? Pair{(E)0, (E)0} : Pair{x[0][t], x[1][t]};
+  }
+}
+
+// A workgroup takes `run` times 8 positions of a page.
+template <typename E, int D, bool kPacked>
+__global__ __launch_bounds__(256) void k_cache_read(ReadArgs a, int run) {
+  constexpr int kHeadsK = kPacked ? 512 / D : 1, kHeadsV = kPacked ? 4 : 1;  // that a wave takes at once
+  const Place p = find_place(a.c, a.N, a.offsets, a.first, kGroup * run);
+  if (p.row < 0) return;
+  const int H = a.c.kv_heads;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ks = (H + kHeadsK - 1) / kHeadsK, tasks = ks + (H + kHeadsV - 1) / kHeadsV;
+  for (int x = (int)blockIdx.y * 4 + wave; x < run * tasks; x += 4 * (int)gridDim.y) {
+    const int sub = x / tasks, task = x - sub * tasks, base = sub * kGroup;
+    Part g;
+    g.t0 = max(p.e0 - base, 0);
+    g.t1 = min(p.e0 + p.n - base, kGroup);
+    if (g.t0 >= g.t1) continue;
+    g.row = p.row + max(base - p.e0, 0);
+    g.at = p.at + base;
+    g.page = p.page;
+    if (task < ks) {
+      if constexpr (kPacked) read_k4<E, D>(a, g, task * kHeadsK, lane);
+      else read_k<E, D>(a, g, task, lane);
     } else {
-      // a lane takes two neighbouring elements of the group's tokens
-      for (int i = lane; i < D / 2; i += 64) {
-        if constexpr (kPacked) {
-          const uint8_t* blob = static_cast<const uint8_t*>(a.V) + p * a.c.page_bytes;
-          const u32x2 code = *reinterpret_cast<const u32x2*>(blob + h * (page * (D / 2)) + v_code_at<D>(g.at >> 3, i));
-          const u32x2 byte = *reinterpret_cast<const u32x2*>(
-              blob + H * page * (D / 2) + h * (page * (D / 32)) + (i >> 4) * page + g.at);
-#pragma unroll
-          for (int t = 0; t < kGroup; ++t) {
-            const int r = t - g.e0;
-            const uint32_t s = byte[t >> 2] >> (8 * (t & 3)) & 255u;
-            if (r >= 0 && r < g.n)
-              put2(out + r * step + 2 * i, there ? code[t >> 2] >> (8 * (t & 3)) : 0u,
-                   there ? (s == kNoScale ? NAN : scale_of(s)) : 1.f);
-          }
-        } else {
-          typedef E Pair __attribute__((ext_vector_type(2)));
-          const E* from = static_cast<const E*>(a.V) + (p * H + h) * page * D;
-          alignas(16) E x[2][kGroup];
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int q = 0; q < kGroup / kE; ++q)
-              *reinterpret_cast<u32x4*>(&x[e][q * kE]) = *reinterpret_cast<const u32x4*>(
-                  from + ((int64_t)(g.at / kE + q) * D + 2 * i + e) * kE);
-#pragma unroll
-          for (int t = 0; t < kGroup; ++t) {
-            const int r = t - g.e0;
-            if (r >= 0 && r < g.n)
-              *reinterpret_cast<Pair*>(out + r * step + 2 * i) =
-                  there ? Pair{x[0][t], x[1][t]} : Pair{(E)0, (E)0};
-          }
-        }
-      }
+      if constexpr (kPacked) read_v4<E, D>(a, g, (task - ks) * kHeadsV, lane);
+      else read_v<E, D>(a, g, task - ks, lane);
     }
   }
 }
@@ -547,9 +671,11 @@ hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStr
 
 hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStream_t stream) {
   TimingScope t("cache_read", stream);
-  const int active = a.N / kGroup + a.c.slots;
-  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(active, 2 * a.c.kv_heads));
-#define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a)
+  int run = 1;  // finding the place is shared by more tokens where there are enough to fill the card
+  while (2 * run * kGroup <= (1 << a.c.page_shift) && run < 8 && a.N / (2 * run * kGroup) >= 2048) run *= 2;
+  const int size = run * kGroup, tasks = packed ? (a.c.kv_heads + 3) / 4 + (a.c.kv_heads * a.c.head_dim + 511) / 512 : 2 * a.c.kv_heads;
+  const dim3 grid((unsigned)(a.N / size + 3 * a.c.slots), split_of(a.N / size + a.c.slots, run * tasks));
+#define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a, run)
 #define READ_DIMS(E, P)                       \
   switch (a.c.head_dim) {                     \
     case 64: READ(E, 64, P); break;           \
