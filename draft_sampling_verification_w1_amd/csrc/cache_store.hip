@@ -55,13 +55,14 @@ struct Place {
 // offsets[s] / size + 3 s on, which leaves room for a group that is cut at either end.  Each thread
 // looks at its slots' offsets and start position at once, so that finding the group is one round
 // trip, its page another.
+template <int kThreads>
 __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int32_t* offsets,
                                             const int32_t* starts, int size) {
   __shared__ int found[6];
   const int w = blockIdx.x;
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
-  for (int s = threadIdx.x; s < c.slots; s += 256) {
+  for (int s = threadIdx.x; s < c.slots; s += kThreads) {
     const int o0 = min(max(offsets[s], 0), N), o1 = min(max(offsets[s + 1], o0), N);
     const int start = starts[s], held = c.t.held[s];
     const int first = o0 / size + 3 * s;
@@ -131,7 +132,9 @@ __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 
 // sin and cos of a binary64 angle (below 2^40 in magnitude), rounded to binary32.
 __device__ __forceinline__ float2 cos_sin(double angle) {
-  const double k = rint(angle * 0.63661977236758134);
+  // the nearest whole number, left in the low bits of the sum
+  const double sum = fma(angle, 0.63661977236758134, 6755399441055744.0);  // + 1.5 2^52
+  const double k = sum - 6755399441055744.0;
   double r = fma(-k, 1.5707963267948966, angle);
   r = fma(-k, 6.123233995736766e-17, r);
   const double z = r * r;
@@ -151,7 +154,7 @@ __device__ __forceinline__ float2 cos_sin(double angle) {
   c = fma(c, z, 4.1666666666666664e-02);
   c = fma(c, z, -0.5);
   c = fma(c, z, 1.0);
-  const int q = (int)((int64_t)k & 3);
+  const int q = (int)(__double_as_longlong(sum) & 3);
   const float fs = (float)s, fc = (float)c;
   const float a = (q & 1) ? fs : fc, b = (q & 1) ? fc : fs;
   return make_float2((q == 1 || q == 2) ? -a : a, (q & 2) ? -b : b);
@@ -265,16 +268,60 @@ __device__ __forceinline__ void store_k(const StoreArgs& a, const Place& g, int 
   }
 }
 
-// Elements 2 i and 2 i + 1 of head h of V, all tokens of the group.
+// Four neighbouring places of kBytes bytes each, those of `mask` stored in as few pieces as they make.
+template <int kBytes>
+__device__ __forceinline__ void put4(uint8_t* to, const uint32_t* w, uint32_t mask) {
+  if (mask == 15u) {
+    typedef uint32_t Four __attribute__((ext_vector_type(kBytes)));
+    Four all;
+#pragma unroll
+    for (int i = 0; i < kBytes; ++i) {
+      if constexpr (kBytes == 1) all = w[i];
+      else all[i] = w[i];
+    }
+    *reinterpret_cast<Four*>(to) = all;
+    return;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t m = mask >> (2 * h) & 3u;
+    if constexpr (kBytes == 4) {
+      if (m == 3u) *reinterpret_cast<u32x2*>(to + 8 * h) = u32x2{w[2 * h], w[2 * h + 1]};
+      else if (m) *reinterpret_cast<uint32_t*>(to + 8 * h + (m & 2u) * 2) = m == 1u ? w[2 * h] : w[2 * h + 1];
+    } else if constexpr (kBytes == 2) {
+      if (m == 3u) *reinterpret_cast<uint32_t*>(to + 4 * h) = w[h];
+      else if (m) *reinterpret_cast<uint16_t*>(to + 4 * h + (m & 2u)) = (uint16_t)(m == 1u ? w[h] : w[h] >> 16);
+    } else {
+      const uint32_t x = w[0] >> (16 * h);
+      if (m == 3u) *reinterpret_cast<uint16_t*>(to + 2 * h) = (uint16_t)x;
+      else if (m) to[2 * h + (m >> 1)] = (uint8_t)(m == 1u ? x : x >> 8);
+    }
+  }
+}
+// The group's 8 places side by side (one or two bytes each).
+template <int kBytes>
+__device__ __forceinline__ void put8places(uint8_t* to, const uint32_t* w, uint32_t mask) {
+  if (mask == 255u) {
+    if constexpr (kBytes == 2) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+    else *reinterpret_cast<u32x2*>(to) = u32x2{w[0], w[1]};
+    return;
+  }
+  put4<kBytes>(to, w, mask & 15u);
+  put4<kBytes>(to + 4 * kBytes, w + kBytes, mask >> 4);
+}
+
+// Elements 2 i and 2 i + 1 of head h of V, all tokens of the group, by their places in it.
 template <typename E, int D, bool kPacked>
 __device__ __forceinline__ void store_v(const StoreArgs& a, const Place& g, int h, int i, bool live) {
   const int page = 1 << a.c.page_shift, H = a.c.kv_heads;
   const E* from = static_cast<const E*>(a.v) + ((int64_t)g.row * H + h) * D + 2 * i;
+  const uint32_t mask = ((1u << g.n) - 1u) << g.e0;
+  // places without a token hold a neighbour's
+  const auto row = [&](int t) { return (int64_t)min(max(t - g.e0, 0), g.n - 1) * H * D; };
   if constexpr (kPacked) {
     float2 x[kGroup];
 #pragma unroll
-    for (int t = 0; t < kGroup; ++t)
-      x[t] = live ? load2(from + (int64_t)min(t, g.n - 1) * H * D) : make_float2(0.f, 0.f);
+    for (int t = 0; t < kGroup; ++t) x[t] = live ? load2(from + row(t)) : make_float2(0.f, 0.f);
     uint32_t word[2] = {0u, 0u}, bytes[2] = {0u, 0u};
 #pragma unroll
     for (int t = 0; t < kGroup; ++t) {
@@ -291,65 +338,58 @@ __device__ __forceinline__ void store_v(const StoreArgs& a, const Place& g, int 
     }
     if (!live || g.page < 0) return;
     uint8_t* blob = static_cast<uint8_t*>(a.V) + (int64_t)g.page * a.c.page_bytes;
-    uint8_t* code = blob + h * (page * (D / 2)) + v_code_at<D>(g.at >> 3, i);
-    uint8_t* scale = blob + H * page * (D / 2) + h * (page * (D / 32)) + (i >> 4) * page + g.at;
-    if (g.n == kGroup) {
-      *reinterpret_cast<u32x2*>(code) = u32x2{word[0], word[1]};
-      if ((i & 15) == 0) *reinterpret_cast<u32x2*>(scale) = u32x2{bytes[0], bytes[1]};
-    } else {
-#pragma unroll
-      for (int t = 0; t < kGroup; ++t) {
-        if (t >= g.n) break;
-        code[g.e0 + t] = (uint8_t)(word[t >> 2] >> (8 * (t & 3)));
-        if ((i & 15) == 0) scale[g.e0 + t] = (uint8_t)(bytes[t >> 2] >> (8 * (t & 3)));
-      }
-    }
+    put8places<1>(blob + h * (page * (D / 2)) + v_code_at<D>(g.at >> 3, i), word, mask);
+    if ((i & 15) == 0)
+      put8places<1>(blob + H * page * (D / 2) + h * (page * (D / 32)) + (i >> 4) * page + g.at, bytes, mask);
   } else {
     if (!live || g.page < 0) return;
     constexpr int kE = 16 / (int)sizeof(E);
-    typedef E Pair __attribute__((ext_vector_type(2)));
-    alignas(16) E x[2][kGroup];
-#pragma unroll
-    for (int t = 0; t < kGroup; ++t) {
-      const Pair p = *reinterpret_cast<const Pair*>(from + (int64_t)min(t, g.n - 1) * H * D);
-      x[0][t] = p[0];
-      x[1][t] = p[1];
-    }
     E* to = static_cast<E*>(a.V) + ((int64_t)g.page * H + h) * page * D;
+    if constexpr (sizeof(E) == 2) {
+      uint32_t x[kGroup], w[2][kGroup / 2];
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (g.n == kGroup) {
+      for (int t = 0; t < kGroup; ++t) x[t] = *reinterpret_cast<const uint32_t*>(from + row(t));
 #pragma unroll
-        for (int p = 0; p < kGroup / kE; ++p)
-          *reinterpret_cast<u32x4*>(to + ((int64_t)(g.at / kE + p) * D + 2 * i + e) * kE) =
-              *reinterpret_cast<const u32x4*>(&x[e][p * kE]);
-      } else {
-#pragma unroll
-        for (int t = 0; t < kGroup; ++t) {
-          if (t >= g.n) break;
-          const int row = g.at + g.e0 + t;
-          to[((int64_t)(row / kE) * D + 2 * i + e) * kE + row % kE] = x[e][t];
-        }
+      for (int t = 0; t < kGroup / 2; ++t) {
+        w[0][t] = x[2 * t] & 0xFFFFu | x[2 * t + 1] << 16;
+        w[1][t] = x[2 * t] >> 16 | x[2 * t + 1] & 0xFFFF0000u;
       }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        put8places<2>(reinterpret_cast<uint8_t*>(to + ((int64_t)(g.at / kE) * D + 2 * i + e) * kE), w[e], mask);
+    } else {
+      u32x2 x[kGroup];
+#pragma unroll
+      for (int t = 0; t < kGroup; ++t) x[t] = *reinterpret_cast<const u32x2*>(from + row(t));
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int p = 0; p < kGroup / kE; ++p) {
+          const uint32_t w[4] = {x[4 * p][e], x[4 * p + 1][e], x[4 * p + 2][e], x[4 * p + 3][e]};
+          put4<4>(reinterpret_cast<uint8_t*>(to + ((int64_t)(g.at / kE + p) * D + 2 * i + e) * kE), w,
+                  mask >> (4 * p) & 15u);
+        }
     }
   }
 }
 
+constexpr int kStoreThreads = 64 * kGroup;  // a wave for each token's angles
+
 template <typename E, int D, bool kPacked>
-__global__ __launch_bounds__(256) void k_cache_store(StoreArgs a) {
+__global__ __launch_bounds__(kStoreThreads, sizeof(E) == 2 ? 6 : 4) void k_cache_store(StoreArgs a) {
   constexpr int kUnits = D / 16;                           // lanes of a token of one head
   constexpr int kHeads = kUnits < 8 ? 8 / kUnits : 1;      // heads that a wave takes at once
   constexpr int kTurns = kUnits > 8 ? kUnits / 8 : 1;      // or rounds of the wave for a head
   __shared__ float2 cs[kGroup * (D / 2)];
-  __shared__ __align__(16) uint32_t tops[4][64 / kUnits * (D / 8)];
-  const Place g = find_place(a.c, a.N, a.offsets, a.c.t.lens, kGroup);
+  __shared__ __align__(16) uint32_t tops[kGroup][64 / kUnits * (D / 8)];
+  const Place g = find_place<kStoreThreads>(a.c, a.N, a.offsets, a.c.t.lens, kGroup);
   if (g.row < 0) return;
   const int half = a.rot / 2;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   // The waves' rounds: first V's, which need no angles, then K's and the queries'.
   const int kv = (a.c.kv_heads + kHeads - 1) / kHeads * kTurns, qs = (a.heads + kHeads - 1) / kHeads * kTurns;
-  const int stride = 4 * (int)gridDim.y, rounds = 2 * kv + qs;
-  int round = (int)blockIdx.y * 4 + wave;
+  const int stride = kGroup * (int)gridDim.y, rounds = 2 * kv + qs;
+  int round = (int)blockIdx.y * kGroup + wave;
   int turned = round < kv ? round + (kv - round + stride - 1) / stride * stride : round;
 
   // A lane's two pieces (c0, c1) of token t of K's or a query's head.
@@ -381,16 +421,21 @@ __global__ __launch_bounds__(256) void k_cache_store(StoreArgs a) {
     next[1].load(from + 8 * c1);
   };
   if (turned < rounds) fetch(turned);
-  for (int x = threadIdx.x; x < g.n * half; x += 256) {
-    const int t = x / half, j = x - t * half;
-    cs[t * half + j] = cos_sin((double)(g.pos + t) * a.freqs[j]);
-  }
+  if (wave < g.n)
+    for (int j = lane; j < half; j += 64) cs[wave * half + j] = cos_sin((double)(g.pos + wave) * a.freqs[j]);
   for (; round < kv; round += stride) {
     const int x = round % kTurns * 64 + lane;
     const int h = round / kTurns * kHeads + (kHeads > 1 ? x / (8 * kUnits) : 0);
     store_v<E, D, kPacked>(a, g, min(h, a.c.kv_heads - 1), kHeads > 1 ? x % (D / 2) : x, h < a.c.kv_heads);
   }
   __syncthreads();
+  // a lane has the same pieces of the same token in all rounds: its angles stay in registers
+  float2 w[8];
+  {
+    const int t = (turned % kTurns * 64 + lane) / kUnits % kGroup;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = turns && t < g.n ? cs[t * half + 8 * u + i] : make_float2(1.f, 0.f);
+  }
   // a round's loads are under way while the one before is turned and stored
   for (; turned < rounds; turned += stride) {
     const At at = place(turned);
@@ -399,7 +444,6 @@ __global__ __launch_bounds__(256) void k_cache_store(StoreArgs a) {
     next[1].values(q);
     if (turned + stride < rounds) fetch(turned + stride);
     if (at.live && turns) {
-      const float2* w = cs + at.t * half + 8 * u;
       if (apart) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) turn(p[i], q[i], w[i]);
@@ -609,7 +653,7 @@ __device__ __forceinline__ void read_v(const ReadArgs& a, const Part& g, int h, 
 template <typename E, int D, bool kPacked>
 __global__ __launch_bounds__(256) void k_cache_read(ReadArgs a, int run) {
   constexpr int kHeadsK = kPacked ? 512 / D : 1, kHeadsV = kPacked ? 4 : 1;  // that a wave takes at once
-  const Place p = find_place(a.c, a.N, a.offsets, a.first, kGroup * run);
+  const Place p = find_place<256>(a.c, a.N, a.offsets, a.first, kGroup * run);
   if (p.row < 0) return;
   const int H = a.c.kv_heads;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -634,10 +678,10 @@ __global__ __launch_bounds__(256) void k_cache_read(ReadArgs a, int run) {
 }
 
 // Workgroups that share a group's heads: as few as fill the card.
-unsigned split_of(int groups, int tasks) {
-  const int most = (tasks + 3) / 4;
-  const int want = (2048 + groups - 1) / groups;
-  return (unsigned)(want < most ? want : most);
+unsigned split_of(int groups, int tasks, int waves) {
+  const int most = (tasks + waves - 1) / waves;
+  const int want = 8192 / waves / groups;
+  return (unsigned)(want < 1 ? 1 : (want < most ? want : most));
 }
 
 }  // namespace
@@ -645,10 +689,10 @@ unsigned split_of(int groups, int tasks) {
 hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStream_t stream) {
   TimingScope t("cache_store", stream);
   const int per = a.c.head_dim == 64 ? 2 : 1;
-  const int tasks = 2 * ((a.c.kv_heads + per - 1) / per) + (a.heads + per - 1) / per;
+  const int tasks = (2 * ((a.c.kv_heads + per - 1) / per) + (a.heads + per - 1) / per) * (a.c.head_dim == 256 ? 2 : 1);
   const int active = a.N / kGroup + a.c.slots;
-  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(active, tasks));
-#define STORE(E, D, P) hipLaunchKernelGGL((k_cache_store<E, D, P>), grid, dim3(256), 0, stream, a)
+  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(active, tasks, kGroup));
+#define STORE(E, D, P) hipLaunchKernelGGL((k_cache_store<E, D, P>), grid, dim3(kStoreThreads), 0, stream, a)
 #define STORE_DIMS(E, P)                       \
   switch (a.c.head_dim) {                      \
     case 64: STORE(E, 64, P); break;           \
@@ -674,7 +718,7 @@ hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStrea
   int run = 1;  // finding the place is shared by more tokens where there are enough to fill the card
   while (2 * run * kGroup <= (1 << a.c.page_shift) && run < 8 && a.N / (2 * run * kGroup) >= 2048) run *= 2;
   const int size = run * kGroup, tasks = packed ? (a.c.kv_heads + 3) / 4 + (a.c.kv_heads * a.c.head_dim + 511) / 512 : 2 * a.c.kv_heads;
-  const dim3 grid((unsigned)(a.N / size + 3 * a.c.slots), split_of(a.N / size + a.c.slots, run * tasks));
+  const dim3 grid((unsigned)(a.N / size + 3 * a.c.slots), split_of(a.N / size + a.c.slots, run * tasks, 4));
 #define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a, run)
 #define READ_DIMS(E, P)                       \
   switch (a.c.head_dim) {                     \
