@@ -25,11 +25,19 @@
 //     keys x 4 elements, from where the conversion builds the matrix operand of 8 keys;
 //   scales [head][D / 32][token], so that 8 keys' scales are one 8-byte load.
 //
-// Work.  A workgroup takes an aligned group of 8 positions of a slot (what V stores side by
-// side) and shares its heads out over its waves and over blockIdx.y; a wave takes one head of K, V
-// or the queries at a time (two of 64 dimensions), 16 bytes per lane and load.  K and
-// queries: a lane holds two 8-element pieces of one token that rotate with each other.  V: a
-// lane holds two neighbouring elements of all 8 tokens, which is a transposition in registers.
+// Work.  A workgroup of 8 waves takes an aligned group of 8 positions of a slot (what V stores
+// side by side); blockIdx.y shares its heads out where there are few groups.  Each wave works out the angles
+// of one token, then the waves take one head of V, K or the queries at a time (two of 64
+// dimensions).  V: a lane holds two neighbouring elements of all 8 tokens, which is a
+// transposition in registers, and a group that is not full is stored in as few pieces as its
+// places make.  K and queries: a lane holds two 8-element pieces of one token that rotate with each
+// other, the same ones for all heads, so that its angles stay in registers (read from LDS for each head, their
+// bank conflicts took longer than the memory: 35 us against 26 for the chunk below); the next
+// head's pieces are on their way while one is turned.
+//
+// Bound by memory.  Alone on the card: 256 chunks of 17 tokens, 40 + 8 heads of 128 dimensions in bf16,
+// 107 MB: 23 us, 4.6 TB/s; two chunks of 2048 tokens into 4 bits 17 us, where 88 MB move.
+// Small calls are latency: 7 us from one launch to the next, as a launch of two dependent loads takes.
 #include "device_common.h"
 #include "kernels.h"
 
@@ -481,7 +489,10 @@ __device__ __forceinline__ u32x2 two(float, uint32_t code, float s) {
   const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(code, s, kSel);
   return __builtin_bit_cast(u32x2, b);
 }
-// kPairs pairs of elements, 16 bytes at a time where there are as many.
+// kPairs pairs of elements, 16 bytes at a time where there are as many.  The rows are written once and are as a
+// rule more than the caches hold: whole stretches of a wave's 16-byte stores pass the caches by (112 ->
+// 81 us for 97,000 tokens of 8 x 2 x 128 in bf16, 6.5 TB/s).  Where a lane's elements take more stores than one, the
+// caches have to put the lines together (binary32: 195 us against 364).
 template <typename P, int kPairs>
 __device__ __forceinline__ void put(void* to, const P (&x)[kPairs]) {
   constexpr int kBytes = kPairs * (int)sizeof(P);
@@ -490,7 +501,8 @@ __device__ __forceinline__ void put(void* to, const P (&x)[kPairs]) {
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) all.p[i] = x[i];
 #pragma unroll
-  for (int i = 0; i < kBytes / (int)sizeof(Word); ++i) static_cast<Word*>(to)[i] = all.w[i];
+  for (int i = 0; i < kBytes / (int)sizeof(Word); ++i) if constexpr (kBytes <= 16) __builtin_nontemporal_store(all.w[i], static_cast<Word*>(to) + i);
+    else static_cast<Word*>(to)[i] = all.w[i];
 }
 
 // A block of values that are all NaN.
@@ -620,8 +632,8 @@ __device__ __forceinline__ void read_k(const ReadArgs& a, const Part& g, int h, 
     if (t < g.t0 || t >= g.t1) continue;
 #pragma unroll
     for (int i = 0; i < 8 / kE; ++i)
-      *reinterpret_cast<u32x4*>(out + (int64_t)t * H * D + 8 * c + i * kE) =
-          g.page < 0 ? u32x4{0u, 0u, 0u, 0u} : w[r][i];
+      __builtin_nontemporal_store(g.page < 0 ? u32x4{0u, 0u, 0u, 0u} : w[r][i],
+                                  reinterpret_cast<u32x4*>(out + (int64_t)t * H * D + 8 * c + i * kE));
   }
 }
 
@@ -644,8 +656,8 @@ __device__ __forceinline__ void read_v(const ReadArgs& a, const Part& g, int h, 
 #pragma unroll
     for (int t = 0; t < kGroup; ++t)
       if (t >= g.t0 && t < g.t1)
-        *reinterpret_cast<Pair*>(out + (int64_t)t * H * D + 2 * i) =
-            g.page < 0 ? Pair{(E)0, (E)0} : Pair{x[0][t], x[1][t]};
+        __builtin_nontemporal_store(g.page < 0 ? Pair{(E)0, (E)0} : Pair{x[0][t], x[1][t]},
+                                    reinterpret_cast<Pair*>(out + (int64_t)t * H * D + 2 * i));
   }
 }
 
@@ -677,7 +689,9 @@ __global__ __launch_bounds__(256) void k_cache_read(ReadArgs a, int run) {
   }
 }
 
-// Workgroups that share a group's heads: as few as fill the card.
+// Workgroups that share a group's heads: as many as the card holds (256 x 32 waves) without a second turn.
+// Half and twice as many waves: 23.4 and 22.3 us against 23.4 (256 chunks of 17 tokens), 24.5 and 26.1
+// against 24.5 (two chunks of 2048 tokens stored and read).
 unsigned split_of(int groups, int tasks, int waves) {
   const int most = (tasks + waves - 1) / waves;
   const int want = 8192 / waves / groups;
@@ -715,9 +729,13 @@ hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStr
 
 hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStream_t stream) {
   TimingScope t("cache_read", stream);
-  int run = 1;  // finding the place is shared by more tokens where there are enough to fill the card
-  while (2 * run * kGroup <= (1 << a.c.page_shift) && run < 8 && a.N / (2 * run * kGroup) >= 2048) run *= 2;
-  const int size = run * kGroup, tasks = packed ? (a.c.kv_heads + 3) / 4 + (a.c.kv_heads * a.c.head_dim + 511) / 512 : 2 * a.c.kv_heads;
+  // Two groups to a workgroup (a page has 16 tokens or more) share finding their place where the
+  // tokens fill the card several times and the stores are 16 bytes per lane: 80.8 us against 84.4 for 97,000
+  // tokens of 8 heads of 128 dimensions in bf16.  The others lose by it: out of 4 bits in
+  // binary32 224 against 195, from bf16 178 against 160, from f32 355 against 336.
+  const int run = packed && bf16 && a.N >= 8192 ? 2 : 1;
+  const int size = run * kGroup;
+  const int tasks = packed ? (a.c.kv_heads + 3) / 4 + (a.c.kv_heads * a.c.head_dim + 511) / 512 : 2 * a.c.kv_heads;
   const dim3 grid((unsigned)(a.N / size + 3 * a.c.slots), split_of(a.N / size + a.c.slots, run * tasks, 4));
 #define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a, run)
 #define READ_DIMS(E, P)                       \
