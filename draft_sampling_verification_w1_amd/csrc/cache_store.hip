@@ -59,13 +59,13 @@ struct Place {
   int64_t pos;   // position of the first row
 };
 
-// The workgroup's group of `size` positions (blockIdx.x).  Slot s's groups are numbered from
-// offsets[s] / size + 3 s on, which leaves room for a group that is cut at either end.  Each thread
+// The workgroup's group (blockIdx.x).  Slot s's groups are numbered from
+// offsets[s] / 8 + 3 s on, which leaves room for a group that is cut at either end.  Each thread
 // looks at its slots' offsets and start position at once, so that finding the group is one round
 // trip, its page another.
 template <int kThreads>
 __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int32_t* offsets,
-                                            const int32_t* starts, int size) {
+                                            const int32_t* starts) {
   __shared__ int found[6];
   const int w = blockIdx.x;
   if (threadIdx.x == 0) found[0] = -1;
@@ -73,8 +73,8 @@ __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int
   for (int s = threadIdx.x; s < c.slots; s += kThreads) {
     const int o0 = min(max(offsets[s], 0), N), o1 = min(max(offsets[s + 1], o0), N);
     const int start = starts[s], held = c.t.held[s];
-    const int first = o0 / size + 3 * s;
-    if (o0 < o1 && first <= w && w < o1 / size + 3 * (s + 1)) {
+    const int first = o0 / kGroup + 3 * s;
+    if (o0 < o1 && first <= w && w < o1 / kGroup + 3 * (s + 1)) {
       found[0] = s;
       found[1] = o0;
       found[2] = o1;
@@ -88,13 +88,13 @@ __device__ __forceinline__ Place find_place(const CacheArgs& c, int N, const int
   const int s = found[0], o0 = found[1], o1 = found[2], start = found[4];
   if (s < 0) return g;
   const int64_t base = max(start, 0);
-  const int64_t first = (base / size + found[3]) * size;  // of the group
+  const int64_t first = (base / kGroup + found[3]) * kGroup;  // of the group
   g.e0 = first < base ? (int)(base - first) : 0;
   g.pos = first + g.e0;
   const int64_t row = o0 + (g.pos - base);
   if (row >= o1) return g;
   g.row = (int)row;
-  g.n = (int)min((int64_t)(size - g.e0), o1 - row);
+  g.n = (int)min((int64_t)(kGroup - g.e0), o1 - row);
   const int64_t j = g.pos >> c.page_shift;
   if (start >= 0 && j < min(found[5], c.max_pages)) {
     const int p = c.t.table[(int64_t)s * c.max_pages + j];
@@ -125,13 +125,18 @@ struct Eight {
     }
   }
 };
-// 8 elements rounded to nearest even.
+// 8 elements rounded to nearest even.  kPast: past the caches, for rows that are written whole by 16-byte
+// stores (queries of 256 chunks of 17 tokens, 35 MB: 33 us against 36; the attention behind reads them as
+// fast).  Binary32 takes two stores that the caches put together.
+template <bool kPast = false>
 __device__ __forceinline__ void store8(uint16_t* p, const float (&x)[8]) {
   bf16x8 b;
 #pragma unroll
   for (int i = 0; i < 8; ++i) b[i] = (__bf16)x[i];
-  *reinterpret_cast<bf16x8*>(p) = b;
+  if constexpr (kPast) __builtin_nontemporal_store(b, reinterpret_cast<bf16x8*>(p));
+  else *reinterpret_cast<bf16x8*>(p) = b;
 }
+template <bool kPast = false>
 __device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
@@ -390,7 +395,7 @@ __global__ __launch_bounds__(kStoreThreads, sizeof(E) == 2 ? 6 : 4) void k_cache
   constexpr int kTurns = kUnits > 8 ? kUnits / 8 : 1;      // or rounds of the wave for a head
   __shared__ float2 cs[kGroup * (D / 2)];
   __shared__ __align__(16) uint32_t tops[kGroup][64 / kUnits * (D / 8)];
-  const Place g = find_place<kStoreThreads>(a.c, a.N, a.offsets, a.c.t.lens, kGroup);
+  const Place g = find_place<kStoreThreads>(a.c, a.N, a.offsets, a.c.t.lens);
   if (g.row < 0) return;
   const int half = a.rot / 2;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -466,8 +471,8 @@ __global__ __launch_bounds__(kStoreThreads, sizeof(E) == 2 ? 6 : 4) void k_cache
     if (at.query) {
       if (at.live) {
         E* to = static_cast<E*>(a.q_out) + at.at;
-        store8(to + 8 * c0, p);
-        store8(to + 8 * c1, q);
+        store8<true>(to + 8 * c0, p);
+        store8<true>(to + 8 * c1, q);
       }
     } else {
       // lanes of one token of one head share D / 8 maxima
@@ -490,8 +495,8 @@ __device__ __forceinline__ u32x2 two(float, uint32_t code, float s) {
   return __builtin_bit_cast(u32x2, b);
 }
 // kPairs pairs of elements, 16 bytes at a time where there are as many.  The rows are written once and are as a
-// rule more than the caches hold: whole stretches of a wave's 16-byte stores pass the caches by (112 ->
-// 81 us for 97,000 tokens of 8 x 2 x 128 in bf16, 6.5 TB/s).  Where a lane's elements take more stores than one, the
+// rule more than the caches hold: whole stretches of a wave's 16-byte stores pass the caches by (104 ->
+// 84 us for 102,000 tokens of 8 x 2 x 128 in bf16).  Where a lane's elements take more stores than one, the
 // caches have to put the lines together (binary32: 195 us against 364).
 template <typename P, int kPairs>
 __device__ __forceinline__ void put(void* to, const P (&x)[kPairs]) {
@@ -661,24 +666,19 @@ __device__ __forceinline__ void read_v(const ReadArgs& a, const Part& g, int h, 
   }
 }
 
-// A workgroup takes `run` times 8 positions of a page.
+// A workgroup of 4 waves takes a group of 8 positions, whose place costs a round trip; two or four groups, so that
+// more tokens share it, take longer where the states don't fit in the caches (97 -> 103 -> 109 us
+// for 102,000 tokens).
 template <typename E, int D, bool kPacked>
-__global__ __launch_bounds__(256) void k_cache_read(ReadArgs a, int run) {
+__global__ __launch_bounds__(256) void k_cache_read(ReadArgs a) {
   constexpr int kHeadsK = kPacked ? 512 / D : 1, kHeadsV = kPacked ? 4 : 1;  // that a wave takes at once
-  const Place p = find_place<256>(a.c, a.N, a.offsets, a.first, kGroup * run);
+  const Place p = find_place<256>(a.c, a.N, a.offsets, a.first);
   if (p.row < 0) return;
+  const Part g = {p.row, p.e0, p.e0 + p.n, p.at, p.page};
   const int H = a.c.kv_heads;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ks = (H + kHeadsK - 1) / kHeadsK, tasks = ks + (H + kHeadsV - 1) / kHeadsV;
-  for (int x = (int)blockIdx.y * 4 + wave; x < run * tasks; x += 4 * (int)gridDim.y) {
-    const int sub = x / tasks, task = x - sub * tasks, base = sub * kGroup;
-    Part g;
-    g.t0 = max(p.e0 - base, 0);
-    g.t1 = min(p.e0 + p.n - base, kGroup);
-    if (g.t0 >= g.t1) continue;
-    g.row = p.row + max(base - p.e0, 0);
-    g.at = p.at + base;
-    g.page = p.page;
+  for (int task = (int)blockIdx.y * 4 + wave; task < tasks; task += 4 * (int)gridDim.y) {
     if (task < ks) {
       if constexpr (kPacked) read_k4<E, D>(a, g, task * kHeadsK, lane);
       else read_k<E, D>(a, g, task, lane);
@@ -704,8 +704,8 @@ hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStr
   TimingScope t("cache_store", stream);
   const int per = a.c.head_dim == 64 ? 2 : 1;
   const int tasks = (2 * ((a.c.kv_heads + per - 1) / per) + (a.heads + per - 1) / per) * (a.c.head_dim == 256 ? 2 : 1);
-  const int active = a.N / kGroup + a.c.slots;
-  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(active, tasks, kGroup));
+  const int groups = a.N / kGroup + a.c.slots;
+  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(groups, tasks, kGroup));
 #define STORE(E, D, P) hipLaunchKernelGGL((k_cache_store<E, D, P>), grid, dim3(kStoreThreads), 0, stream, a)
 #define STORE_DIMS(E, P)                       \
   switch (a.c.head_dim) {                      \
@@ -729,15 +729,10 @@ hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStr
 
 hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStream_t stream) {
   TimingScope t("cache_read", stream);
-  // Two groups to a workgroup (a page has 16 tokens or more) share finding their place where the
-  // tokens fill the card several times and the stores are 16 bytes per lane: 80.8 us against 84.4 for 97,000
-  // tokens of 8 heads of 128 dimensions in bf16.  The others lose by it: out of 4 bits in
-  // binary32 224 against 195, from bf16 178 against 160, from f32 355 against 336.
-  const int run = packed && bf16 && a.N >= 8192 ? 2 : 1;
-  const int size = run * kGroup;
+  const int groups = a.N / kGroup + a.c.slots;
   const int tasks = packed ? (a.c.kv_heads + 3) / 4 + (a.c.kv_heads * a.c.head_dim + 511) / 512 : 2 * a.c.kv_heads;
-  const dim3 grid((unsigned)(a.N / size + 3 * a.c.slots), split_of(a.N / size + a.c.slots, run * tasks, 4));
-#define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a, run)
+  const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(groups, tasks, 4));
+#define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a)
 #define READ_DIMS(E, P)                       \
   switch (a.c.head_dim) {                     \
     case 64: READ(E, 64, P); break;           \
