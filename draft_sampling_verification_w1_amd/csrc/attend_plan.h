@@ -112,11 +112,16 @@ PLAN_FN int64_t plan_span(int64_t total, int grid) {
 
 // Where a batch has few groups, of one row tile each, a group is cut by itself, into pieces of
 // about `target` units, so that no workgroup pays what a group costs beside its steps
-// twice.  total, groups: of the batch, groups > 0.  0: too many groups, the line is cut into spans.
+// twice.  A group of n units takes as long as its longest piece, then as long as the join of its pieces:
+// pieces are no shorter than the square root of n, the next power of two (a token over 30,000 of 32 heads
+// on 8: 24.7 -> 20.3 us, of 8 heads on one: 37 -> 21, 9 tokens over 4,000: 30 -> 20).
+// total, groups: of the batch, groups > 0.  0: too many groups, the line is cut into spans.
 PLAN_FN int64_t plan_target(int64_t total, int64_t groups, int grid) {
   if (2 * groups > grid) return 0;
   const int64_t rest = grid - groups, target = (total + rest - 1) / rest;  // pieces: total / target + groups at most
-  return target > kMinSpan ? target : kMinSpan;
+  int64_t least = kMinSpan;
+  while (least * least < total / groups) least *= 2;
+  return target > least ? target : least;
 }
 PLAN_FN int plan_pieces(int units, int64_t target) { return (int)((units + target - 1) / target); }
 // First unit of piece j of n.
