@@ -330,8 +330,8 @@ int check_own_type(const dspark_cache* c, const char* what, const char* other) {
   return DSPARK_OK;
 }
 
-bool overlap(const void* a, const void* b, size_t bytes) {
-  return (uintptr_t)a < (uintptr_t)b + bytes && (uintptr_t)b < (uintptr_t)a + bytes;
+bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  return (uintptr_t)a < (uintptr_t)b + b_bytes && (uintptr_t)b < (uintptr_t)a + a_bytes;
 }
 
 // One layer's pages of K or V.
@@ -384,7 +384,8 @@ int attend(const dspark_cache* c, const dspark_cache_tables* t, int layer, const
   const bool bf16 = dtype == DSPARK_BF16, packed = c->dtype == DSPARK_MXFP4;
   const AttendLayout L = attend_layout(c, bf16, N, heads, max_chunk);
   if (int e = check_ws_bytes(L.bytes, ws, ws_bytes)) return e;
-  if (overlap(q, out, (size_t)N * heads * c->head_dim * (bf16 ? 2 : 4)))
+  const size_t q_bytes = (size_t)N * heads * c->head_dim * (bf16 ? 2 : 4);
+  if (overlap(q, q_bytes, out, q_bytes))
     return fail(DSPARK_ERR_ARG, "%s: q and out must not overlap", what);
   AttendArgs a = {};
   a.c = cache_args(c, t);
@@ -1171,8 +1172,12 @@ __attribute__((visibility("default"))) int dspark_cache_store(
     if (!aligned16(q) || !aligned16(q_out))
       return fail(DSPARK_ERR_ARG, "cache_store: q and q_out must be 16-byte aligned");
     const size_t bytes = (size_t)N * heads * c->head_dim * (dtype == DSPARK_BF16 ? 2 : 4);
-    if (q != q_out && overlap(q, q_out, bytes))
+    if (q != q_out && overlap(q, bytes, q_out, bytes))
       return fail(DSPARK_ERR_ARG, "cache_store: q_out must be q or not overlap it");
+    // other workgroups' queries may be written before the keys and values are read
+    const size_t rows = (size_t)N * c->kv_heads * c->head_dim * (dtype == DSPARK_BF16 ? 2 : 4);
+    if (overlap(q_out, bytes, k, rows) || overlap(q_out, bytes, v, rows))
+      return fail(DSPARK_ERR_ARG, "cache_store: q_out must not overlap k or v");
   }
   StoreArgs a = {};
   a.c = cache_args(c, t);
@@ -1206,7 +1211,7 @@ __attribute__((visibility("default"))) int dspark_cache_read(
   if (!aligned16(K) || !aligned16(V) || !aligned16(k) || !aligned16(v))
     return fail(DSPARK_ERR_ARG, "cache_read: K, V, k and v must be 16-byte aligned");
   const size_t bytes = (size_t)N * c->kv_heads * c->head_dim * (dtype == DSPARK_BF16 ? 2 : 4);
-  if (overlap(k, v, bytes)) return fail(DSPARK_ERR_ARG, "cache_read: k and v must not overlap");
+  if (overlap(k, bytes, v, bytes)) return fail(DSPARK_ERR_ARG, "cache_read: k and v must not overlap");
   ReadArgs a = {};
   a.c = cache_args(c, t);
   a.N = N;

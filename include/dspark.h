@@ -430,8 +430,8 @@ typedef struct {
  * queries rotated by their positions lens[s] + i - offsets[s] (rot; NULL: no rotation),
  * keys and values converted to the cache's type.  dtype: of k, v, q and q_out; the cache's own, or
  * DSPARK_F32 or DSPARK_BF16 for a 4-bit cache.  heads: query heads, a multiple of kv_heads,
- * q [N, heads, head_dim] to q_out (which may be q, and must not overlap it otherwise); 0: no
- * queries (q and q_out are not read).  Queries need rot.  Rows behind offsets[slots] of q_out are left
+ * q [N, heads, head_dim] to q_out (which may be q, and must not overlap it otherwise, nor k or
+ * v); 0: no queries (q and q_out are not read).  Queries need rot.  Rows behind offsets[slots] of q_out are left
  * as they were; queries of tokens without a page are rotated like the others.
  * 4 bits: rotated keys (binary32) and values are divided by the block's scale, the smallest power of two
  * within 2^-120 .. 2^125 of which the block's largest magnitude is at most 7, and rounded to the
@@ -475,7 +475,8 @@ int dspark_attend(const dspark_cache* c, const dspark_cache_tables* t, int32_t l
 
 /* dspark_attend over a 4-bit cache: keys and values are what the codes stand for, exactly;
  * dtype of q and out: DSPARK_BF16 (products of bf16 operands, weights rounded to bf16) or
- * DSPARK_F32.  A block whose scale byte is 255 must not be seen.  Everything else as in dspark_attend. */
+ * DSPARK_F32.  A block whose scale byte is 255 is not finite: no token of the chunk may see it.
+ * Everything else as in dspark_attend. */
 int dspark_attend4(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
                    const void* K, const void* V, int32_t N, int32_t heads, int32_t dtype,
                    const void* q, const int32_t* offsets, float scale, int32_t max_chunk, void* out,

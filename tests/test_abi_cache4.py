@@ -90,6 +90,20 @@ def test_store_arguments(D, pool):  # noqa: F811
 
 
 @pytest.mark.parametrize("pool", [1, 2])
+@pytest.mark.parametrize("name", ["k", "v"])
+def test_turned_queries_beside_keys_and_values(D, pool, name):  # noqa: F811
+    """Turned queries [40, 8, 128] over keys or values [40, 2, 128] are refused: from the last byte of one to the
+    first of the other."""
+    L = D.lib()
+    c, t = ctypes.byref(cache(D, dtype=pool)), ctypes.byref(tables(D))
+    rows, queries = 40 * 2 * 128 * 2, 40 * 8 * 128 * 2
+    out = P + (1 << 24)
+    for at in (out, out + queries - 16, out - rows + 16):
+        kv = {"k": P, "v": P, name: at}
+        refused(D, ERR_ARG, L.dspark_cache_store(c, t, 0, P, P, 40, 1, kv["k"], kv["v"], P, rotation(D), 8, P, out, None))
+
+
+@pytest.mark.parametrize("pool", [1, 2])
 def test_read_arguments(D, pool):  # noqa: F811
     L = D.lib()
     c, t = ctypes.byref(cache(D, dtype=pool)), ctypes.byref(tables(D))
