@@ -304,8 +304,10 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       }
     }
   };
-  // what a page holds behind the last token seen, or where there is no page, counts as zeros
-  auto clear_v = [&](int t, int pa, int pb, RawV<D>& v) {
+  // What a page holds behind the last token seen, or where there is no page, counts as zeros.  Blocks without
+  // a value (scale byte 255) do too, so that the weight 0 of a row that doesn't see the token meets no NaN;
+  // true if there are any: bit 8 r + 7 of none[u] is set if one of key r's is.
+  auto clear_v = [&](int t, int pa, int pb, RawV<D>& v, uint32_t (&none)[2]) {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int key = kF32 ? 16 * u + 4 * quad : 8 * quad + 4 * u;
@@ -317,7 +319,22 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
         v.w[g][2 + u] &= mask;
       }
       v.scale[u] = (v.scale[u] & mask) | (0x7F7F7F7Fu & ~mask);
+      none[u] = v.scale[u] & ((v.scale[u] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
     }
+    if (__ballot((none[0] | none[1]) != 0u) == 0) return false;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t mask = ~((none[u] >> 7) * 255u);
+#pragma unroll
+      for (int g = 0; g < D / 64; ++g) {
+        v.w[g][u] &= mask;
+        v.w[g][2 + u] &= mask;
+      }
+      v.scale[u] = (v.scale[u] & mask) | (0x7F7F7F7Fu & ~mask);
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) none[u] |= (uint32_t)__shfl_xor((int)none[u], off, 64);
+    }
+    return true;
   };
   // f32: operands of a 16-key block: lane (n, quad), operand s: elements quad D / 4 + 4 s ..
   auto k_operands = [&](const RawK<D>& r, Chunk (&k)[kSteps]) {
@@ -491,7 +508,17 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     load_k(ahead, pa[j], pb[j], k[j]);
     if (__builtin_expect(partial, 0)) {
       asm volatile("");  // a branch, not selections in every step
-      clear_v(t, kBuf > 1 && t >= t1 ? -1 : ma, kBuf > 1 && t >= t1 ? -1 : mb, v[j]);
+      uint32_t none[2];
+      if (clear_v(t, kBuf > 1 && t >= t1 ? -1 : ma, kBuf > 1 && t >= t1 ? -1 : mb, v[j], none)) {
+        // rows that see the token are NaN by its score (as bits: the compiler takes numbers for granted)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              s[i][u][r] = __uint_as_float(none[u] >> (8 * r + 7) & 1u ? 0x7FC00000u : __float_as_uint(s[i][u][r]));
+      }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         // of this step's keys

@@ -475,8 +475,9 @@ int dspark_attend(const dspark_cache* c, const dspark_cache_tables* t, int32_t l
 
 /* dspark_attend over a 4-bit cache: keys and values are what the codes stand for, exactly;
  * dtype of q and out: DSPARK_BF16 (products of bf16 operands, weights rounded to bf16) or
- * DSPARK_F32.  A block whose scale byte is 255 is not finite: no token of the chunk may see it.
- * Everything else as in dspark_attend. */
+ * DSPARK_F32.  Where a block has the scale byte 255, rows that see its token are NaN (of a
+ * value's block: in its 32 elements, the others may be NaN, too), the others don't depend on
+ * it.  Everything else as in dspark_attend. */
 int dspark_attend4(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
                    const void* K, const void* V, int32_t N, int32_t heads, int32_t dtype,
                    const void* q, const int32_t* offsets, float scale, int32_t max_chunk, void* out,
