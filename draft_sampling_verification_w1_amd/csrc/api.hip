@@ -348,14 +348,16 @@ struct AttendLayout {
 AttendLayout attend_layout(const dspark_cache* c, bool bf16, int N, int heads, int max_chunk) {
   AttendLayout L = {};
   const bool packed = c->dtype == DSPARK_MXFP4;
-  const auto grid_of = packed ? attend4_grid : attend_grid;
+  const auto grid_of = [&](int rows) {
+    return packed ? attend4_grid(c->head_dim, rows) : attend_grid(bf16, c->head_dim, rows);
+  };
   const int longest = max_chunk < N ? max_chunk : N;
   L.rows = (packed ? attend4_rows : attend_rows)(bf16, c->head_dim, heads / c->kv_heads, longest);
-  L.grid = grid_of(bf16, c->head_dim, L.rows);
+  L.grid = grid_of(L.rows);
   // sized for any tile, whatever chunk a call names
   size_t records = 0, most = 0;
   for (int rows = 16; rows <= (packed ? attend4_max_rows : attend_max_rows)(bf16, c->head_dim); rows += 16) {
-    const size_t g = grid_of(bf16, c->head_dim, rows);
+    const size_t g = grid_of(rows);
     const size_t n = 2 * g * rows;
     records = records > n ? records : n;
     most = most > g ? most : g;

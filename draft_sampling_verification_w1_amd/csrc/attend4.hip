@@ -9,7 +9,27 @@
 //   V: a lane's 16 bytes are 8 keys x 4 elements.  A conversion takes two neighbouring
 //     elements of one key with that key's scale to two bf16 (exact: two significant bits);
 //     a byte permutation pairs the keys up as the matrix operand wants them.
-// Every wave loads and converts its own operands: no LDS and no barrier in the loop.
+// Every wave loads and converts its own codes, straight from the pages; the queries lie in LDS as
+// operands; the loop over the keys has no barrier.
+//
+// What bounds it.  A step of 32 keys by 48 rows of 128 dimensions is 12 scaled products of 32 cycles
+// (queries in two parts) and 24 of 16, beside 64 conversions and permutations, 48 exponentials and as many
+// roundings at 4 to 9 cycles each: both units take about as long, and one wave hardly runs them side by
+// side.  Two waves per SIMD do, where one is kept at the matrix products (matrix_first).  256 slots
+// of 17 tokens: the matrix units are busy 39 % of the time, the vector unit 51 %.
+//
+// Measured (32 heads on 8, 128 dimensions, bf16), with the join:
+//   1 token over 30,000: 20 us (attention 14, join 5), 1.6 TB/s: what a launch, the plan, the page
+//     ids and the queries take before the first step;
+//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 44 us, 1.2 TB/s;
+//   256 slots, up to 4,096 cached, 17 new tokens: 300 us, 2.6 TB/s of codes and scales, 610 TFLOP/s (whole
+//     elements: 600 us);
+//   256 slots, up to 4,096 cached, 1 new token: 140 us;
+//   2 prompts, 2,048 tokens behind up to 8,192: 455 us, 1,000 TFLOP/s (whole elements: 500 us).
+// Tried without gain: one wave per SIMD on 80 rows (492 us for the 324 of then), values converted one step late,
+// two waves to a workgroup (343), the next group's pages and queries loaded before a group's
+// join (355), values converted once into LDS for 8 waves (461 for 460), tiles of 192, 96 and 256 rows for
+// prompts (469, 462, 474).
 #include "attend_common.h"
 
 namespace dspark {
@@ -137,9 +157,8 @@ __host__ __device__ constexpr int lds_pieces() {
 
 // Key steps [first, end) of a group; `rec`: the record that takes the sums of a group
 // that is cut, or -1.  RW x KW waves: RW row groups of NQ 16-row blocks each, KW parts of the
-// key range.  kBuf: steps whose codes are on their way or in registers.  kHalf: pages of 16 tokens, two
-// of which a step spans.
-template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
+// key range.  kHalf: pages of 16 tokens, two of which a step spans.
+template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
 __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& it, int first,
                                               int end, int64_t rec, float* sh_ml, int* sh_limit,
                                               uint32_t* sh_scale, u32x4* sh) {
@@ -372,19 +391,16 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
   };
 
-  // Loads are started without a condition (behind the end the last step's again), so that
-  // the number on their way is known where one is waited for.
-  RawK<D> k[kBuf][2];
-  RawV<D> v[kBuf];
-  int pa[kBuf], pb[kBuf];
+  // The next step's codes are on their way from where this step's are used last (two steps ahead takes
+  // registers and gains nothing: 3 % behind for 48 and 96 rows).  They are started without a condition (behind
+  // the end the last step's again), so that the number on their way is known where one is waited for.
+  RawK<D> k[2];
+  RawV<D> v;
+  int pa, pb;
   if (t0 < t1) {
-#pragma unroll
-    for (int j = 0; j < kBuf; ++j) {
-      const int t = min(t0 + j, t1 - 1);
-      pages_of(t, pa[j], pb[j]);
-      load_k(t, pa[j], pb[j], k[j]);
-      load_v(t, pa[j], pb[j], v[j]);
-    }
+    pages_of(t0, pa, pb);
+    load_k(t0, pa, pb, k);
+    load_v(t0, pa, pb, v);
   }
 #pragma unroll
   for (int x = 0; x < kMine; ++x)
@@ -459,13 +475,10 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
     far = __ballot(far) != 0;
   };
-  for (int tb = t0; tb < t1; tb += kBuf) {
-#pragma unroll
-   for (int j = 0; j < kBuf; ++j) {
-    const int t = tb + j, ahead = min(t + kBuf, t1 - 1);
-    const int ma = pa[j], mb = pb[j];
-    // (behind the part's last step: no key at all)
-    const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0 || (kBuf > 1 && t >= t1);
+  for (int t = t0; t < t1; ++t) {
+    const int ahead = min(t + 1, t1 - 1);
+    const int ma = pa, mb = pb;
+    const bool partial = (t + 1) * kKeys > common || ma < 0 || mb < 0;
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -473,8 +486,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     matrix_first();
     if constexpr (kF32) {
       Chunk ko[2][kSteps];
-      k_operands(k[j][0], ko[0]);
-      k_operands(k[j][1], ko[1]);
+      k_operands(k[0], ko[0]);
+      k_operands(k[1], ko[1]);
 #pragma unroll
       for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -493,9 +506,9 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
           const i32x8 qo = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t* w = k[j][u].w + 4 * b;
+            const uint32_t* w = k[u].w + 4 * b;
             const i32x8 ko = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
-            const int ks = (int)(k[j][u].scale[b] >> (8 * (n & 3)));  // its low byte counts
+            const int ks = (int)(k[u].scale[b] >> (8 * (n & 3)));  // its low byte counts
             if (D != 64 && (c & 1))
               s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 1, (int)q_scale[i]);
             else
@@ -504,12 +517,12 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
         }
     }
     matrix_done();
-    pages_of(ahead, pa[j], pb[j]);
-    load_k(ahead, pa[j], pb[j], k[j]);
+    pages_of(ahead, pa, pb);
+    load_k(ahead, pa, pb, k);
     if (__builtin_expect(partial, 0)) {
       asm volatile("");  // a branch, not selections in every step
       uint32_t none[2];
-      if (clear_v(t, kBuf > 1 && t >= t1 ? -1 : ma, kBuf > 1 && t >= t1 ? -1 : mb, v[j], none)) {
+      if (clear_v(t, ma, mb, v, none)) {
         // rows that see the token are NaN by its score (as bits: the compiler takes numbers for granted)
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
@@ -522,7 +535,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
         // of this step's keys
-        const int left = kBuf > 1 && t >= t1 ? 0 : sh_limit[wrow + 16 * i + n] - t * kKeys;
+        const int left = sh_limit[wrow + 16 * i + n] - t * kKeys;
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -548,13 +561,13 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     matrix_first();
     float vs[8];
 #pragma unroll
-    for (int r = 0; r < 8; ++r) vs[r] = scale_of(v[j].scale[r >> 2] >> (8 * (r & 3)) & 255u);
+    for (int r = 0; r < 8; ++r) vs[r] = scale_of(v.scale[r >> 2] >> (8 * (r & 3)) & 255u);
 #pragma unroll
     for (int g = 0; g < D / 64; ++g)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         Chunk lo[kVC], hi[kVC];
-        v_operands(v[j], vs, g, h, lo, hi);
+        v_operands(v, vs, g, h, lo, hi);
 #pragma unroll
         for (int u = 0; u < kVC; ++u)
 #pragma unroll
@@ -564,8 +577,7 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
           }
       }
     matrix_done();
-    load_v(ahead, pa[j], pb[j], v[j]);
-   }
+    load_v(ahead, pa, pb, v);
   }
 
   // ---- the sums of the key parts joined: the other parts leave theirs in LDS in the
@@ -755,7 +767,7 @@ __device__ __forceinline__ void find_piece(const AttendArgs& a, int rows, const 
   j = left - g.head * n;
 }
 
-template <typename E, int D, int NQ, int RW, int KW, int kBuf, bool kHalf>
+template <typename E, int D, int NQ, int RW, int KW, bool kHalf>
 __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) void k_attend4(AttendArgs a) {
   constexpr int kRows = 16 * NQ * RW;
   __shared__ Plan4 plan;
@@ -813,7 +825,7 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
       cut.first = (int)rec;
       cut.last = last;
     }
-    attend4_steps<E, D, NQ, RW, KW, kBuf, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_scale, sh);
+    attend4_steps<E, D, NQ, RW, KW, kHalf>(a, g, first, end, rec, sh_ml, sh_limit, sh_scale, sh);
   }
   if (threadIdx.x == 0) a.cuts[1 + span] = cut;
 }
@@ -887,23 +899,23 @@ void start4_join(int rows, const AttendArgs& a, hipStream_t stream) {
   }
 }
 
-template <typename E, int D, int NQ, int RW, int KW, int kBuf>
+template <typename E, int D, int NQ, int RW, int KW>
 void start4(const AttendArgs& a, hipStream_t stream) {
   const dim3 grid(a.grid), block(64 * RW * KW);
-  if (a.c.page_shift == 4) hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, kBuf, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, kBuf, false>), grid, block, 0, stream, a);
+  if (a.c.page_shift == 4) hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((k_attend4<E, D, NQ, RW, KW, false>), grid, block, 0, stream, a);
 }
 
-// Tiles in use: rows (16 NQ RW), NQ, RW, KW, steps on their way.
-#define ATTEND4_TILES(X) X(16, 1, 1, 4, 2) X(32, 2, 1, 4, 1) X(48, 3, 1, 4, 2) X(64, 2, 2, 2, 2) X(96, 3, 2, 2, 2) \
-  X(128, 2, 4, 2, 1) X(192, 3, 4, 2, 1) X(256, 2, 8, 1, 2) X(384, 3, 8, 1, 2)
-#define ATTEND4_TILES_256(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1) X(64, 1, 4, 2, 1) X(128, 1, 8, 1, 1)
-#define ATTEND4_TILES_F32(X) X(16, 1, 1, 4, 1) X(32, 1, 2, 2, 1)
+// Tiles in use: rows (16 NQ RW), NQ, RW, KW.
+#define ATTEND4_TILES(X) X(16, 1, 1, 4) X(32, 2, 1, 4) X(48, 3, 1, 4) X(64, 2, 2, 2) X(96, 3, 2, 2) \
+  X(128, 2, 4, 2) X(192, 3, 4, 2) X(256, 2, 8, 1) X(384, 3, 8, 1)
+#define ATTEND4_TILES_256(X) X(16, 1, 1, 4) X(32, 1, 2, 2) X(64, 1, 4, 2) X(128, 1, 8, 1)
+#define ATTEND4_TILES_F32(X) X(16, 1, 1, 4) X(32, 1, 2, 2)
 
 template <typename E, int D>
 bool start4_rows(int rows, const AttendArgs& a, hipStream_t stream) {
-#define ATTEND4_CASE(ROWS, NQ, RW, KW, BUF) \
-  case ROWS: start4<E, D, NQ, RW, KW, BUF>(a, stream); return true;
+#define ATTEND4_CASE(ROWS, NQ, RW, KW) \
+  case ROWS: start4<E, D, NQ, RW, KW>(a, stream); return true;
   if constexpr (sizeof(E) == 4) {
     switch (rows) { ATTEND4_TILES_F32(ATTEND4_CASE) }
   } else if constexpr (D == 256) {
@@ -926,7 +938,7 @@ int attend4_rows(bool bf16, int head_dim, int group, int max_chunk) {
   const int64_t rows = (int64_t)max_chunk * group;
   const int64_t tiles = (rows + most - 1) / most;
   const int need = (int)((rows + tiles - 1) / tiles);
-#define ATTEND4_SIZE(ROWS, NQ, RW, KW, BUF) \
+#define ATTEND4_SIZE(ROWS, NQ, RW, KW) \
   if (ROWS >= need) return ROWS;
   if (!bf16) {
     ATTEND4_TILES_F32(ATTEND4_SIZE)
@@ -940,14 +952,17 @@ int attend4_rows(bool bf16, int head_dim, int group, int max_chunk) {
 }
 
 // What a group costs beside its steps, in steps, where spans hold several groups (a span that
-// holds part of one group pays it whatever its steps are).
+// holds part of one group pays it whatever its steps are).  256 slots of 17 tokens by the charge: 0 321
+// us, 8 306, 14 299, 20 298, 30 300.
 int attend4_extra(int groups, int grid) {
   return groups >= 2 * grid ? 20 : 0;
 }
 
-// Workgroups, and spans at most: what is resident at once.
-int attend4_grid(bool bf16, int head_dim, int rows) {
-  return bf16 && head_dim <= 128 && rows <= 96 ? 512 : 256;
+// Workgroups, and spans at most: what is resident at once, two waves per SIMD.  Tiles of 16 rows could have
+// four, but their groups are then cut into more pieces (256 slots, one token: 1024 workgroups 170
+// us, 512 140, 256 184).
+int attend4_grid(int head_dim, int rows) {
+  return head_dim <= 128 && rows <= 96 ? 512 : 256;
 }
 
 hipError_t launch_attend4(bool bf16, int rows, const AttendArgs& a, hipStream_t stream) {

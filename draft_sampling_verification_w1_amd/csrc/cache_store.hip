@@ -387,6 +387,7 @@ __device__ __forceinline__ void store_v(const StoreArgs& a, const Place& g, int 
 }
 
 constexpr int kStoreThreads = 64 * kGroup;  // a wave for each token's angles
+// (registers: bf16 for three workgroups on a CU, 24.4 us against 27.4 for four with two chunks of 2048 tokens)
 
 template <typename E, int D, bool kPacked>
 __global__ __launch_bounds__(kStoreThreads, sizeof(E) == 2 ? 6 : 4) void k_cache_store(StoreArgs a) {

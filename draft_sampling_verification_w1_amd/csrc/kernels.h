@@ -381,7 +381,7 @@ int attend_max_rows(bool bf16, int head_dim);
 int attend_rows(bool bf16, int head_dim, int group, int max_chunk);
 hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
 // The same over a 4-bit cache (attend4.hip); bf16: the queries' type.
-int attend4_grid(bool bf16, int head_dim, int rows);
+int attend4_grid(int head_dim, int rows);
 int attend4_max_rows(bool bf16, int head_dim);
 int attend4_rows(bool bf16, int head_dim, int group, int max_chunk);
 int attend4_extra(int groups, int grid);
