@@ -13,10 +13,10 @@
 // operands; the loop over the keys has no barrier.
 //
 // What bounds it.  A step of 32 keys by 48 rows of 128 dimensions is 12 scaled products of 32 cycles
-// (queries in two parts) and 24 of 16, beside 64 conversions and permutations, 48 exponentials and as many
+// (queries in two parts) and 24 of 16, beside 64 conversions and permutations, 24 exponentials and as many
 // roundings at 4 to 9 cycles each: both units take about as long, and one wave hardly runs them side by
 // side.  Two waves per SIMD do, where one is kept at the matrix products (matrix_first).  256 slots
-// of 17 tokens: the matrix units are busy 39 % of the time, the vector unit 51 %.
+// of 17 tokens: the matrix units are busy 38 % of the time, the vector units 59 %.
 //
 // Measured (32 heads on 8, 128 dimensions, bf16), with the join:
 //   1 token over 30,000: 20 us (attention 14, join 5), 1.6 TB/s: what a launch, the plan, the page

@@ -35,8 +35,8 @@
 // bank conflicts took longer than the memory: 35 us against 26 for the chunk below); the next
 // head's pieces are on their way while one is turned.
 //
-// Bound by memory.  Alone on the card: 256 chunks of 17 tokens, 40 + 8 heads of 128 dimensions in bf16,
-// 107 MB: 23 us, 4.6 TB/s; two chunks of 2048 tokens into 4 bits 17 us, where 88 MB move.
+// Bound by memory.  Alone on the card: 256 chunks of 17 tokens, 32 heads on 8 of 128 dimensions in bf16,
+// 107 MB: 23 us, 4.6 TB/s (33 from memory that no cache holds); two chunks of 2048 tokens into 4 bits 17 us, where 88 MB move.
 // Small calls are latency: 7 us from one launch to the next, as a launch of two dependent loads takes.
 #include "device_common.h"
 #include "kernels.h"
