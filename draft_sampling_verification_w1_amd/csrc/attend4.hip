@@ -663,7 +663,7 @@ struct Shape4 {
 // The line of work (attend_common.h), or, where it has few groups, their pieces one after the other
 // (attend_plan.h, plan_target): before[] and spans then count pieces.
 struct Plan4 : Plan {
-  int64_t target;  // units of a piece, 0: the line is cut into spans
+  int target;  // units of a piece, 0: the line is cut into spans
   int64_t totals[kPlanWaves][2];
   int near[kPlanThreads][3];  // a slot's token rows and length, if there are no more slots
 };
@@ -680,7 +680,7 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.c.slots + kPlanThreads - 1) / kPlanThreads;
   const int s0 = tid < kPlanThreads ? tid * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
-  const bool few = (int64_t)a.c.slots * a.c.kv_heads * 2 <= a.grid;  // at most, as far as slots tell
+  const bool few = plan_few((int64_t)a.c.slots * a.c.kv_heads, a.grid);  // as far as slots tell
   int64_t x = 0, groups = 0, steps = 0;
   int long_chunk = 0, mine = 0;
   for (int s = s0; s < s1; ++s) {
@@ -703,6 +703,8 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
     plan.per = per;
     plan.target = 0;
   }
+  int target[kTargets];
+  bool whole = false;
   if (few) {  // (then there are no more slots than threads)
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -713,17 +715,21 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
       plan.totals[wave][0] = steps;
       plan.totals[wave][1] = groups;
     }
-    const bool whole = !__syncthreads_or(long_chunk);
+    whole = !__syncthreads_or(long_chunk);
     steps = groups = 0;
 #pragma unroll
     for (int w = 0; w < kPlanWaves; ++w) {
       steps += plan.totals[w][0];
       groups += plan.totals[w][1];
     }
-    if (whole && groups > 0) {
-      const int64_t target = plan_target(steps, groups, a.grid);
-      x = mine > 0 ? (int64_t)plan_pieces(mine, target) * a.c.kv_heads : 0;
-      if (tid == 0) plan.target = target;
+    whole = whole && groups > 0;
+    if (whole) {
+      // pieces by each target, summed up side by side in 16 bits each (768 of a batch at most)
+      plan_targets(steps, (int)groups, a.grid, target);
+      x = 0;
+#pragma unroll
+      for (int k = 0; k < kTargets; ++k)
+        x |= (int64_t)(plan_pieces(mine, target[k]) * a.c.kv_heads) << (16 * k);
     }
   }
 #pragma unroll
@@ -738,6 +744,18 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
   for (int w = 0; w < kPlanWaves; ++w) {
     if (w < wave) x += plan.sum[w];
     total += plan.sum[w];
+  }
+  if (whole) {
+    int best = kTargets - 1, span_units = target[kTargets - 1];
+#pragma unroll
+    for (int k = kTargets - 2; k >= 0; --k)
+      if ((int)(total >> (16 * k) & 0xFFFF) <= a.grid) {
+        best = k;
+        span_units = target[k];
+      }
+    x = x >> (16 * best) & 0xFFFF;
+    total = total >> (16 * best) & 0xFFFF;
+    if (tid == 0) plan.target = span_units;
   }
   if (tid < kPlanThreads) plan.before[tid + 1] = x;
   if (tid == 0) {

@@ -25,7 +25,7 @@ int main() {
     std::vector<SlotWork> work(slots);
     int row = 0;
     int64_t groups = 0, steps = 0;
-    bool whole = (int64_t)slots * heads * 2 <= grid;
+    bool whole = plan_few((int64_t)slots * heads, grid);
     for (int s = 0; s < slots; ++s) {
       int cached, chunk;
       if (scanf("%d %d", &cached, &chunk) != 2) return 1;
@@ -37,7 +37,15 @@ int main() {
         whole &= work[s].tiles == 1;
       }
     }
-    const int64_t target = whole && groups ? plan_target(steps, groups, grid) : 0;
+    int target = 0, targets[kTargets];
+    if (whole && groups) plan_targets(steps, (int)groups, grid, targets);
+    for (int k = kTargets - 1; whole && groups && k >= 0; --k) {
+      int64_t pieces = 0;
+      for (const SlotWork& w : work)
+        if (w.tiles) pieces += (int64_t)heads * plan_pieces(tile_units(w, group, rows, 0), targets[k]);
+      if (pieces > 768) return 2;  // the kernel's sums take 16 bits
+      if (k == kTargets - 1 || pieces <= grid) target = targets[k];
+    }
     std::vector<int64_t> first(slots + 1, 0);
     for (int s = 0; s < slots; ++s) {
       const SlotWork& w = work[s];
