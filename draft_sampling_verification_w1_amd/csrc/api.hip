@@ -1207,7 +1207,8 @@ __attribute__((visibility("default"))) int dspark_cache_read(
   if (int e = check_cache(c)) return e;
   if (int e = check_tables(t)) return e;
   if (int e = check_rows(c, dtype, "cache_read")) return e;
-  if (int e = check_tokens(c, layer, N, c->kv_heads, "cache_read")) return e;
+  if (int e = check_tokens(c, layer, N ? N : 1, c->kv_heads, "cache_read")) return e;
+  if (N == 0) return ok();  // no slot has a token: no rows
   if (!K || !V || !k || !v || !offsets)
     return fail(DSPARK_ERR_ARG, "cache_read: tensor pointers must be non-NULL");
   if (!aligned16(K) || !aligned16(V) || !aligned16(k) || !aligned16(v))

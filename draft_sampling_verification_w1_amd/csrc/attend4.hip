@@ -21,7 +21,7 @@
 // Measured (32 heads on 8, 128 dimensions, bf16), with the join:
 //   1 token over 30,000: 20 us (attention 14, join 5), 1.6 TB/s: what a launch, the plan, the page
 //     ids and the queries take before the first step;
-//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 44 us, 1.2 TB/s;
+//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 40 us, 1.3 TB/s;
 //   256 slots, up to 4,096 cached, 17 new tokens: 300 us, 2.6 TB/s of codes and scales, 610 TFLOP/s (whole
 //     elements: 600 us);
 //   256 slots, up to 4,096 cached, 1 new token: 140 us;

@@ -447,7 +447,8 @@ int dspark_cache_store(const dspark_cache* c, const dspark_cache_tables* t, int3
  * behind the committed tokens).  dtype: as in dspark_cache_store (what 4 bits stand for is a bf16
  * value: no rounding).  Positions that no page of the slot holds are 0, and all of a slot whose
  * first is negative; rows behind offsets[slots] are left as they were.  Positions that a page holds and no
- * token was written to have any value.  first [slots] int32.  k and v must not overlap. */
+ * token was written to have any value.  first [slots] int32.  k and v must not overlap.
+ * 0 <= N <= 2^22 (0: no rows, no tensor is looked at). */
 int dspark_cache_read(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
                       const void* K, const void* V, int32_t N, int32_t dtype, const int32_t* offsets,
                       const int32_t* first, void* k, void* v, void* stream);

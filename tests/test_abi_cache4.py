@@ -114,8 +114,10 @@ def test_read_arguments(D, pool):  # noqa: F811
 
     for layer in (-1, 2):
         refused(D, ERR_RANGE, read(layer=layer))
-    for n in (0, -5, 2 ** 22 + 1):
+    for n in (-5, 2 ** 22 + 1):
         refused(D, ERR_SHAPE, read(N=n))
+    assert read(N=0, off=None, k=None, v=None) == 0  # no rows: nothing to do
+    refused(D, ERR_RANGE, read(N=0, layer=2))
     for name in ("K", "V", "k", "v"):
         for value in (None, P + 8):
             refused(D, ERR_ARG, read(**{name: value}))

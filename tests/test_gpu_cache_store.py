@@ -294,6 +294,15 @@ def test_absent_pages(C):
     assert host(k)[:16].any() and not host(k)[16:].any()
 
 
+def test_read_of_no_rows(C):
+    """Slots without tokens: no rows."""
+    c = C.PagedCache(3, 2, 4, 16, 1, 2, 64, C.FOUR_BITS)
+    zero = ints([0, 0, 0])
+    k, v = c.read(0, ints([0, 0, 0, 0]), first=zero, N=0)
+    assert k.shape == v.shape == (0, 2, 64)
+    assert c.read(0, ints([0, 0, 0, 0]), first=zero, out=(k, v))[0] is k
+
+
 def test_many_slots(C):
     rng = np.random.default_rng(4096)
     lens, chunks = rng.integers(0, 30, 4096).tolist(), rng.integers(0, 3, 4096).tolist()
