@@ -5,6 +5,7 @@
 // cache_store.hip.  What differs is how the operands come about:
 //   K, bf16 queries: the codes and scales go into the scaled matrix product as they lie in memory,
 //     16 bytes (a block of 32 elements) per lane; the queries are two 8-bit operands (Queries).
+//     Where these are too coarse for a row and the keys of a step, both are bf16 operands.
 //   K, f32 queries: a lane's D / 4 neighbouring elements of a key, converted to binary32.
 //   V: a lane's 16 bytes are 8 keys x 4 elements.  A conversion takes two neighbouring
 //     elements of one key with that key's scale to two bf16 (exact: two significant bits);
@@ -30,6 +31,8 @@
 // two waves to a workgroup (343), the next group's pages and queries loaded before a group's
 // join (355), values converted once into LDS for 8 waves (461 for 460), tiles of 192, 96 and 256 rows for
 // prompts (469, 462, 474).
+#include <type_traits>
+
 #include "attend_common.h"
 
 namespace dspark {
@@ -38,8 +41,6 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
 
 template <int kSel>
 __device__ __forceinline__ uint32_t pair_bf16(uint32_t w, float s) {
@@ -80,7 +81,7 @@ struct Queries<float, D> {
     for (int s = 0; s < kPieces; ++s)
       raw[s] = live ? *reinterpret_cast<const u32x4*>(p + quad * (D / 4) + 4 * s) : u32x4{0u, 0u, 0u, 0u};
   }
-  __device__ __forceinline__ void put(int, u32x4* to, uint32_t*) const {
+  __device__ __forceinline__ void put(int, float, u32x4* to, uint32_t*) const {
 #pragma unroll
     for (int s = 0; s < kPieces; ++s) to[64 * s] = raw[s];
   }
@@ -91,12 +92,20 @@ struct Queries<float, D> {
 // row's largest element to [128, 256), and lo, what is left, 16 times finer.  bf16 has 8
 // significant bits: the sum is exact for elements above 2^-13 of the row's largest, and off by at most
 // 2^-21 of that below.  The product with 4-bit codes and their scales is exact, sums are binary32.
+// What the sums are off by, added up over a row (rest), moves its score with a key by no more
+// than scale rest max|k|.  16 rows have a limit, the largest scale byte of a key up to which that is below
+// kSplit for all of them; steps with larger ones are multiplied in bf16 (exact_scores).
 //   operand of 128 dimensions: lane group quad holds elements 16 quad .. + 15 and 64 + 16 quad .. + 15
 //   D = 64: hi and lo are the two halves of one operand, the keys' blocks are loaded twice.
 // Operand c: pieces 2 c and 2 c + 1; c even hi, odd lo (D = 64: piece 0 hi, 1 lo).  The scale bytes of hi and lo
-// are bytes 0 and 1 of a word (D = 64: byte 0 that of the lane group's half).
+// are bytes 0 and 1 of a word (D = 64: byte 0 that of the lane group's half), byte 3 is the 16 rows' limit.
 template <int D>
 constexpr int kQueryOps = D / 64;
+// How far (binary logarithm) the two parts may move a score: 0.034 % of a weight, a twelfth of what its rounding to
+// bf16 may take.  Rows whose elements lie within 2^13 of the largest have no limit; of normal variates of 128
+// dimensions one row in 30 has, for keys in the thousands.  Where every step is multiplied in bf16, 256 slots of 17 tokens
+// take 687 us instead of 295, a token over 30,000 24 instead of 20.5.
+constexpr float kSplit = 0x1p-11f;
 
 template <int D>
 struct Queries<uint16_t, D> {
@@ -109,41 +118,68 @@ struct Queries<uint16_t, D> {
       for (int h = 0; h < 2; ++h)
         raw[g][h] = live ? *reinterpret_cast<const u32x4*>(p + 64 * g + 16 * quad + 8 * h) : u32x4{0u, 0u, 0u, 0u};
   }
-  __device__ __forceinline__ void put(int quad, u32x4* to, uint32_t* scale) const {
-    uint32_t top = 0u;
+  __device__ __forceinline__ void put(int quad, float scale_log2, u32x4* to, uint32_t* scale) const {
+    // the largest magnitude and the smallest but 0, less a bit
+    typedef uint16_t Two __attribute__((ext_vector_type(2)));
+    Two large = {0, 0}, small = {0xFFFF, 0xFFFF};
 #pragma unroll
     for (int g = 0; g < D / 64; ++g)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          top = max(top, max(raw[g][h][i] & 0x7FFFu, raw[g][h][i] >> 16 & 0x7FFFu));
+        for (int i = 0; i < 4; ++i) {
+          const Two m = __builtin_bit_cast(Two, raw[g][h][i] & 0x7FFF7FFFu);
+          large = __builtin_elementwise_max(large, m);
+          small = __builtin_elementwise_min(small, m - Two{1, 1});
+        }
+    uint32_t top = max((uint32_t)large.x, (uint32_t)large.y);
     top = max(top, (uint32_t)__shfl_xor((int)top, 16, 64));
     top = max(top, (uint32_t)__shfl_xor((int)top, 32, 64));
     const uint32_t byte = max((int)(top >> 7) - 7, 5);
     const float f = __uint_as_float((254u - byte) << 23);
+    float rest = 0.f;  // in units of lo
+    const auto split = [&](auto with_rest) {
 #pragma unroll
-    for (int g = 0; g < D / 64; ++g) {
-      u32x4 his, los;
+      for (int g = 0; g < D / 64; ++g) {
+        u32x4 his, los;
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t w0 = raw[g][h][2 * i], w1 = raw[g][h][2 * i + 1];
-          const float a = bf16_lo(w0) * f, b = bf16_hi(w0) * f, c = bf16_lo(w1) * f, d = bf16_hi(w1) * f;
-          int hi = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-          hi = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, hi, true);
-          int lo = __builtin_amdgcn_cvt_pk_fp8_f32((a - __builtin_amdgcn_cvt_f32_fp8(hi, 0)) * 16.f,
-                                                   (b - __builtin_amdgcn_cvt_f32_fp8(hi, 1)) * 16.f, 0, false);
-          lo = __builtin_amdgcn_cvt_pk_fp8_f32((c - __builtin_amdgcn_cvt_f32_fp8(hi, 2)) * 16.f,
-                                               (d - __builtin_amdgcn_cvt_f32_fp8(hi, 3)) * 16.f, lo, true);
-          his[2 * h + i] = (uint32_t)hi;
-          los[2 * h + i] = (uint32_t)lo;
-        }
-      to[64 * (D == 64 ? 0 : g / 2 * 4 + g % 2)] = his;
-      to[64 * (D == 64 ? 1 : g / 2 * 4 + 2 + g % 2)] = los;
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t w0 = raw[g][h][2 * i], w1 = raw[g][h][2 * i + 1];
+            const float a = bf16_lo(w0) * f, b = bf16_hi(w0) * f, c = bf16_lo(w1) * f, d = bf16_hi(w1) * f;
+            int hi = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+            hi = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, hi, true);
+            const float x[4] = {(a - __builtin_amdgcn_cvt_f32_fp8(hi, 0)) * 16.f,
+                                (b - __builtin_amdgcn_cvt_f32_fp8(hi, 1)) * 16.f,
+                                (c - __builtin_amdgcn_cvt_f32_fp8(hi, 2)) * 16.f,
+                                (d - __builtin_amdgcn_cvt_f32_fp8(hi, 3)) * 16.f};
+            int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
+            lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+            if constexpr (decltype(with_rest)::value)
+              rest += fabsf(x[0] - __builtin_amdgcn_cvt_f32_fp8(lo, 0)) + fabsf(x[1] - __builtin_amdgcn_cvt_f32_fp8(lo, 1)) +
+                      (fabsf(x[2] - __builtin_amdgcn_cvt_f32_fp8(lo, 2)) + fabsf(x[3] - __builtin_amdgcn_cvt_f32_fp8(lo, 3)));
+            his[2 * h + i] = (uint32_t)hi;
+            los[2 * h + i] = (uint32_t)lo;
+          }
+        to[64 * (D == 64 ? 0 : g / 2 * 4 + g % 2)] = his;
+        to[64 * (D == 64 ? 1 : g / 2 * 4 + 2 + g % 2)] = los;
+      }
+    };
+    int limit = 255;
+    // one of the lane's elements is below 2^-6 in units of hi, or no normal number
+    if (__ballot(min((uint32_t)small.x, (uint32_t)small.y) + 1u < max((int)byte - 6, 1) << 7)) {
+      split(std::true_type());
+      rest += __shfl_xor(rest, 16, 64);
+      rest += __shfl_xor(rest, 32, 64);
+      // 2^(byte - 127) rest / 16 scale_log2 6 2^(limit - 127) <= kSplit, by the exponent of what stands beside the powers
+      const float x = rest * (scale_log2 * (6.f / kSplit));
+      if (x > 0.f) limit = min(max(384 - (int)byte - (int)(__float_as_uint(x) >> 23), 0), 255);
+      limit = 255 - (int)max16((uint32_t)(255 - limit));
+    } else {
+      split(std::false_type());
     }
-    *scale = D == 64 ? (quad < 2 ? byte : byte - 4) : byte | (byte - 4) << 8;
+    *scale = (D == 64 ? (quad < 2 ? byte : byte - 4) : byte | (byte - 4) << 8) | (uint32_t)limit << 24;
   }
 };
 
@@ -405,11 +441,14 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
   for (int x = 0; x < kMine; ++x)
     if (x * KW + part < NQ)
-      rows_of[x].put(quad, mine + (x * KW + part) * Query::kPieces * 64, &sh_scale[((wave % RW) * NQ + x * KW + part) * 64 + lane]);
+      rows_of[x].put(quad, a.scale_log2, mine + (x * KW + part) * Query::kPieces * 64, &sh_scale[((wave % RW) * NQ + x * KW + part) * 64 + lane]);
   __syncthreads();
   uint32_t q_scale[NQ];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) q_scale[i] = kF32 ? 0u : sh_scale[((wave % RW) * NQ + i) * 64 + lane];
+  int limit = 255;  // of the wave's rows
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) limit = min(limit, kF32 ? 255 : __builtin_amdgcn_readfirstlane((int)(q_scale[i] >> 24)));
   wait_loads();
   f32x4 s[NQ][2];
   Chunk p[NQ][kVC];
@@ -475,6 +514,32 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
     far = __ballot(far) != 0;
   };
+  // bf16: a step's scores from bf16 operands: the keys' codes converted, the queries as they are in memory.  An operand
+  // takes 8 elements of a lane's block.
+  auto exact_scores = [&]() {
+    constexpr int kOps = D == 64 ? 2 : D / 32;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int row = row0 + wrow + 16 * i + n, token = row < rows ? row / G : 0;
+      const E* from = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row < rows ? row - token * G : 0)) * D;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < kOps; ++c) {
+        const int b = c / 4;
+        const u32x4 x = *reinterpret_cast<const u32x4*>(
+            from + (D == 64 ? 32 * (quad & 1) + 16 * (quad >> 1) + 8 * c : 128 * b + 32 * quad + 8 * (c & 3)));
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t byte = k[u].scale[b] >> (8 * (n & 3)) & 255u;
+          const float f = byte == 255u ? NAN : scale_of(byte);
+          const uint32_t w = D == 64 ? (quad < 2 ? k[u].w[c & 1] : k[u].w[2 + (c & 1)]) : k[u].w[c];
+          const u32x4 y = {pair_bf16<0>(w, f), pair_bf16<1>(w, f), pair_bf16<2>(w, f), pair_bf16<3>(w, f)};
+          if constexpr (!kF32) s[i][u] = Op::score(__builtin_bit_cast(Chunk, y), __builtin_bit_cast(Chunk, x), s[i][u]);
+        }
+      }
+    }
+  };
   for (int t = t0; t < t1; ++t) {
     const int ahead = min(t + 1, t1 - 1);
     const int ma = pa, mb = pb;
@@ -517,6 +582,16 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
         }
     }
     matrix_done();
+    if constexpr (!kF32) {
+      if (limit < 255) {
+        uint32_t top = 0u;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int b = 0; b < (D + 127) / 128; ++b) top = max(top, k[u].scale[b] >> (8 * (n & 3)) & 255u);
+        if (__builtin_expect(__ballot((int)top > limit) != 0, 0)) exact_scores();
+      }
+    }
     pages_of(ahead, pa, pb);
     load_k(ahead, pa, pb, k);
     if (__builtin_expect(partial, 0)) {

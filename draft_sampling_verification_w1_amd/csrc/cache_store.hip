@@ -188,9 +188,6 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
   const int e = (int)(top >> 23) - 2 + ((top & 0x7FFFFFu) > 0x600000u);
   return top >= 0x7F800000u ? 255u : (uint32_t)min(max(e, 7), 252);
 }
-// The power of two of a scale byte; blocks without values take zero codes.
-__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
-
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 template <int kSel>
@@ -202,15 +199,6 @@ __device__ __forceinline__ uint32_t code8(const float (&x)[8], float scale) {
   w = code2<1>(w, x[2], x[3], scale);
   w = code2<2>(w, x[4], x[5], scale);
   return code2<3>(w, x[6], x[7], scale);
-}
-
-// Largest of 16 neighbouring lanes, in all of them (rotations within a row of 16 lanes).
-__device__ __forceinline__ uint32_t max16(uint32_t x) {
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true));
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xF, 0xF, true));
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xF, 0xF, true));
-  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xF, 0xF, true));
-  return x;
 }
 
 // Two neighbouring elements in binary32.

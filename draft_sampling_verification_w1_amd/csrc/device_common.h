@@ -268,6 +268,18 @@ struct CandState {
   }
 };
 
+// Largest of 16 neighbouring lanes, in all of them (rotations within a row of 16 lanes).
+__device__ __forceinline__ uint32_t max16(uint32_t x) {
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xF, 0xF, true));
+  x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x121, 0xF, 0xF, true));
+  return x;
+}
+
+// The power of two of a 4-bit block's scale byte; blocks without values take zero codes.
+__device__ __forceinline__ float scale_of(uint32_t byte) { return __uint_as_float(byte << 23); }
+
 struct LsePartials {
   float* m;
   double* s;

@@ -475,8 +475,9 @@ int dspark_attend(const dspark_cache* c, const dspark_cache_tables* t, int32_t l
                   void* stream);
 
 /* dspark_attend over a 4-bit cache: keys and values are what the codes stand for, exactly;
- * dtype of q and out: DSPARK_BF16 (products of bf16 operands, weights rounded to bf16) or
- * DSPARK_F32.  Where a block has the scale byte 255, rows that see its token are NaN (of a
+ * dtype of q and out: DSPARK_BF16 (weights rounded to bf16) or DSPARK_F32.  A bf16 query is
+ * multiplied as the sum of two 8-bit parts, exact for elements within 2^13 of the row's largest; where
+ * smaller ones could move a scaled score by more than 2^-11 ln 2, as bf16.  Where a block has the scale byte 255, rows that see its token are NaN (of a
  * value's block: in its 32 elements, the others may be NaN, too), the others don't depend on
  * it.  Everything else as in dspark_attend. */
 int dspark_attend4(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
