@@ -28,13 +28,13 @@ HIPCC_FLAGS = [
 ]
 
 
-# Per-source flags.  The split passes never produce or test a NaN (entries
-# outside the vocabulary are -inf, and a block whose maximum is -inf is left
-# before any difference of infinities is formed); without NaNs to honour, the
-# compiler drops the NaN-quieting v_max it otherwise puts in front of every
-# maximum of matrix-core results.
-EXTRA_FLAGS = {"bias_pass.hip": ["-fno-honor-nans"], "attend.hip": ["-fno-honor-nans"],
-               "attend4.hip": ["-fno-honor-nans"]}
+# Per-source flags.  These passes never produce or test a NaN (entries outside the
+# vocabulary are -inf, a block whose maximum is -inf is left before any
+# difference of infinities is formed, and keys and values of whole elements are
+# finite by their contract); without NaNs to honour, the compiler drops the
+# NaN-quieting v_max it otherwise puts in front of every maximum of matrix-core
+# results.  attend4.hip is not among them: its blocks without a value are NaN.
+EXTRA_FLAGS = {"bias_pass.hip": ["-fno-honor-nans"], "attend.hip": ["-fno-honor-nans"]}
 
 
 def _hipcc() -> str:

@@ -598,14 +598,14 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       asm volatile("");  // a branch, not selections in every step
       uint32_t none[2];
       if (clear_v(t, ma, mb, v, none)) {
-        // rows that see the token are NaN by its score (as bits: the compiler takes numbers for granted)
+        // rows that see the token are NaN by its score
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
           for (int u = 0; u < 2; ++u)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-              s[i][u][r] = __uint_as_float(none[u] >> (8 * r + 7) & 1u ? 0x7FC00000u : __float_as_uint(s[i][u][r]));
+              s[i][u][r] = none[u] >> (8 * r + 7) & 1u ? NAN : s[i][u][r];
       }
 #pragma unroll
       for (int i = 0; i < NQ; ++i) {
