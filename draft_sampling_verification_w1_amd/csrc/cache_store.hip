@@ -7,7 +7,7 @@
 // The angle is a binary64 product (p f_j loses everything in binary32 from some 10^5
 // positions on); it is reduced by the nearest multiple of pi / 2 (two parts of pi / 2, one
 // fma each, exact to 2^-53 or so) and the sine and cosine are their Taylor series on
-// [-pi/4, pi/4] (to r^15: below 2^-52), rounded to binary32 once.  A workgroup works them out
+// [-pi/4, pi/4] (to r^15 and r^16: off by less than 2^-52), rounded to binary32 once.  A workgroup works them out
 // for its 8 tokens and all heads use them from LDS: there is no table that ends at some
 // longest position and none to read.  The pair's products and sums are rounded one by one
 // in binary32 (no fma), so that the 4-bit codes follow from the plain definition bit for bit.
@@ -159,7 +159,8 @@ __device__ __forceinline__ float2 cos_sin(double angle) {
   s = fma(s, z, 8.3333333333333332e-03);
   s = fma(s, z, -1.6666666666666666e-01);
   s = fma(s, z * r, r);
-  double c = -1.1470745597729725e-11;  // -1 / 14!
+  double c = 4.7794773323873853e-14;  // 1 / 16!
+  c = fma(c, z, -1.1470745597729725e-11);
   c = fma(c, z, 2.0876756987868100e-09);
   c = fma(c, z, -2.7557319223985888e-07);
   c = fma(c, z, 2.4801587301587302e-05);
