@@ -10,7 +10,8 @@
 // [-pi/4, pi/4] (to r^15 and r^16: off by less than 2^-52), rounded to binary32 once.  A workgroup works them out
 // for its 8 tokens and all heads use them from LDS: there is no table that ends at some
 // longest position and none to read.  The pair's products and sums are rounded one by one
-// in binary32 (no fma), so that the 4-bit codes follow from the plain definition bit for bit.
+// in binary32 (no fma), so that the 4-bit codes follow from the plain definition bit for bit (but for a sine or
+// cosine within 2^-52 of the middle between two binary32 numbers, one in some 10^8).
 //
 // 4 bits.  32 elements of a token share a power of two 2^e, an element is one of +-{0, 0.5, 1,
 // 1.5, 2, 3, 4, 6} 2^e (E2M1 with E8M0 scales, the types of gfx950's conversions and matrix
