@@ -759,7 +759,7 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
   int64_t x = 0, groups = 0, steps = 0;
   int long_chunk = 0, mine = 0;
   for (int s = s0; s < s1; ++s) {
-    const SlotWork w = slot_work(a, s, rows);
+    const SlotWork w = slot_work(a, s, rows, a.extra);
     x += w.units;
     if (per == 1) {
       plan.near[s][0] = w.o0;
@@ -896,7 +896,10 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
       last = span + n - 1;
       x = x1;
     } else {
-      find_group(a, kRows, plan, x, g, [&](int s) { return plan.per == 1 ? near_work(a, plan, s, kRows) : slot_work(a, s, kRows); });
+      const auto work_of = [&](int s) {
+        return plan.per == 1 ? near_work(a, plan, s, kRows) : slot_work(a, s, kRows, a.extra);
+      };
+      find_group(a, kRows, plan, x, g, work_of, a.extra, true);
       if (g.units == 0) {
         x = g.next;
         continue;

@@ -87,11 +87,12 @@ struct Ops<float> {
 };
 
 // ---- the batch's work, cut into equal spans (attend_plan.h) --------------------------
-__device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int rows) {
+// extra: what a group takes on the line in front of its first step.
+__device__ __forceinline__ SlotWork slot_work(const AttendArgs& a, int s, int rows, int extra = 0) {
   const int o0 = min(max(a.offsets[s], 0), a.N);
   const int o1 = min(max(a.offsets[s + 1], o0), a.N);
   return plan_slot(o0, o1, a.c.t.lens[s], (int64_t)a.c.max_pages << a.c.page_shift, a.group, rows,
-                   a.c.kv_heads, a.extra);
+                   a.c.kv_heads, extra);
 }
 
 // Units before each plan thread's run of slots (thread t: slots [t per, t per + per)).
@@ -157,10 +158,11 @@ struct Group {
 };
 
 // `g` may hold the group before it: a slot is looked up when the line leaves it.  work_of(s):
-// the slot's work.
+// the slot's work; extra, narrow: as in slot_work and plan_place.
 template <typename F>
 __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const Plan& plan,
-                                           int64_t x, Group& g, F work_of) {
+                                           int64_t x, Group& g, F work_of, int extra = 0,
+                                           bool narrow = false) {
   if (x >= g.slot_end) {
     int lo = 0, hi = kPlanThreads - 1;
     while (lo < hi) {
@@ -180,7 +182,7 @@ __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const 
     g.slot_start = start;
     g.slot_end = start + g.w.units;
   }
-  const PlanPlace at = plan_place(g.w, a.group, rows, x - g.slot_start, a.extra);
+  const PlanPlace at = plan_place(g.w, a.group, rows, x - g.slot_start, extra, narrow);
   g.head = at.head;
   g.tile = at.tile;
   g.units = at.units;
