@@ -392,14 +392,14 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     return true;
   };
   // f32: operands of a 16-key block: lane (n, quad), operand s: elements quad D / 4 + 4 s ..
-  auto k_operands = [&](const RawK<D>& r, Chunk (&k)[kSteps]) {
+  auto k_operands = [&](const auto& r, auto (&k)[kSteps]) {
 #pragma unroll
     for (int s = 0; s < kSteps; ++s) {
       const float f = scale_of(r.scale[D == 256 ? s / 8 : 0] >> (8 * (n & 3)) & 255u);
       const uint32_t w = r.w[s / 2];
       const f32x2 x = s & 1 ? pair_f32<2>(w, f) : pair_f32<0>(w, f);
       const f32x2 y = s & 1 ? pair_f32<3>(w, f) : pair_f32<1>(w, f);
-      if constexpr (kF32) k[s] = f32x4{x[0], x[1], y[0], y[1]};
+      k[s] = f32x4{x[0], x[1], y[0], y[1]};
     }
   };
   // operands d and d + 1 (d = 4 g + 2 h): elements n D / 16 + d, .. + 1 of the lane's keys

@@ -104,39 +104,27 @@ struct Plan {
   int per;
 };
 
-// kThreads: of the workgroup, a multiple of 64; each takes kRuns neighbouring runs of slots.
-template <int kThreads = kPlanThreads>
+// By all threads of a workgroup, of which there are kPlanThreads at least.
 __device__ __forceinline__ void make_plan(const AttendArgs& a, int rows, Plan& plan) {
-  constexpr int kRuns = kThreads < kPlanThreads ? kPlanThreads / kThreads : 1;
-  constexpr int kWaves = (kThreads < kPlanThreads ? kThreads : kPlanThreads) / 64;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int per = (a.c.slots + kPlanThreads - 1) / kPlanThreads;
-  int64_t run[kRuns], x = 0;
-#pragma unroll
-  for (int r = 0; r < kRuns; ++r) {
-    const int t = tid * kRuns + r;
-    const int s0 = t < kPlanThreads ? t * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
-    for (int s = s0; s < s1; ++s) x += slot_work(a, s, rows).units;
-    run[r] = x;
-  }
-  const int64_t mine = x;
+  const int s0 = tid < kPlanThreads ? tid * per : a.c.slots, s1 = min(s0 + per, a.c.slots);
+  int64_t x = 0;
+  for (int s = s0; s < s1; ++s) x += slot_work(a, s, rows).units;
 #pragma unroll
   for (int off = 1; off < 64; off <<= 1) {
     const int64_t y = __shfl_up(x, off, 64);
     if (lane >= off) x += y;
   }
-  if (lane == 63 && wave < kWaves) plan.sum[wave] = x;
+  if (lane == 63 && wave < kPlanWaves) plan.sum[wave] = x;
   __syncthreads();
   int64_t total = 0;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
+  for (int w = 0; w < kPlanWaves; ++w) {
     if (w < wave) x += plan.sum[w];
     total += plan.sum[w];
   }
-  if (tid * kRuns < kPlanThreads) {
-#pragma unroll
-    for (int r = 0; r < kRuns; ++r) plan.before[tid * kRuns + r + 1] = x - mine + run[r];
-  }
+  if (tid < kPlanThreads) plan.before[tid + 1] = x;
   if (tid == 0) {
     const int64_t span = plan_span(total, a.grid);
     plan.before[0] = 0;

@@ -83,8 +83,9 @@ struct PlanPlace {
   int64_t next;  // the next pair's first unit
 };
 
-// narrow: a division in 32 bits where it can be; one in 64 takes a hundred instructions more, which counts for groups of
-// few steps, but a branch around it costs prompts over whole elements 0.6 % (two chunks of 2,048: 505.5 us, 502.5 without).
+// narrow: a division in 32 bits where it can be; one in 64 takes a hundred instructions more.  For groups of few
+// steps (4 bits); the branch around it makes the longest tiles' loop over whole elements 11 % longer
+// (two chunks of 2,048: 505.5 us, 502.5 without).
 PLAN_FN PlanPlace plan_place(const SlotWork& w, int group, int rows, int64_t left, int extra = 0, bool narrow = false) {
   PlanPlace g;
   const int64_t pair = narrow && left <= INT32_MAX ? (int64_t)((int32_t)left / w.pair_units) : left / w.pair_units;
