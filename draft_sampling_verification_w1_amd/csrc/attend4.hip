@@ -175,7 +175,7 @@ struct Queries<uint16_t, D> {
       // 2^(byte - 127) rest / 16 scale_log2 6 2^(limit - 127) <= kSplit, by the exponent of what stands beside the powers
       const float x = rest * (scale_log2 * (6.f / kSplit));
       if (x > 0.f) limit = min(max(384 - (int)byte - (int)(__float_as_uint(x) >> 23), 0), 255);
-      limit = 255 - (int)max16((uint32_t)(255 - limit));
+      limit = 255 - (int)max_lanes16((uint32_t)(255 - limit));
     } else {
       split(std::false_type());
     }

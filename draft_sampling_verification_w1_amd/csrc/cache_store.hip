@@ -328,7 +328,7 @@ __device__ __forceinline__ void store_v(const StoreArgs& a, const Place& g, int 
     uint32_t word[2] = {0u, 0u}, bytes[2] = {0u, 0u};
 #pragma unroll
     for (int t = 0; t < kGroup; ++t) {
-      const uint32_t byte = scale_byte(max16(max(magnitude(x[t].x), magnitude(x[t].y))));
+      const uint32_t byte = scale_byte(max_lanes16(max(magnitude(x[t].x), magnitude(x[t].y))));
       const float s = scale_of(byte);
       uint32_t& w = word[t >> 2];
       uint32_t old = w;

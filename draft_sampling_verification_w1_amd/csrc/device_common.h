@@ -269,7 +269,7 @@ struct CandState {
 };
 
 // Largest of 16 neighbouring lanes, in all of them (rotations within a row of 16 lanes).
-__device__ __forceinline__ uint32_t max16(uint32_t x) {
+__device__ __forceinline__ uint32_t max_lanes16(uint32_t x) {
   x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x128, 0xF, 0xF, true));
   x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x124, 0xF, 0xF, true));
   x = max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x122, 0xF, 0xF, true));
