@@ -799,12 +799,8 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
     }
     whole = whole && groups > 0;
     if (whole) {
-      // pieces by each target, summed up side by side in 16 bits each (768 of a batch at most)
       plan_targets(steps, (int)groups, a.grid, target);
-      x = 0;
-#pragma unroll
-      for (int k = 0; k < kTargets; ++k)
-        x |= (int64_t)(plan_pieces(mine, target[k]) * a.c.kv_heads) << (16 * k);
+      x = plan_packed(mine, target, a.c.kv_heads);
     }
   }
 #pragma unroll
@@ -821,16 +817,11 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
     total += plan.sum[w];
   }
   if (whole) {
-    int best = kTargets - 1, span_units = target[kTargets - 1];
-#pragma unroll
-    for (int k = kTargets - 2; k >= 0; --k)
-      if ((int)(total >> (16 * k) & 0xFFFF) <= a.grid) {
-        best = k;
-        span_units = target[k];
-      }
-    x = x >> (16 * best) & 0xFFFF;
-    total = total >> (16 * best) & 0xFFFF;
-    if (tid == 0) plan.target = span_units;
+    int units;
+    const int best = plan_choice(total, a.grid, target, units);
+    x = plan_unpacked(x, best);
+    total = plan_unpacked(total, best);
+    if (tid == 0) plan.target = units;
   }
   if (tid < kPlanThreads) plan.before[tid + 1] = x;
   if (tid == 0) {
@@ -844,20 +835,15 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
 // The group of piece x of the batch: its slot is the run of slots that x lies in.  j, n: which piece of how many.
 __device__ __forceinline__ void find_piece(const AttendArgs& a, int rows, const Plan4& plan, int x,
                                            Group& g, int& j, int& n) {
-  int lo = 0, hi = kPlanThreads - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (plan.before[mid] <= x) lo = mid;
-    else hi = mid - 1;
-  }
-  const int left = x - (int)plan.before[lo];
-  g.w = near_work(a, plan, lo, rows);
-  g.slot = lo;
+  const int s = plan_run(plan.before, kPlanThreads, x);
+  g.w = near_work(a, plan, s, rows);
+  g.slot = s;
   g.tile = 0;
   g.units = tile_units(g.w, a.group, rows, 0);
-  n = plan_pieces(g.units, plan.target);
-  g.head = left / n;
-  j = left - g.head * n;
+  const PlanPiece p = plan_piece(g.units, plan.target, x - (int)plan.before[s]);
+  g.head = p.head;
+  j = p.j;
+  n = p.n;
 }
 
 template <typename E, int D, int NQ, int RW, int KW, bool kHalf>

@@ -152,12 +152,7 @@ __device__ __forceinline__ void find_group(const AttendArgs& a, int rows, const 
                                            int64_t x, Group& g, F work_of, int extra = 0,
                                            bool narrow = false) {
   if (x >= g.slot_end) {
-    int lo = 0, hi = kPlanThreads - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (plan.before[mid] <= x) lo = mid;
-      else hi = mid - 1;
-    }
+    const int lo = plan_run(plan.before, kPlanThreads, x);
     int64_t start = plan.before[lo];
     int s = lo * plan.per;
     const int end = min(s + plan.per, a.c.slots);

@@ -137,6 +137,46 @@ PLAN_FN void plan_targets(int64_t total, int groups, int grid, int (&target)[kTa
   }
 }
 PLAN_FN int plan_pieces(int units, int target) { return (int)(((uint32_t)units + (uint32_t)target - 1u) / (uint32_t)target); }
+// Pieces of a slot's groups by each target, in 16 bits each, so that one sum over the slots counts all of them: 768 of a
+// batch at most (a workgroup's even share each, and one that is not full for every group).
+PLAN_FN int64_t plan_packed(int units, const int (&target)[kTargets], int kv_heads) {
+  int64_t x = 0;
+  for (int k = 0; k < kTargets; ++k) x |= (int64_t)(plan_pieces(units, target[k]) * kv_heads) << (16 * k);
+  return x;
+}
+PLAN_FN int plan_unpacked(int64_t x, int k) { return (int)(x >> (16 * k) & 0xFFFF); }
+// Which target it is, and its units, by the batch's packed sum.
+PLAN_FN int plan_choice(int64_t total, int grid, const int (&target)[kTargets], int& units) {
+  int best = kTargets - 1;
+  units = target[kTargets - 1];
+  for (int k = kTargets - 2; k >= 0; --k)
+    if (plan_unpacked(total, k) <= grid) {
+      best = k;
+      units = target[k];
+    }
+  return best;
+}
+// The last of `runs` runs of slots that starts at x or before it (before: what lies in front of each run).
+PLAN_FN int plan_run(const int64_t* before, int runs, int64_t x) {
+  int lo = 0, hi = runs - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (before[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+// Piece `left` of a slot whose groups have n pieces each: the j-th of head's.
+struct PlanPiece {
+  int head, j, n;
+};
+PLAN_FN PlanPiece plan_piece(int units, int target, int left) {
+  PlanPiece p;
+  p.n = plan_pieces(units, target);
+  p.head = left / p.n;
+  p.j = left - p.head * p.n;
+  return p;
+}
 // First unit of piece j of n.
 PLAN_FN int piece_start(int units, int j, int n) { return (int)((int64_t)units * j / n); }
 
