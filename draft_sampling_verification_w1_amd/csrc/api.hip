@@ -401,7 +401,6 @@ int attend(const dspark_cache* c, const dspark_cache_tables* t, int layer, const
   a.offsets = offsets;
   a.out = out;
   a.grid = L.grid;
-  a.extra = packed ? attend4_extra(c->slots * c->kv_heads, L.grid) : 0;
   a.part_o = at<float>(ws, L.o);
   a.part_ml = at<float>(ws, L.ml);
   a.cuts = at<AttendCut>(ws, L.cuts);

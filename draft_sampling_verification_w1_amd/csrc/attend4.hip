@@ -743,10 +743,14 @@ struct Plan4 : Plan {
   int near[kPlanThreads][3];  // a slot's token rows and length, if there are no more slots
 };
 
+__device__ __forceinline__ int charge_of(const AttendArgs& a) {
+  return plan_charge((int64_t)a.c.slots * a.c.kv_heads, a.grid);
+}
+
 __device__ __forceinline__ SlotWork near_work(const AttendArgs& a, const Plan4& plan, int s, int rows) {
   return plan_slot(__builtin_amdgcn_readfirstlane(plan.near[s][0]), __builtin_amdgcn_readfirstlane(plan.near[s][1]),
                    __builtin_amdgcn_readfirstlane(plan.near[s][2]), (int64_t)a.c.max_pages << a.c.page_shift, a.group,
-                   rows, a.c.kv_heads, a.extra);
+                   rows, a.c.kv_heads, charge_of(a));
 }
 
 template <int kThreads>
@@ -759,7 +763,7 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
   int64_t x = 0, groups = 0, steps = 0;
   int long_chunk = 0, mine = 0;
   for (int s = s0; s < s1; ++s) {
-    const SlotWork w = slot_work(a, s, rows, a.extra);
+    const SlotWork w = slot_work(a, s, rows, charge_of(a));
     x += w.units;
     if (per == 1) {
       plan.near[s][0] = w.o0;
@@ -883,9 +887,9 @@ __global__ __launch_bounds__(64 * RW * KW, (Shape4<E, D, NQ, RW, KW>::waves)) vo
       x = x1;
     } else {
       const auto work_of = [&](int s) {
-        return plan.per == 1 ? near_work(a, plan, s, kRows) : slot_work(a, s, kRows, a.extra);
+        return plan.per == 1 ? near_work(a, plan, s, kRows) : slot_work(a, s, kRows, charge_of(a));
       };
-      find_group(a, kRows, plan, x, g, work_of, a.extra, true);
+      find_group(a, kRows, plan, x, g, work_of, charge_of(a), true);
       if (g.units == 0) {
         x = g.next;
         continue;
@@ -1031,13 +1035,6 @@ int attend4_rows(bool bf16, int head_dim, int group, int max_chunk) {
   }
 #undef ATTEND4_SIZE
   return most;
-}
-
-// What a group costs beside its steps, in steps, where spans hold several groups (a span that
-// holds part of one group pays it whatever its steps are).  256 slots of 17 tokens by the charge: 0 321
-// us, 8 306, 14 299, 20 298, 30 300.
-int attend4_extra(int groups, int grid) {
-  return groups >= 2 * grid ? 20 : 0;
 }
 
 // Workgroups, and spans at most: what is resident at once, two waves per SIMD.  Tiles of 16 rows could have

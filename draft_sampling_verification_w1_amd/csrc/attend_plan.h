@@ -122,7 +122,18 @@ PLAN_FN int64_t plan_span(int64_t total, int grid) {
 // (By the last alone: 32 slots of 1 to 17 tokens 44.0 us instead of 42.3, a token over 130,000 43.5 instead of 40.5.)
 // total, groups: of the batch, groups > 0 (2 groups at most grid).
 constexpr int kTargets = 4;
+// Both sides of the boundary (cut by themselves, on a line with the charge below; 32 query heads on 8 of 128, 512
+// workgroups): 24 slots of 1 to 17 tokens over 2,100 35.5 and 41 us, 32 slots 40 and 45, 40 slots 44.6 and 46.5, 48 slots
+// 55 and 52; one token over 8,000 of 32 slots 48 and 48, 33 slots 51 and 46, 60 slots 81 and 72.
 PLAN_FN bool plan_few(int64_t groups, int grid) { return 2 * groups <= grid; }
+// What a group costs beside its steps, in steps, where spans hold several groups (`extra` above).  256 slots of 17
+// tokens by the charge: 0 321 us, 8 306, 14 299, 20 298, 30 300.  Without and with it, from the boundary on: 33 slots of 1 to
+// 17 tokens over 2,100 48 and 43 us, 60 slots 67 and 57; one token over 8,000 of 33 slots 49 and 46; a token over
+// 30,000 of a single one of 33 or 128 slots 26 and 22; 96 slots of 17 tokens over 4,096, 24 heads on 8 of 64, 86 and 74; 128 slots of
+// 9 tokens over 2,000, 16 heads on 2 of 256, 99.6 and 98.5; 64 slots of 5 tokens over 1,000, fp32, 57 and 55.  Few groups of
+// several row tiles have none: two prompts 458 without and 440 with it, 512 tokens over 8,192 118 and 123,
+// two chunks of 200 over 1,000 in fp32 52 and 65.
+PLAN_FN int plan_charge(int64_t groups, int grid) { return plan_few(groups, grid) ? 0 : 20; }
 PLAN_FN int64_t plan_div(int64_t x, int y) {  // x, y >= 0
   return x >> 31 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }

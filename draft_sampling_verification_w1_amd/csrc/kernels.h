@@ -371,7 +371,6 @@ struct AttendArgs {
   const int32_t* offsets;  // [slots + 1]
   void* out;               // [N, heads, head_dim]
   int grid;                // workgroups = spans of the batch's work at most (attend_grid)
-  int extra;               // what a group takes on the line beside its steps (4 bits)
   float* part_o;           // [2 * grid][rows][head_dim] of cut groups
   float* part_ml;          // [2 * grid][rows][2] largest score and sum
   AttendCut* cuts;         // [1 + grid]: the number of spans (first), then one per span
@@ -384,7 +383,6 @@ hipError_t launch_attend(bool bf16, int rows, const AttendArgs& a, hipStream_t s
 int attend4_grid(int head_dim, int rows);
 int attend4_max_rows(bool bf16, int head_dim);
 int attend4_rows(bool bf16, int head_dim, int group, int max_chunk);
-int attend4_extra(int groups, int grid);
 hipError_t launch_attend4(bool bf16, int rows, const AttendArgs& a, hipStream_t stream);
 
 }  // namespace dspark
