@@ -461,8 +461,9 @@ int dspark_cache_read(const dspark_cache* c, const dspark_cache_tables* t, int32
  * dspark_cache_append; rows behind offsets[slots] are left as they were.  A
  * slot may have no rows.  Scores, sums and outputs accumulate in binary32 (bf16:
  * the weights are rounded to bf16 for the product with v; one rounding at the
- * end).  Keys and values that any of the chunk's tokens sees must be finite and the
- * scaled scores below 5e29 in magnitude; what else the pages hold does not matter.
+ * end).  Keys and values that any of the chunk's tokens sees must be finite, the values below
+ * 2^90 (their weighted sums are divided at the end) and the scaled scores below 5e29 in
+ * magnitude; what else the pages hold does not matter.
  * out must not overlap q (a row's keys are shared out over workgroups).
  * max_chunk: the longest chunk expected, >= 1; it chooses the tiling only, any
  * chunk is computed.  scale > 0.  heads a multiple of kv_heads, N * heads <= 2^30.
