@@ -97,14 +97,15 @@ struct Queries<float, D> {
 // kSplit for all of them; steps with larger ones are multiplied in bf16 (exact_scores).
 //   operand of 128 dimensions: lane group quad holds elements 16 quad .. + 15 and 64 + 16 quad .. + 15
 //   D = 64: hi and lo are the two halves of one operand, the keys' blocks are loaded twice.
-// Operand c: pieces 2 c and 2 c + 1; c even hi, odd lo (D = 64: piece 0 hi, 1 lo).  The scale bytes of hi and lo
-// are bytes 0 and 1 of a word (D = 64: byte 0 that of the lane group's half), byte 3 is the 16 rows' limit.
+// Operand c: pieces 2 c and 2 c + 1; c even hi, odd lo (D = 64: piece 0 hi, 1 lo).  The scale bytes of hi
+// and lo are bytes 0 and 1 of a word (D = 64: byte 0 that of the lane group's half), byte 3 is the 16
+// rows' limit.
 template <int D>
 constexpr int kQueryOps = D / 64;
-// How far (binary logarithm) the two parts may move a score: 0.034 % of a weight, a twelfth of what its rounding to
-// bf16 may take.  Rows whose elements lie within 2^13 of the largest have no limit; of normal variates of 128
-// dimensions one row in 30 has, for keys in the thousands.  Where every step is multiplied in bf16, 256 slots of 17 tokens
-// take 687 us instead of 295, a token over 30,000 24 instead of 20.5.
+// How far (binary logarithm) the two parts may move a score: 0.034 % of a weight, a twelfth of what its
+// rounding to bf16 may take.  Rows whose elements lie within 2^13 of the largest have no limit; of normal
+// variates of 128 dimensions one row in 30 has, for keys in the thousands.  Where every step is multiplied
+// in bf16, 256 slots of 17 tokens take 687 us instead of 295, a token over 30,000 24 instead of 20.5.
 constexpr float kSplit = 0x1p-11f;
 
 template <int D>
@@ -116,7 +117,8 @@ struct Queries<uint16_t, D> {
     for (int g = 0; g < D / 64; ++g)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        raw[g][h] = live ? *reinterpret_cast<const u32x4*>(p + 64 * g + 16 * quad + 8 * h) : u32x4{0u, 0u, 0u, 0u};
+        raw[g][h] =
+            live ? *reinterpret_cast<const u32x4*>(p + 64 * g + 16 * quad + 8 * h) : u32x4{0u, 0u, 0u, 0u};
   }
   __device__ __forceinline__ void put(int quad, float scale_log2, u32x4* to, uint32_t* scale) const {
     // the largest magnitude and the smallest but 0, less a bit
@@ -157,8 +159,10 @@ struct Queries<uint16_t, D> {
             int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
             lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
             if constexpr (decltype(with_rest)::value)
-              rest += fabsf(x[0] - __builtin_amdgcn_cvt_f32_fp8(lo, 0)) + fabsf(x[1] - __builtin_amdgcn_cvt_f32_fp8(lo, 1)) +
-                      (fabsf(x[2] - __builtin_amdgcn_cvt_f32_fp8(lo, 2)) + fabsf(x[3] - __builtin_amdgcn_cvt_f32_fp8(lo, 3)));
+              rest += fabsf(x[0] - __builtin_amdgcn_cvt_f32_fp8(lo, 0)) +
+                      fabsf(x[1] - __builtin_amdgcn_cvt_f32_fp8(lo, 1)) +
+                      (fabsf(x[2] - __builtin_amdgcn_cvt_f32_fp8(lo, 2)) +
+                       fabsf(x[3] - __builtin_amdgcn_cvt_f32_fp8(lo, 3)));
             his[2 * h + i] = (uint32_t)hi;
             los[2 * h + i] = (uint32_t)lo;
           }
@@ -172,7 +176,8 @@ struct Queries<uint16_t, D> {
       split(std::true_type());
       rest += __shfl_xor(rest, 16, 64);
       rest += __shfl_xor(rest, 32, 64);
-      // 2^(byte - 127) rest / 16 scale_log2 6 2^(limit - 127) <= kSplit, by the exponent of what stands beside the powers
+      // 2^(byte - 127) rest / 16 scale_log2 6 2^(limit - 127) <= kSplit, by the exponent of what stands
+      // beside the powers of two
       const float x = rest * (scale_log2 * (6.f / kSplit));
       if (x > 0.f) limit = min(max(384 - (int)byte - (int)(__float_as_uint(x) >> 23), 0), 255);
       limit = 255 - (int)max_lanes16((uint32_t)(255 - limit));
@@ -267,7 +272,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     const int i = x * KW + part, row = row0 + wrow + 16 * i + n;
     const bool live = i < NQ && row < rows;
     const int token = live ? row / G : 0;
-    rows_of[x].load(q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0)) * D, live, quad);
+    const int64_t at = (int64_t)(it.w.o0 + token) * a.heads + it.head * G + (live ? row - token * G : 0);
+    rows_of[x].load(q + at * D, live, quad);
   }
   __syncthreads();  // the last group's limits, queries and sums are out of LDS
   for (int r = threadIdx.x; r < kRows; r += kThreads)
@@ -289,9 +295,11 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
   const uint8_t* Kb = static_cast<const uint8_t*>(a.K) + it.head * page * (D / 2);
   const uint8_t* Vb = static_cast<const uint8_t*>(a.V) + it.head * page * (D / 2);
   // from a page's codes of this head to its scales
-  const uint32_t to_scales = (uint32_t)(H * page * (D / 2) - it.head * page * (D / 2) + it.head * page * (D / 32));
+  const uint32_t to_scales =
+      (uint32_t)(H * page * (D / 2) - it.head * page * (D / 2) + it.head * page * (D / 32));
   const int k_key = Op::key_of(0, n) & (page - 1);
-  const int k_block = kF32 ? quad * D / 128 : (D == 64 ? quad & 1 : quad);  // the first, others 4 on (f32: 1 on)
+  // the first block, others 4 on (f32: 1 on)
+  const int k_block = kF32 ? quad * D / 128 : (D == 64 ? quad & 1 : quad);
   const uint32_t k_lane = (uint32_t)((k_block * page + k_key) * 16 + (kF32 && D == 64 ? (quad & 1) * 8 : 0));
   const uint32_t ks_lane = to_scales + (uint32_t)(k_block * page + (k_key & (kF32 ? ~3 : ~7)));
   const int v_key = (kF32 ? 4 * quad : 8 * quad) & (page - 1);
@@ -353,8 +361,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
         for (int g = 0; g < D / 64; ++g)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
-            v.w[g][2 * h + u] =
-                *reinterpret_cast<const uint32_t*>(base + (row >> 3) * (D / 64 * 256) + g * 256 + h * 8 + v_lane);
+            v.w[g][2 * h + u] = *reinterpret_cast<const uint32_t*>(
+                base + (row >> 3) * (D / 64 * 256) + g * 256 + h * 8 + v_lane);
         v.scale[u] = *reinterpret_cast<const uint32_t*>(base + row + vs_lane);
       }
     }
@@ -403,11 +411,13 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
   };
   // operands d and d + 1 (d = 4 g + 2 h): elements n D / 16 + d, .. + 1 of the lane's keys
-  auto v_operands = [&](const RawV<D>& r, const float (&s)[8], int g, int h, Chunk (&lo)[kVC], Chunk (&hi)[kVC]) {
+  auto v_operands = [&](const RawV<D>& r, const float (&s)[8], int g, int h, Chunk (&lo)[kVC],
+                        Chunk (&hi)[kVC]) {
     const uint32_t x = r.w[g][2 * h], y = r.w[g][2 * h + 1];
     if constexpr (!kF32) {
-      const uint32_t p[8] = {pair_bf16<0>(x, s[0]), pair_bf16<1>(x, s[1]), pair_bf16<2>(x, s[2]), pair_bf16<3>(x, s[3]),
-                             pair_bf16<0>(y, s[4]), pair_bf16<1>(y, s[5]), pair_bf16<2>(y, s[6]), pair_bf16<3>(y, s[7])};
+      const uint32_t p[8] = {pair_bf16<0>(x, s[0]), pair_bf16<1>(x, s[1]), pair_bf16<2>(x, s[2]),
+                             pair_bf16<3>(x, s[3]), pair_bf16<0>(y, s[4]), pair_bf16<1>(y, s[5]),
+                             pair_bf16<2>(y, s[6]), pair_bf16<3>(y, s[7])};
       u32x4 a, b;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -417,12 +427,14 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
       lo[0] = __builtin_bit_cast(Chunk, a);
       hi[0] = __builtin_bit_cast(Chunk, b);
     } else {
-      const f32x2 p[8] = {pair_f32<0>(x, s[0]), pair_f32<1>(x, s[1]), pair_f32<2>(x, s[2]), pair_f32<3>(x, s[3]),
-                          pair_f32<0>(y, s[4]), pair_f32<1>(y, s[5]), pair_f32<2>(y, s[6]), pair_f32<3>(y, s[7])};
+      const f32x2 p[8] = {pair_f32<0>(x, s[0]), pair_f32<1>(x, s[1]), pair_f32<2>(x, s[2]),
+                          pair_f32<3>(x, s[3]), pair_f32<0>(y, s[4]), pair_f32<1>(y, s[5]),
+                          pair_f32<2>(y, s[6]), pair_f32<3>(y, s[7])};
 #pragma unroll
       for (int u = 0; u < kVC; ++u) {
-        lo[u] = __builtin_bit_cast(Chunk, f32x4{p[4 * u][0], p[4 * u + 1][0], p[4 * u + 2][0], p[4 * u + 3][0]});
-        hi[u] = __builtin_bit_cast(Chunk, f32x4{p[4 * u][1], p[4 * u + 1][1], p[4 * u + 2][1], p[4 * u + 3][1]});
+        const f32x2* const z = p + 4 * u;
+        lo[u] = __builtin_bit_cast(Chunk, f32x4{z[0][0], z[1][0], z[2][0], z[3][0]});
+        hi[u] = __builtin_bit_cast(Chunk, f32x4{z[0][1], z[1][1], z[2][1], z[3][1]});
       }
     }
   };
@@ -441,14 +453,16 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
   for (int x = 0; x < kMine; ++x)
     if (x * KW + part < NQ)
-      rows_of[x].put(quad, a.scale_log2, mine + (x * KW + part) * Query::kPieces * 64, &sh_scale[((wave % RW) * NQ + x * KW + part) * 64 + lane]);
+      rows_of[x].put(quad, a.scale_log2, mine + (x * KW + part) * Query::kPieces * 64,
+                     &sh_scale[((wave % RW) * NQ + x * KW + part) * 64 + lane]);
   __syncthreads();
   uint32_t q_scale[NQ];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) q_scale[i] = kF32 ? 0u : sh_scale[((wave % RW) * NQ + i) * 64 + lane];
   int limit = 255;  // of the wave's rows
 #pragma unroll
-  for (int i = 0; i < NQ; ++i) limit = min(limit, kF32 ? 255 : __builtin_amdgcn_readfirstlane((int)(q_scale[i] >> 24)));
+  for (int i = 0; i < NQ; ++i)
+    if constexpr (!kF32) limit = min(limit, __builtin_amdgcn_readfirstlane((int)(q_scale[i] >> 24)));
   wait_loads();
   f32x4 s[NQ][2];
   Chunk p[NQ][kVC];
@@ -501,7 +515,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const float mx = fmaxf(fmaxf(fmaxf(s[i][0][0], s[i][0][1]), fmaxf(s[i][0][2], s[i][0][3])),
-                             fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3]))) * a.scale_log2;
+                             fmaxf(fmaxf(s[i][1][0], s[i][1][1]), fmaxf(s[i][1][2], s[i][1][3]))) *
+                       a.scale_log2;
       float mn = fmaxf(m[i], mx);
       mn = fmaxf(mn, __shfl_xor(mn, 16, 64));
       mn = fmaxf(mn, __shfl_xor(mn, 32, 64));
@@ -514,14 +529,15 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     }
     far = __ballot(far) != 0;
   };
-  // bf16: a step's scores from bf16 operands: the keys' codes converted, the queries as they are in memory.  An operand
-  // takes 8 elements of a lane's block.
+  // bf16: a step's scores from bf16 operands: the keys' codes converted, the queries as they are in memory.
+  // An operand takes 8 elements of a lane's block.
   auto exact_scores = [&]() {
     constexpr int kOps = D == 64 ? 2 : D / 32;
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int row = row0 + wrow + 16 * i + n, token = row < rows ? row / G : 0;
-      const E* from = q + ((int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row < rows ? row - token * G : 0)) * D;
+      const int64_t at = (int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row < rows ? row - token * G : 0);
+      const E* from = q + at * D;
 #pragma unroll
       for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -535,7 +551,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
           const float f = byte == 255u ? NAN : scale_of(byte);
           const uint32_t w = D == 64 ? (quad < 2 ? k[u].w[c & 1] : k[u].w[2 + (c & 1)]) : k[u].w[c];
           const u32x4 y = {pair_bf16<0>(w, f), pair_bf16<1>(w, f), pair_bf16<2>(w, f), pair_bf16<3>(w, f)};
-          if constexpr (!kF32) s[i][u] = Op::score(__builtin_bit_cast(Chunk, y), __builtin_bit_cast(Chunk, x), s[i][u]);
+          if constexpr (!kF32)
+            s[i][u] = Op::score(__builtin_bit_cast(Chunk, y), __builtin_bit_cast(Chunk, x), s[i][u]);
         }
       }
     }
@@ -567,17 +584,20 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
         for (int c = 0; c < kQueryOps<D>; ++c) {
           const int b = D == 256 ? c / 2 : 0;
-          const u32x4 x = mine[(i * Query::kPieces + 2 * c) * 64], y = mine[(i * Query::kPieces + 2 * c + 1) * 64];
-          const i32x8 qo = {(int)x[0], (int)x[1], (int)x[2], (int)x[3], (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
+          const u32x4 x = mine[(i * Query::kPieces + 2 * c) * 64];
+          const u32x4 y = mine[(i * Query::kPieces + 2 * c + 1) * 64];
+          const i32x8 qo = {(int)x[0], (int)x[1], (int)x[2], (int)x[3],
+                            (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const uint32_t* w = k[u].w + 4 * b;
             const i32x8 ko = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
             const int ks = (int)(k[u].scale[b] >> (8 * (n & 3)));  // its low byte counts
+            const int qs = (int)q_scale[i];
             if (D != 64 && (c & 1))
-              s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 1, (int)q_scale[i]);
+              s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 1, qs);
             else
-              s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 0, (int)q_scale[i]);
+              s[i][u] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(ko, qo, s[i][u], 4, 0, 0, ks, 0, qs);
           }
         }
     }
@@ -748,8 +768,8 @@ __device__ __forceinline__ int charge_of(const AttendArgs& a) {
 }
 
 __device__ __forceinline__ SlotWork near_work(const AttendArgs& a, const Plan4& plan, int s, int rows) {
-  return plan_slot(__builtin_amdgcn_readfirstlane(plan.near[s][0]), __builtin_amdgcn_readfirstlane(plan.near[s][1]),
-                   __builtin_amdgcn_readfirstlane(plan.near[s][2]), (int64_t)a.c.max_pages << a.c.page_shift, a.group,
+  const auto uniform = [&](int i) { return __builtin_amdgcn_readfirstlane(plan.near[s][i]); };
+  return plan_slot(uniform(0), uniform(1), uniform(2), (int64_t)a.c.max_pages << a.c.page_shift, a.group,
                    rows, a.c.kv_heads, charge_of(a));
 }
 
@@ -836,7 +856,8 @@ __device__ __forceinline__ void make_plan4(const AttendArgs& a, int rows, Plan4&
   __syncthreads();
 }
 
-// The group of piece x of the batch: its slot is the run of slots that x lies in.  j, n: which piece of how many.
+// The group of piece x of the batch: its slot is the run of slots that x lies in.  j, n: which piece of how
+// many.
 __device__ __forceinline__ void find_piece(const AttendArgs& a, int rows, const Plan4& plan, int x,
                                            Group& g, int& j, int& n) {
   const int s = plan_run(plan.before, kPlanThreads, x);
@@ -929,7 +950,8 @@ __global__ __launch_bounds__(1024) void k_attend4_join(AttendArgs a, int rows_pe
   if (k >= a.cuts[0].first) return;
   const AttendCut cut = a.cuts[1 + k];
   if (cut.rows == 0) return;
-  const int c = (int)threadIdx.x % kCols, at = (int)threadIdx.x / kCols % kAtOnce, j = (int)threadIdx.x / (kCols * kAtOnce);
+  const int c = (int)threadIdx.x % kCols, at = (int)threadIdx.x / kCols % kAtOnce;
+  const int j = (int)threadIdx.x / (kCols * kAtOnce);
   for (int r0 = 0; r0 < cut.rows; r0 += kAtOnce) {
     const int r = r0 + at;
     const bool live = r < cut.rows;

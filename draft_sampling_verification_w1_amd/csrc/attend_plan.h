@@ -83,12 +83,14 @@ struct PlanPlace {
   int64_t next;  // the next pair's first unit
 };
 
-// narrow: a division in 32 bits where it can be; one in 64 takes a hundred instructions more.  For groups of few
-// steps (4 bits); the branch around it makes the longest tiles' loop over whole elements 11 % longer
+// narrow: a division in 32 bits where it can be; one in 64 takes a hundred instructions more.  For groups
+// of few steps (4 bits); the branch around it makes the longest tiles' loop over whole elements 11 % longer
 // (two chunks of 2,048: 505.5 us, 502.5 without).
-PLAN_FN PlanPlace plan_place(const SlotWork& w, int group, int rows, int64_t left, int extra = 0, bool narrow = false) {
+PLAN_FN PlanPlace plan_place(const SlotWork& w, int group, int rows, int64_t left, int extra = 0,
+                             bool narrow = false) {
   PlanPlace g;
-  const int64_t pair = narrow && left <= INT32_MAX ? (int64_t)((int32_t)left / w.pair_units) : left / w.pair_units;
+  const bool fits = narrow && left <= INT32_MAX;
+  const int64_t pair = fits ? (int64_t)((int32_t)left / w.pair_units) : left / w.pair_units;
   const int off = (int)(left - pair * w.pair_units);
   g.head = (int)(pair / w.pairs);
   const int i = (int)(pair - (int64_t)g.head * w.pairs), j = w.tiles - 1 - i;
@@ -112,33 +114,37 @@ PLAN_FN int64_t plan_span(int64_t total, int grid) {
   return span > kMinSpan ? span : kMinSpan;
 }
 
-// Where a batch has few groups, of one row tile each, a group is cut by itself, into pieces of
-// about `target` units, so that no workgroup pays what a group costs beside its steps
-// twice.  A group of n units takes as long as its longest piece, then as long as the join of its pieces:
-// pieces are no shorter than the square root of n, the next power of two (a token over 30,000 of 32 heads
-// on 8: 24.7 -> 20.3 us, of 8 heads on one: 37 -> 21, 9 tokens over 4,000: 30 -> 20).
-// The target is the least of kTargets, from a little above a workgroup's share of an even line on, by which the
-// pieces are no more than workgroups; by the last one they always are (a piece that is not full for every group).
-// (By the last alone: 32 slots of 1 to 17 tokens 44.0 us instead of 42.3, a token over 130,000 43.5 instead of 40.5.)
+// Where a batch has few groups, of one row tile each, a group is cut by itself, into pieces of about
+// `target` units, so that no workgroup pays what a group costs beside its steps twice.  A group of n units
+// takes as long as its longest piece, then as long as the join of its pieces: pieces are no shorter than the
+// square root of n, the next power of two (a token over 30,000 of 32 heads on 8: 24.7 -> 20.3 us, of 8 heads
+// on one: 37 -> 21, 9 tokens over 4,000: 30 -> 20).
+// The target is the least of kTargets, from a little above a workgroup's share of an even line on, by which
+// the pieces are no more than workgroups; by the last one they always are (a piece that is not full for
+// every group).  (By the last alone: 32 slots of 1 to 17 tokens 44.0 us instead of 42.3, a token over
+// 130,000 43.5 instead of 40.5.)
 // total, groups: of the batch, groups > 0 (2 groups at most grid).
 constexpr int kTargets = 4;
-// Both sides of the boundary (cut by themselves, on a line with the charge below; 32 query heads on 8 of 128, 512
-// workgroups): 24 slots of 1 to 17 tokens over 2,100 35.5 and 41 us, 32 slots 40 and 45, 40 slots 44.6 and 46.5, 48 slots
-// 55 and 52; one token over 8,000 of 32 slots 48 and 48, 33 slots 51 and 46, 60 slots 81 and 72.
+// Both sides of the boundary (cut by themselves, on a line with the charge below; 32 query heads on 8 of 128,
+// 512 workgroups): 24 slots of 1 to 17 tokens over 2,100 35.5 and 41 us, 32 slots 40 and 45, 40 slots 44.6
+// and 46.5, 48 slots 55 and 52; one token over 8,000 of 32 slots 48 and 48, 33 slots 51 and 46, 60 slots 81
+// and 72.
 PLAN_FN bool plan_few(int64_t groups, int grid) { return 2 * groups <= grid; }
-// What a group costs beside its steps, in steps, where spans hold several groups (`extra` above).  256 slots of 17
-// tokens by the charge: 0 321 us, 8 306, 14 299, 20 298, 30 300.  Without and with it, from the boundary on: 33 slots of 1 to
-// 17 tokens over 2,100 48 and 43 us, 60 slots 67 and 57; one token over 8,000 of 33 slots 49 and 46; a token over
-// 30,000 of a single one of 33 or 128 slots 26 and 22; 96 slots of 17 tokens over 4,096, 24 heads on 8 of 64, 86 and 74; 128 slots of
-// 9 tokens over 2,000, 16 heads on 2 of 256, 99.6 and 98.5; 64 slots of 5 tokens over 1,000, fp32, 57 and 55.  Few groups of
-// several row tiles have none: two prompts 458 without and 440 with it, 512 tokens over 8,192 118 and 123,
-// two chunks of 200 over 1,000 in fp32 52 and 65.
+// What a group costs beside its steps, in steps, where spans hold several groups (`extra` above).  256 slots
+// of 17 tokens by the charge: 0 321 us, 8 306, 14 299, 20 298, 30 300.  Without and with it, from the
+// boundary on: 33 slots of 1 to 17 tokens over 2,100 48 and 43 us, 60 slots 67 and 57; one token over 8,000
+// of 33 slots 49 and 46; a token over 30,000 of a single one of 33 or 128 slots 26 and 22; 96 slots of 17
+// tokens over 4,096, 24 heads on 8 of 64, 86 and 74; 128 slots of 9 tokens over 2,000, 16 heads on 2 of 256,
+// 99.6 and 98.5; 64 slots of 5 tokens over 1,000, fp32, 57 and 55.  Few groups of several row tiles have none:
+// two prompts 458 without and 440 with it, 512 tokens over 8,192 118 and 123, two chunks of 200 over 1,000 in
+// fp32 52 and 65.
 PLAN_FN int plan_charge(int64_t groups, int grid) { return plan_few(groups, grid) ? 0 : 20; }
 PLAN_FN int64_t plan_div(int64_t x, int y) {  // x, y >= 0
   return x >> 31 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
 }
 PLAN_FN void plan_targets(int64_t total, int groups, int grid, int (&target)[kTargets]) {
-  const int64_t even = plan_div(total + grid - 1, grid), most = plan_div(total + grid - groups - 1, grid - groups);
+  const int64_t even = plan_div(total + grid - 1, grid);
+  const int64_t most = plan_div(total + grid - groups - 1, grid - groups);
   const int64_t mean = plan_div(total, groups);
   int64_t least = kMinSpan;
   while (least * least < mean) least *= 2;
@@ -147,9 +153,11 @@ PLAN_FN void plan_targets(int64_t total, int groups, int grid, int (&target)[kTa
     target[k] = (int)(t > least ? t : least);
   }
 }
-PLAN_FN int plan_pieces(int units, int target) { return (int)(((uint32_t)units + (uint32_t)target - 1u) / (uint32_t)target); }
-// Pieces of a slot's groups by each target, in 16 bits each, so that one sum over the slots counts all of them: 768 of a
-// batch at most (a workgroup's even share each, and one that is not full for every group).
+PLAN_FN int plan_pieces(int units, int target) {
+  return (int)(((uint32_t)units + (uint32_t)target - 1u) / (uint32_t)target);
+}
+// Pieces of a slot's groups by each target, in 16 bits each, so that one sum over the slots counts all of
+// them: 768 of a batch at most (an even share for each workgroup, and one that is not full for every group).
 PLAN_FN int64_t plan_packed(int units, const int (&target)[kTargets], int kv_heads) {
   int64_t x = 0;
   for (int k = 0; k < kTargets; ++k) x |= (int64_t)(plan_pieces(units, target[k]) * kv_heads) << (16 * k);

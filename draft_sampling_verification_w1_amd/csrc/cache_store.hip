@@ -497,8 +497,10 @@ __device__ __forceinline__ void put(void* to, const P (&x)[kPairs]) {
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) all.p[i] = x[i];
 #pragma unroll
-  for (int i = 0; i < kBytes / (int)sizeof(Word); ++i) if constexpr (kBytes <= 16) __builtin_nontemporal_store(all.w[i], static_cast<Word*>(to) + i);
+  for (int i = 0; i < kBytes / (int)sizeof(Word); ++i) {
+    if constexpr (kBytes <= 16) __builtin_nontemporal_store(all.w[i], static_cast<Word*>(to) + i);
     else static_cast<Word*>(to)[i] = all.w[i];
+  }
 }
 
 // A block of values that are all NaN.
@@ -657,9 +659,9 @@ __device__ __forceinline__ void read_v(const ReadArgs& a, const Part& g, int h, 
   }
 }
 
-// A workgroup of 4 waves takes a group of 8 positions, whose place costs a round trip; two or four groups, so that
-// more tokens share it, take longer where the states don't fit in the caches (97 -> 103 -> 109 us
-// for 102,000 tokens).
+// A workgroup of 4 waves takes a group of 8 positions, whose place costs a round trip; two or four groups, so
+// that more tokens share it, take longer where the states don't fit in the caches (97 -> 103 -> 109 us for
+// 102,000 tokens).
 template <typename E, int D, bool kPacked>
 __global__ __launch_bounds__(256) void k_cache_read(ReadArgs a) {
   constexpr int kHeadsK = kPacked ? 512 / D : 1, kHeadsV = kPacked ? 4 : 1;  // that a wave takes at once
@@ -694,7 +696,8 @@ unsigned split_of(int groups, int tasks, int waves) {
 hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStream_t stream) {
   TimingScope t("cache_store", stream);
   const int per = a.c.head_dim == 64 ? 2 : 1;
-  const int tasks = (2 * ((a.c.kv_heads + per - 1) / per) + (a.heads + per - 1) / per) * (a.c.head_dim == 256 ? 2 : 1);
+  const int rounds = 2 * ((a.c.kv_heads + per - 1) / per) + (a.heads + per - 1) / per;
+  const int tasks = rounds * (a.c.head_dim == 256 ? 2 : 1);
   const int groups = a.N / kGroup + a.c.slots;
   const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(groups, tasks, kGroup));
 #define STORE(E, D, P) hipLaunchKernelGGL((k_cache_store<E, D, P>), grid, dim3(kStoreThreads), 0, stream, a)
@@ -721,7 +724,8 @@ hipError_t launch_cache_store(bool bf16, bool packed, const StoreArgs& a, hipStr
 hipError_t launch_cache_read(bool bf16, bool packed, const ReadArgs& a, hipStream_t stream) {
   TimingScope t("cache_read", stream);
   const int groups = a.N / kGroup + a.c.slots;
-  const int tasks = packed ? (a.c.kv_heads + 3) / 4 + (a.c.kv_heads * a.c.head_dim + 511) / 512 : 2 * a.c.kv_heads;
+  const int H = a.c.kv_heads;
+  const int tasks = packed ? (H + 3) / 4 + (H * a.c.head_dim + 511) / 512 : 2 * H;
   const dim3 grid((unsigned)(a.N / kGroup + 3 * a.c.slots), split_of(groups, tasks, 4));
 #define READ(E, D, P) hipLaunchKernelGGL((k_cache_read<E, D, P>), grid, dim3(256), 0, stream, a)
 #define READ_DIMS(E, P)                       \
