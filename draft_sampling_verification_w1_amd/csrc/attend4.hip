@@ -20,17 +20,16 @@
 // of 17 tokens: the matrix units are busy 38 % of the time, the vector units 59 %.
 //
 // Measured (32 heads on 8, 128 dimensions, bf16), with the join:
-//   1 token over 30,000: 20 us (attention 14, join 5), 1.6 TB/s: what a launch, the plan, the page
-//     ids and the queries take before the first step;
-//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 40 us, 1.3 TB/s;
-//   256 slots, up to 4,096 cached, 17 new tokens: 300 us, 2.6 TB/s of codes and scales, 610 TFLOP/s (whole
-//     elements: 600 us);
-//   256 slots, up to 4,096 cached, 1 new token: 140 us;
-//   2 prompts, 2,048 tokens behind up to 8,192: 455 us, 1,000 TFLOP/s (whole elements: 500 us).
-// Tried without gain: one wave per SIMD on 80 rows (492 us for the 324 of then), values converted one step late,
-// two waves to a workgroup (343), the next group's pages and queries loaded before a group's
-// join (355), values converted once into LDS for 8 waves (461 for 460), tiles of 192, 96 and 256 rows for
-// prompts (469, 462, 474).
+//   1 token over 30,000: 20 us (attention 15, join 5), 1.6 TB/s: what a launch, the plan, the page
+//     ids and the queries take before the first step (whole elements: 48 us);
+//   32 slots, up to 2,100 cached, 1 to 17 new tokens: 41 us, 1.2 TB/s (61);
+//   256 slots, up to 4,096 cached, 17 new tokens: 295 us, 2.7 TB/s, 620 TFLOP/s (572);
+//   256 slots, up to 4,096 cached, 1 new token: 142 us, 5.0 TB/s;
+//   2 prompts, 2,048 tokens behind up to 8,192: 457 us, 990 TFLOP/s (494).
+// Tried without gain: one wave per SIMD on 80 rows (492 us for the 324 of then), values converted one step
+// late, two waves to a workgroup (343), the next group's pages and queries loaded before a group's join
+// (355), values converted once into LDS for 8 waves (461 for 460), tiles of 192, 96 and 256 rows for prompts
+// (469, 462, 474).
 #include <type_traits>
 
 #include "attend_common.h"
@@ -536,8 +535,8 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int row = row0 + wrow + 16 * i + n, token = row < rows ? row / G : 0;
-      const int64_t at = (int64_t)(it.w.o0 + token) * a.heads + it.head * G + (row < rows ? row - token * G : 0);
-      const E* from = q + at * D;
+      const int h = it.head * G + (row < rows ? row - token * G : 0);
+      const E* from = q + ((int64_t)(it.w.o0 + token) * a.heads + h) * D;
 #pragma unroll
       for (int u = 0; u < 2; ++u) s[i][u] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll

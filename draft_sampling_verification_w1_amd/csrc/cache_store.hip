@@ -7,11 +7,11 @@
 // The angle is a binary64 product (p f_j loses everything in binary32 from some 10^5
 // positions on); it is reduced by the nearest multiple of pi / 2 (two parts of pi / 2, one
 // fma each, exact to 2^-53 or so) and the sine and cosine are their Taylor series on
-// [-pi/4, pi/4] (to r^15 and r^16: off by less than 2^-52), rounded to binary32 once.  A workgroup works them out
-// for its 8 tokens and all heads use them from LDS: there is no table that ends at some
+// [-pi/4, pi/4] (to r^15 and r^16: off by less than 2^-52), rounded to binary32 once.  A workgroup works
+// them out for its 8 tokens and all heads use them from LDS: there is no table that ends at some
 // longest position and none to read.  The pair's products and sums are rounded one by one
-// in binary32 (no fma), so that the 4-bit codes follow from the plain definition bit for bit (but for a sine or
-// cosine within 2^-52 of the middle between two binary32 numbers, one in some 10^8).
+// in binary32 (no fma), so that the 4-bit codes follow from the plain definition bit for bit (but for a
+// sine or cosine within 2^-52 of the middle between two binary32 numbers, one in some 10^8).
 //
 // 4 bits.  32 elements of a token share a power of two 2^e, an element is one of +-{0, 0.5, 1,
 // 1.5, 2, 3, 4, 6} 2^e (E2M1 with E8M0 scales, the types of gfx950's conversions and matrix
@@ -37,7 +37,9 @@
 // head's pieces are on their way while one is turned.
 //
 // Bound by memory.  Alone on the card: 256 chunks of 17 tokens, 32 heads on 8 of 128 dimensions in bf16,
-// 107 MB: 23 us, 4.6 TB/s (33 from memory that no cache holds); two chunks of 2048 tokens into 4 bits 17 us, where 88 MB move.
+// 107 MB: 23 us, 4.6 TB/s, on the same inputs again; 28 us where three calls' inputs take turns, 33 where
+// six do, of which no cache holds any.  Two chunks of 2048 tokens into 4 bits 17 us, where 88 MB move; the same from
+// binary32 42 us (171 MB).
 // Small calls are latency: 7 us from one launch to the next, as a launch of two dependent loads takes.
 #include "device_common.h"
 #include "kernels.h"

@@ -26,8 +26,8 @@ SYMBOLS = ("dspark_w2_packed_bytes", "dspark_pack_w2", "dspark_workspace_bytes",
            "dspark_cache_init", "dspark_cache_fork", "dspark_cache_reserve", "dspark_cache_commit",
            "dspark_cache_free", "dspark_cache_compact_workspace_bytes", "dspark_cache_compact",
            "dspark_cache_copy_pages", "dspark_cache_append", "dspark_cache_store", "dspark_cache_read",
-           "dspark_attend_workspace_bytes", "dspark_attend", "dspark_attend4", "dspark_check_inputs", "dspark_last_error", "dspark_timing_enable",
-           "dspark_timing_report")
+           "dspark_attend_workspace_bytes", "dspark_attend", "dspark_attend4", "dspark_check_inputs",
+           "dspark_last_error", "dspark_timing_enable", "dspark_timing_report")
 
 
 class Problem(ctypes.Structure):

@@ -431,8 +431,8 @@ typedef struct {
  * keys and values converted to the cache's type.  dtype: of k, v, q and q_out; the cache's own, or
  * DSPARK_F32 or DSPARK_BF16 for a 4-bit cache.  heads: query heads, a multiple of kv_heads,
  * q [N, heads, head_dim] to q_out (which may be q, and must not overlap it otherwise, nor k or
- * v); 0: no queries (q and q_out are not read).  Queries need rot.  Rows behind offsets[slots] of q_out are left
- * as they were; queries of tokens without a page are rotated like the others.
+ * v); 0: no queries (q and q_out are not read).  Queries need rot.  Rows behind offsets[slots] of q_out
+ * are left as they were; queries of tokens without a page are rotated like the others.
  * 4 bits: rotated keys (binary32) and values are divided by the block's scale, the smallest power of two
  * within 2^-120 .. 2^125 of which the block's largest magnitude is at most 7, and rounded to the
  * nearest (ties to the even code), 6 at most.  A block with an infinity or NaN gets the scale
@@ -478,9 +478,9 @@ int dspark_attend(const dspark_cache* c, const dspark_cache_tables* t, int32_t l
 /* dspark_attend over a 4-bit cache: keys and values are what the codes stand for, exactly;
  * dtype of q and out: DSPARK_BF16 (weights rounded to bf16) or DSPARK_F32.  A bf16 query is
  * multiplied as the sum of two 8-bit parts, exact for elements within 2^13 of the row's largest; where
- * smaller ones could move a scaled score by more than 2^-11 ln 2, as bf16.  Where a block has the scale byte 255, rows that see its token are NaN (of a
- * value's block: in its 32 elements, the others may be NaN, too), the others don't depend on
- * it.  Everything else as in dspark_attend. */
+ * smaller ones could move a scaled score by more than 2^-11 ln 2, as bf16.  Where a block has the scale byte
+ * 255, rows that see its token are NaN (of a value's block: in its 32 elements, the others may be NaN, too),
+ * the others don't depend on it.  Everything else as in dspark_attend. */
 int dspark_attend4(const dspark_cache* c, const dspark_cache_tables* t, int32_t layer,
                    const void* K, const void* V, int32_t N, int32_t heads, int32_t dtype,
                    const void* q, const int32_t* offsets, float scale, int32_t max_chunk, void* out,
