@@ -603,12 +603,21 @@ __device__ __forceinline__ void attend4_steps(const AttendArgs& a, const Group& 
     matrix_done();
     if constexpr (!kF32) {
       if (limit < 255) {
-        uint32_t top = 0u;
+        uint32_t top[2] = {0u, 0u};
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int b = 0; b < (D + 127) / 128; ++b) top = max(top, k[u].scale[b] >> (8 * (n & 3)) & 255u);
-        if (__builtin_expect(__ballot((int)top > limit) != 0, 0)) exact_scores();
+          for (int b = 0; b < (D + 127) / 128; ++b) top[u] = max(top[u], k[u].scale[b] >> (8 * (n & 3)) & 255u);
+        if (__builtin_expect(__ballot((int)max(top[0], top[1]) > limit) != 0, 0)) {
+          // what no token was written to has no say
+          bool large = false;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const int key = Op::key_of(u, n);
+            large |= (int)top[u] > limit && key < seen - t * kKeys && (key < 16 ? ma : mb) >= 0;
+          }
+          if (__ballot(large) != 0) exact_scores();
+        }
       }
     }
     pages_of(ahead, pa, pb);
